@@ -33,11 +33,9 @@
 // copies or MMAs in flight.
 #include <algorithm>
 
-#include <cuda.h>
-#include <cudaTypedefs.h>
-
 #include "prefill_internal.cuh"
 #include "sm100_async.cuh"
+#include "sm100_tensor.cuh"
 
 namespace moe {
 namespace {
@@ -103,22 +101,6 @@ struct GemmArgs {
 
 // ---------------------------------------------------------------- PTX helpers
 
-__device__ __forceinline__ void tma_load_3d(void *dst, const CUtensorMap *map, int c0, int c1, int c2, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(
-            smem_u32(dst)),
-        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
-        : "memory");
-}
-
-__device__ __forceinline__ void tma_load_2d(void *dst, const CUtensorMap *map, int c0, int c1, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-            smem_u32(dst)),
-        "l"(map), "r"(c0), "r"(c1), "r"(smem_u32(bar))
-        : "memory");
-}
-
 // A pair's tensor copies: into this CTA's shared memory, completion counted on the even
 // CTA's barrier (`mbar`, its address in the cluster window), so that barrier's phase
 // covers the copies of both CTAs.
@@ -139,20 +121,6 @@ __device__ __forceinline__ void tma_load_2d_pair(void *dst, const CUtensorMap *m
         : "memory");
 }
 
-// Shared-memory matrix descriptor of tcgen05: start address, leading / stride
-// byte offsets (16-byte units), fixed version bits 46..48 = 0b001, swizzle mode.
-__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lbo, uint32_t sbo, uint32_t swizzle) {
-    uint64_t d = 0;
-    d |= (uint64_t)((addr & 0x3FFFFu) >> 4);
-    d |= (uint64_t)((lbo >> 4) & 0x3FFFu) << 16;
-    d |= (uint64_t)((sbo >> 4) & 0x3FFFu) << 32;
-    d |= (uint64_t)1 << 46;
-    d |= (uint64_t)(swizzle & 7u) << 61;
-    return d;
-}
-constexpr uint32_t kSwizzle128B = 2;
-constexpr uint32_t kSwizzleNone = 0;
-
 // Instruction descriptor of kind::mxf8f6f4: A = E2M1 (5), B = E4M3 (0), both
 // K-major, M = m (128, or 256 for a CTA pair), N = n, E8M0 scales, scale-factor ids
 // for A and B.
@@ -171,20 +139,6 @@ __device__ __forceinline__ uint32_t idesc_mxf8f6f4(int n, int sf_id, int m = kTi
     return d;
 }
 
-__device__ __forceinline__ void tmem_alloc(uint32_t *dst_smem, uint32_t ncols) {
-    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_u32(dst_smem)),
-                 "r"(ncols)
-                 : "memory");
-    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;" ::: "memory");
-}
-
-__device__ __forceinline__ void tmem_dealloc(uint32_t taddr, uint32_t ncols) {
-    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(taddr), "r"(ncols) : "memory");
-}
-
-__device__ __forceinline__ void tc_fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void tc_fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-
 // Bulk copy global -> shared without a cache hint (16-byte aligned, size a
 // multiple of 16), completion counted in bytes on `bar`.
 __device__ __forceinline__ void bulk_g2s_l2(void *dst, const void *src, uint32_t bytes, uint64_t *bar) {
@@ -192,14 +146,6 @@ __device__ __forceinline__ void bulk_g2s_l2(void *dst, const void *src, uint32_t
                      smem_u32(dst)),
                  "l"(src), "r"(bytes), "r"(smem_u32(bar))
                  : "memory");
-}
-
-// True in one lane of the converged warp (the lowest active lane, lane 0 in the
-// roles below, so a thread's tcgen05 operations and their commits stay together).
-__device__ __forceinline__ bool elect_one() {
-    uint32_t p;
-    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
-    return p != 0;
 }
 
 // One 512-byte scale atom (32 rows x 16 bytes) into 4 TMEM columns of all four lane
@@ -247,35 +193,12 @@ __device__ __forceinline__ void tc_mma_f4(uint32_t d_tmem, uint64_t adesc, uint6
         : "memory");
 }
 
-__device__ __forceinline__ void tc_commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
-                 : "memory");
-}
-
 // ---- CTA pairs (cta_group::2).  A cluster of two CTAs on two SMs: the even CTA issues
 // MMAs of M = 256 whose A rows (128 per CTA) and B columns (N / 2 per CTA, the even CTA
 // the first half) come from both CTAs' shared memory at the same offsets; each CTA's
 // TMEM holds its own 128 accumulator rows, and the scale factors of its A rows and of
 // all N columns of B.  Scale copies, MMAs and commits are issued by the even CTA and act
 // on both; a commit arrives on the barrier at the same offset in both CTAs.
-__device__ __forceinline__ uint32_t cluster_ctarank() {
-    uint32_t r;
-    asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
-    return r;
-}
-
-// All threads of both CTAs (release / acquire at cluster scope).
-__device__ __forceinline__ void cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
-}
-
-// Address in the cluster's shared window of the object at the same offset in CTA `rank`.
-__device__ __forceinline__ uint32_t mapa_shared(const void *p, uint32_t rank) {
-    uint32_t r;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(r) : "r"(smem_u32(p)), "r"(rank));
-    return r;
-}
-
 // `count` arrivals on a barrier of the other CTA (release at cluster scope).
 __device__ __forceinline__ void mbar_arrive_cluster(uint32_t cluster_addr, uint32_t count) {
     asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0], %1;" ::"r"(cluster_addr), "r"(count)
@@ -355,22 +278,6 @@ __device__ __forceinline__ void tc_commit_pair(uint64_t *bar) {
             smem_u32(bar)),
         "h"((uint16_t)3)
         : "memory");
-}
-
-// 16 accumulator columns of this warp's 32 TMEM lanes; the wait is in the same
-// statement, so no use of the registers can be scheduled before the data is there.
-__device__ __forceinline__ void tmem_ld16(uint32_t taddr, float (&v)[16]) {
-    uint32_t r[16];
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
-        "%15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
-          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-        : "r"(taddr)
-        : "memory");
-#pragma unroll
-    for (int i = 0; i < 16; i++) v[i] = __uint_as_float(r[i]);
 }
 
 // ------------------------------------------------------------------- kernel
@@ -1213,18 +1120,6 @@ __global__ void __launch_bounds__(384, 1)
 }
 
 // ------------------------------------------------------------- tensor maps
-
-PFN_cuTensorMapEncodeTiled_v12000 g_encode = nullptr;
-
-cudaError_t get_encoder() {
-    if (g_encode) return cudaSuccess;
-    void *fn = nullptr;
-    cudaDriverEntryPointQueryResult q;
-    cudaError_t e = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
-    if (e != cudaSuccess || q != cudaDriverEntryPointSuccess || fn == nullptr) return cudaErrorNotSupported;
-    g_encode = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(fn);
-    return cudaSuccess;
-}
 
 // A: packed E2M1 weights of all experts, [E][rows][K] with the given strides,
 // unpacked by the copy to 16 elements per 16 bytes (the f8f6f4 operand format).
