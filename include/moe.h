@@ -47,11 +47,14 @@ typedef enum {
     MOE_ERR_BAD_INDEX = 5,         /* device: an expert index outside [0, E), or named too
                                       often in one multi-row decode call */
     MOE_ERR_TIMEOUT = 6,           /* device: a bounded wait gave up */
-    MOE_ERR_NONFINITE = 7          /* device: non-finite router input or logit */
+    MOE_ERR_NONFINITE = 7,         /* device: non-finite router input or logit */
+    MOE_ERR_BAD_PAGE = 8           /* device: a page outside the cache, or a length, row range
+                                      or token outside what the call was given room for */
 } moe_status;
 
 typedef void *moe_stream_t;        /* a cudaStream_t */
 typedef struct moe_pool moe_pool;  /* host-side view of a resident expert pool */
+typedef struct moe_kv moe_kv;      /* host-side view of a paged key/value cache */
 
 /* Operation codes for moe_workspace_size(). */
 enum { MOE_OP_ROUTE = 0, MOE_OP_DECODE = 1, MOE_OP_GROUPED = 2 };
@@ -61,6 +64,9 @@ enum { MOE_ACT_MXFP8 = 1, MOE_ACT_MXFP4 = 2 };
 
 /* Element types of the grouped path's partial outputs. */
 enum { MOE_PARTIAL_F32 = 0, MOE_PARTIAL_BF16 = 1 };
+
+/* Element types of the probabilities and logits of draft verification. */
+enum { MOE_PROB_F32 = 0, MOE_PROB_BF16 = 1 };
 
 /* ------------------------------------------------------------ expert pool
  * One record per expert (the pages' per-(layer, expert) MXFP4 file, 17.5 MiB at
@@ -311,6 +317,109 @@ moe_status moe_combine(const void *partial, int partial_dtype, const int32_t *in
  * MOE_ERR_INVALID_ARG for other modes. */
 moe_status moe_grouped_set_cta_pairs(int mode);
 
+/* ------------------------------------------------- paged key/value cache
+ * What stands next to the routed experts in every layer of a decode or verify step: the
+ * attention's cache, held in 8 bits, and the attention over it.
+ *
+ * A cache is a set of pages in caller-owned device memory; a page holds page_tokens
+ * consecutive tokens of one sequence for all n_layers layers.  Its record is, per layer,
+ * the E4M3 codes [2][heads][page_tokens][head_dim] (keys, then values; one byte each),
+ * then the scales [2][heads] in fp32, then padding to a multiple of 128 bytes: a key or
+ * value is code * scale of its page, side and head.  Pages of a sequence are named by its
+ * row of a page table: token t of sequence b lies in page page_table[b][t / page_tokens]
+ * at slot t % page_tokens.  Entries past a sequence's tokens are not read.
+ *
+ * heads 1..1024, head_dim 64 or 128, page_tokens 16, 32, 64 or 128, n_pages <= 2^24,
+ * n_layers <= 4096.  The mapping of pages to sequences is the caller's: dropping tokens
+ * from the end (rejected drafts) is a smaller length in the next call. */
+
+/* Bytes of one page's record; 0 when the shape is unsupported. */
+size_t moe_kv_page_bytes(int n_layers, int heads, int head_dim, int page_tokens);
+
+/* Create a view of a cache of n_pages pages over `dev_mem` (128-byte aligned, at least
+ * n_pages * moe_kv_page_bytes() bytes).  *out is freed by moe_kv_destroy(). */
+moe_status moe_kv_create(moe_kv **out, void *dev_mem, size_t bytes, int n_pages, int n_layers, int heads,
+                         int head_dim, int page_tokens);
+void moe_kv_destroy(moe_kv *kv);
+
+/* Append rows to sequences of one layer.  k, v: [rows][heads][head_dim] bf16, row r at
+ * k + r * ldk elements (ldk, ldv multiples of 8, at least heads * head_dim; 16-byte
+ * aligned).  Sequence b takes rows cu_rows[b] .. cu_rows[b+1]-1 (cu_rows [seqs+1],
+ * ascending, within 0..rows) at tokens start[b], start[b]+1, ...; start[b] tokens are in
+ * the cache already and what lies past them is replaced.  page_table [seqs][table_width].
+ * Scale of a (page, side, head): the smallest power of two 2^e, e >= -126, with
+ * amax <= 448 * 2^e over the finite new values that land in it.  A page that keeps older
+ * tokens (start[b] % page_tokens of them) keeps max(that, its old scale), and the kept
+ * codes are rounded again as code * (old scale / new scale).  Codes are rounded to nearest
+ * even; infinities saturate to +-448 and NaN stays NaN.  Two sequences must not append
+ * to the same page.  Rows that would land outside the table, or in a page outside the
+ * cache, are not written and MOE_ERR_BAD_PAGE is recorded.  ws:
+ * moe_kv_append_workspace_size() bytes (the status word). */
+size_t moe_kv_append_workspace_size(void);
+moe_status moe_kv_append(const moe_kv *kv, int layer, const uint16_t *k, size_t ldk, const uint16_t *v, size_t ldv,
+                         int rows, const int32_t *cu_rows, const int32_t *start, const int32_t *page_table,
+                         int table_width, int seqs, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* Attention of a few rows per sequence over one layer of the cache (the appended rows
+ * included).  q: [rows][heads_q][head_dim] bf16, row r at q + r * ldq elements (ldq a
+ * multiple of 8, 16-byte aligned); heads_q a multiple of heads, query heads
+ * g * (heads_q / heads) .. share key/value head g.  Sequence b has the rows cu_rows[b] ..
+ * cu_rows[b+1]-1, n of them, at most max_rows (any number: more rows take more tiles), and
+ * kv_len[b] tokens.  Row i of it stands at token kv_len[b] - n + i and sees tokens 0 up to
+ * and with that one: causal among the new rows.  Out: out (like q, ldo) =
+ * sum_t softmax_t(scale * q . k_t) v_t in bf16; lse [rows][heads_q] fp32 (or NULL) = the
+ * natural logarithm of sum_t exp(scale * q . k_t).  A row that sees no token gives out = 0
+ * and lse = -infinity.  Keys and values a row does not see do not reach it, whatever they
+ * are.  scale: positive and finite.
+ * The query is split exactly into two E4M3 parts (a row's values below 2^-16 of its
+ * largest lose their last bits) and the softmax weights into two more (8 significant bits,
+ * as bf16 has), so keys and values enter the tensor cores (kind::f8f6f4) as they lie in
+ * the cache; scores, maxima, sums and outputs are fp32.  The result does not depend on
+ * timing, and a token whose page is outside the cache or past the table is reported as
+ * MOE_ERR_BAD_PAGE (the sequence's rows are then not valid), as are more rows than
+ * max_rows.  ws: moe_kv_attention_workspace_size() bytes for the current device. */
+moe_status moe_kv_attention_workspace_size(const moe_kv *kv, int max_rows, int heads_q, size_t *bytes);
+moe_status moe_kv_attention(const moe_kv *kv, int layer, const uint16_t *q, size_t ldq, int rows, int heads_q,
+                            const int32_t *cu_rows, const int32_t *kv_len, const int32_t *page_table,
+                            int table_width, int seqs, int max_rows, float scale, uint16_t *out, size_t ldo,
+                            float *lse, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ----------------------------------------------------- draft verification
+ * The verdict after the last layer of a verify step ("可选的 Qwen 扩展": several drafted
+ * tokens checked in one forward pass).  Sequence b was fed the tokens tokens[cu_rows[b]]
+ * .. tokens[cu_rows[b+1]-1]: its last accepted token, then its drafts.  Row r of p holds
+ * the target's distribution of the token after tokens[r]; row r of q (or NULL) the
+ * distribution that the draft tokens[r+1] was drawn from (the last row of a sequence is
+ * not read).  p, q: [rows][vocab] in `dtype` (MOE_PROB_*), row r at p + r * ldp elements;
+ * 1 <= vocab <= 2^20.
+ *
+ * moe_verify_sampled keeps the target's distribution whatever the drafts were.  It is
+ * defined in whole numbers, so that it does not depend on the order of sums:
+ * P = floor(2^38 min(max(p, 0), 1)) and Q alike (NaN: 0); a uniform u in [0, 1) counts as
+ * m = floor(2^24 u) (clamped to 0 .. 2^24 - 1).  Draft d after row r is accepted if
+ * m(u_accept[r]) Q_r[d] < 2^24 P_r[d], in order, up to the first that is not.  That row r
+ * (or the last row, if all are accepted) gives the next token, drawn from the weights
+ * W = max(P_r - Q_r, 0) after a rejection, W = P_r after the last row or if all those are
+ * 0: the lowest i with W_0 + .. + W_i > floor(S m(u_sample[b]) / 2^24), S their sum.
+ * q = NULL: drafts that were looked up, not drawn (Q = 2^38 at the draft, 0 elsewhere).
+ * Out: accepted [seqs] = accepted drafts, next [seqs] = the token (-1 if S is 0 or the
+ * sequence has no rows).  A draft outside the vocabulary is not accepted (as P = 0).
+ *
+ * moe_verify_greedy: drafts are accepted while they equal the row's largest logit (ties to
+ * the lower index, NaN never the largest); next = the arg max of the first row whose draft
+ * does not, or of the last row (-1 if the row holds nothing but NaN).
+ *
+ * Rows outside 0..rows are not read; MOE_ERR_BAD_PAGE is recorded and the sequence gets
+ * accepted = 0, next = -1.  ws: moe_verify_workspace_size() bytes. */
+moe_status moe_verify_workspace_size(int seqs, int rows, size_t *bytes);
+moe_status moe_verify_sampled(const void *p, size_t ldp, const void *q, size_t ldq, int dtype, int rows, int vocab,
+                              const int32_t *tokens, const int32_t *cu_rows, int seqs, const float *u_accept,
+                              const float *u_sample, int32_t *accepted, int32_t *next, void *ws, size_t ws_bytes,
+                              moe_stream_t stream);
+moe_status moe_verify_greedy(const void *logits, size_t ld, int dtype, int rows, int vocab, const int32_t *tokens,
+                             const int32_t *cu_rows, int seqs, int32_t *accepted, int32_t *next, void *ws,
+                             size_t ws_bytes, moe_stream_t stream);
+
 /* ------------------------------------------------------------- test support
  * Failure detection without a GPU fault.  Every device wait of the library (the
  * mbarrier waits of the copy/MMA pipelines, the grid barrier of the single-token
@@ -336,7 +445,8 @@ moe_status moe_debug_set_barrier_extra(int extra);
  * kernel ("route_single", "route_logits", "route_select", "decode_fused",
  * "decode_prep", "decode_gateup", "decode_down", "sort_rank", "sort_scan",
  * "sort_scatter", "sort_small", "gather_quant", "gather_split", "gemm_gateup", "gemm_down",
- * "combine", "prescale") is bracketed by CUDA events
+ * "combine", "prescale", "kv_append", "kv_attention", "verify_sampled",
+ * "verify_greedy") is bracketed by CUDA events
  * on its stream (at most 65536 launches are recorded).  moe_trace_end()
  * synchronises the device and returns the number of recorded launches and their
  * summed device time in milliseconds.  Tracing is process-wide and not

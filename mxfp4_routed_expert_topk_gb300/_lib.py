@@ -23,10 +23,12 @@ MOE_ERR_CUDA = 4
 MOE_ERR_BAD_INDEX = 5
 MOE_ERR_TIMEOUT = 6
 MOE_ERR_NONFINITE = 7
+MOE_ERR_BAD_PAGE = 8
 
 MOE_OP_ROUTE, MOE_OP_DECODE, MOE_OP_GROUPED = 0, 1, 2
 MOE_ACT_MXFP8, MOE_ACT_MXFP4 = 1, 2
 MOE_PARTIAL_F32, MOE_PARTIAL_BF16 = 0, 1
+MOE_PROB_F32, MOE_PROB_BF16 = 0, 1
 
 EXPORTED = [
     "moe_pool_bytes", "moe_pool_record_bytes", "moe_pool_create", "moe_pool_destroy",
@@ -39,6 +41,9 @@ EXPORTED = [
     "moe_debug_set_wait_limit", "moe_debug_set_barrier_extra",
     "moe_stream_pool_create", "moe_stream_pool_destroy", "moe_stream_pool_cache", "moe_stream_pool_slots",
     "moe_stream_pool_map", "moe_stream_pool_stats", "moe_host_alloc", "moe_host_free", "moe_host_numa_node",
+    "moe_kv_page_bytes", "moe_kv_create", "moe_kv_destroy", "moe_kv_append_workspace_size", "moe_kv_append",
+    "moe_kv_attention_workspace_size", "moe_kv_attention",
+    "moe_verify_workspace_size", "moe_verify_sampled", "moe_verify_greedy",
 ]
 
 
@@ -92,6 +97,18 @@ def lib() -> ctypes.CDLL:
             "moe_host_numa_node": (_i, [_i]),
             "moe_debug_set_barrier_extra": (_i, [_i]),
             "moe_grouped_set_cta_pairs": (_i, [_i]),
+            "moe_kv_page_bytes": (_sz, [_i, _i, _i, _i]),
+            "moe_kv_create": (_i, [ctypes.POINTER(_vp), _vp, _sz, _i, _i, _i, _i, _i]),
+            "moe_kv_destroy": (None, [_vp]),
+            "moe_kv_append_workspace_size": (_sz, []),
+            "moe_kv_append": (_i, [_vp, _i, _vp, _sz, _vp, _sz, _i, _vp, _vp, _vp, _i, _i, _vp, _sz, _vp]),
+            "moe_kv_attention_workspace_size": (_i, [_vp, _i, _i, ctypes.POINTER(_sz)]),
+            "moe_kv_attention": (_i, [_vp, _i, _vp, _sz, _i, _i, _vp, _vp, _vp, _i, _i, _i, ctypes.c_float, _vp, _sz,
+                                      _vp, _vp, _sz, _vp]),
+            "moe_verify_workspace_size": (_i, [_i, _i, ctypes.POINTER(_sz)]),
+            "moe_verify_sampled": (_i, [_vp, _sz, _vp, _sz, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _sz,
+                                        _vp]),
+            "moe_verify_greedy": (_i, [_vp, _sz, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _sz, _vp]),
             "moe_trace_begin": (_i, [ctypes.c_char_p]),
             "moe_trace_end": (_i, [ctypes.POINTER(_i), ctypes.POINTER(ctypes.c_double)]),
         }
@@ -447,6 +464,207 @@ def moe_grouped_set_cta_pairs(mode: int):
     pairs of SMs (tcgen05 cta_group::2) never (0), always (1), or with MXFP8 rows only
     (2, the default)."""
     _check(lib().moe_grouped_set_cta_pairs(int(mode)), "moe_grouped_set_cta_pairs")
+
+
+# ------------------------------------------------- paged key/value cache
+
+
+def moe_kv_page_bytes(n_layers: int, heads: int, head_dim: int, page_tokens: int) -> int:
+    return int(lib().moe_kv_page_bytes(n_layers, heads, head_dim, page_tokens))
+
+
+class KvCache:
+    """A paged cache of E4M3 keys and values in a caller-owned (PyTorch) device buffer;
+    its contents are undefined until rows are appended."""
+
+    def __init__(self, n_pages: int, n_layers: int, heads: int, head_dim: int, page_tokens: int, device="cuda",
+                 buffer: torch.Tensor | None = None):
+        rec = moe_kv_page_bytes(n_layers, heads, head_dim, page_tokens)
+        if rec == 0:
+            raise MoeError(MOE_ERR_UNSUPPORTED_SHAPE, "moe_kv_page_bytes")
+        self.n_pages, self.n_layers, self.heads = n_pages, n_layers, heads
+        self.head_dim, self.page_tokens, self.page_bytes = head_dim, page_tokens, rec
+        if buffer is None:
+            buffer = torch.empty(n_pages * rec + 128, dtype=torch.uint8, device=device)
+            off = (-buffer.data_ptr()) % 128
+            buffer = buffer[off:off + n_pages * rec]
+        _need(buffer, torch.uint8, "buffer")
+        self.buffer = buffer
+        h = ctypes.c_void_p()
+        _check(lib().moe_kv_create(ctypes.byref(h), _ptr(buffer), buffer.numel(), n_pages, n_layers, heads, head_dim,
+                                   page_tokens), "moe_kv_create")
+        self.handle = h
+
+    def _layer(self, layer: int) -> torch.Tensor:
+        if not 0 <= layer < self.n_layers:
+            raise ValueError(f"layer {layer} of {self.n_layers}")
+        used = self.buffer.view(-1)[:self.n_pages * self.page_bytes]
+        return used.view(self.n_pages, self.n_layers, self.page_bytes // self.n_layers)[:, layer]
+
+    def codes(self, layer: int) -> torch.Tensor:
+        """The layer's codes as values: float8_e4m3fn [n_pages, 2, heads, page_tokens, head_dim] (a view)."""
+        n = 2 * self.heads * self.page_tokens * self.head_dim
+        c = self._layer(layer)[:, :n].unflatten(1, (2, self.heads, self.page_tokens, self.head_dim))
+        return c.view(torch.float8_e4m3fn)
+
+    def scales(self, layer: int) -> torch.Tensor:
+        """The layer's scales: float32 [n_pages, 2, heads] (a view)."""
+        n = 2 * self.heads * self.page_tokens * self.head_dim
+        return self._layer(layer)[:, n:n + 8 * self.heads].view(torch.float32).unflatten(1, (2, self.heads))
+
+    def __del__(self):
+        h = getattr(self, "handle", None)
+        if h is not None and _lib is not None:
+            _lib.moe_kv_destroy(h)
+            self.handle = None
+
+
+def _need_heads(t, heads, dim, name):
+    """Row stride (in elements) of a bf16 [rows, heads, dim] tensor whose rows are dense."""
+    if not (t.is_cuda and t.dtype == torch.bfloat16 and t.dim() == 3 and t.shape[1:] == (heads, dim)
+            and t.stride(2) == 1 and (heads == 1 or t.stride(1) == dim)):
+        raise ValueError(f"{name}: expected a CUDA bfloat16 tensor [rows, {heads}, {dim}] with dense rows")
+    return t.stride(0) if t.shape[0] > 1 else heads * dim
+
+
+def _need_index(t, n, name):
+    _need(t, torch.int32, name)
+    if t.numel() != n:
+        raise ValueError(f"{name}: expected {n} values")
+
+
+def _empty(shape, dtype, like, stream):
+    """A tensor that belongs to the stream the kernel runs on."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
+def _workspace_on(nbytes, like, stream):
+    if stream is None:
+        return workspace(nbytes, like.device)
+    with torch.cuda.stream(stream):
+        return workspace(nbytes, like.device)
+
+
+def moe_kv_append_workspace_size() -> int:
+    return int(lib().moe_kv_append_workspace_size())
+
+
+def moe_kv_append(cache: KvCache, layer: int, k: torch.Tensor, v: torch.Tensor, cu_rows: torch.Tensor,
+                  start: torch.Tensor, page_table: torch.Tensor, ws: torch.Tensor | None = None, stream=None):
+    """Append rows k, v [rows, heads, head_dim] (dense rows, any row stride) to the cache."""
+    ldk = _need_heads(k, cache.heads, cache.head_dim, "k")
+    ldv = _need_heads(v, cache.heads, cache.head_dim, "v")
+    if v.shape[0] != k.shape[0]:
+        raise ValueError("k, v: different row counts")
+    _need(page_table, torch.int32, "page_table")
+    seqs, width = page_table.shape
+    _need_index(cu_rows, seqs + 1, "cu_rows")
+    _need_index(start, seqs, "start")
+    if ws is None:
+        ws = _workspace_on(moe_kv_append_workspace_size(), k, stream)
+    _check(lib().moe_kv_append(cache.handle, layer, _ptr(k), ldk, _ptr(v), ldv, k.shape[0], _ptr(cu_rows), _ptr(start),
+                               _ptr(page_table), width, seqs, _ptr(ws), ws.numel(), _stream(stream)), "moe_kv_append")
+
+
+def moe_kv_attention_workspace_size(cache: KvCache, max_rows: int, heads_q: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_kv_attention_workspace_size(cache.handle, max_rows, heads_q, ctypes.byref(n)),
+           "moe_kv_attention_workspace_size")
+    return int(n.value)
+
+
+def moe_kv_attention(cache: KvCache, layer: int, q: torch.Tensor, cu_rows: torch.Tensor, kv_len: torch.Tensor,
+                     page_table: torch.Tensor, max_rows: int, scale: float | None = None,
+                     out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                     ws: torch.Tensor | None = None, stream=None):
+    """Attention of q [rows, heads_q, head_dim] over the cache; returns out (bf16, like q).
+    scale: head_dim ** -0.5 unless given; lse (float32 [rows, heads_q]) is filled if given."""
+    rows, heads_q = q.shape[:2]
+    ldq = _need_heads(q, heads_q, cache.head_dim, "q")
+    _need(page_table, torch.int32, "page_table")
+    seqs, width = page_table.shape
+    _need_index(cu_rows, seqs + 1, "cu_rows")
+    _need_index(kv_len, seqs, "kv_len")
+    if out is None:
+        out = _empty((rows, heads_q, cache.head_dim), torch.bfloat16, q, stream)
+    ldo = _need_heads(out, heads_q, cache.head_dim, "out")
+    if out.shape[0] != rows:
+        raise ValueError(f"out: expected {rows} rows")
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+        if lse.numel() != rows * heads_q:
+            raise ValueError(f"lse: expected [{rows}, {heads_q}]")
+    if ws is None:
+        ws = _workspace_on(moe_kv_attention_workspace_size(cache, max_rows, heads_q), q, stream)
+    if scale is None:
+        scale = cache.head_dim ** -0.5
+    _check(lib().moe_kv_attention(cache.handle, layer, _ptr(q), ldq, rows, heads_q, _ptr(cu_rows), _ptr(kv_len),
+                                  _ptr(page_table), width, seqs, max_rows, scale, _ptr(out), ldo, _ptr(lse), _ptr(ws),
+                                  ws.numel(), _stream(stream)), "moe_kv_attention")
+    return out
+
+
+# ----------------------------------------------------- draft verification
+
+
+def moe_verify_workspace_size(seqs: int, rows: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_verify_workspace_size(seqs, rows, ctypes.byref(n)), "moe_verify_workspace_size")
+    return int(n.value)
+
+
+def _need_probs(t, name, like=None):
+    """Row stride and dtype code of a [rows, vocab] tensor of probabilities or logits."""
+    if not (t.is_cuda and t.dim() == 2 and t.stride(1) == 1 and t.dtype in (torch.float32, torch.bfloat16)):
+        raise ValueError(f"{name}: expected a CUDA float32 or bfloat16 tensor [rows, vocab] with dense rows")
+    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
+        raise ValueError(f"{name}: expected the shape and type of p")
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1], (MOE_PROB_F32 if t.dtype == torch.float32 else MOE_PROB_BF16)
+
+
+def _verify_outputs(p, tokens, cu_rows, accepted, next_token, ws, stream):
+    rows, seqs = p.shape[0], cu_rows.numel() - 1
+    _need_index(tokens, rows, "tokens")
+    _need_index(cu_rows, max(seqs, 0) + 1, "cu_rows")
+    accepted = _empty((seqs,), torch.int32, p, stream) if accepted is None else accepted
+    next_token = _empty((seqs,), torch.int32, p, stream) if next_token is None else next_token
+    _need_index(accepted, seqs, "accepted")
+    _need_index(next_token, seqs, "next_token")
+    if ws is None:
+        ws = _workspace_on(moe_verify_workspace_size(seqs, rows), p, stream)
+    return seqs, accepted, next_token, ws
+
+
+def moe_verify_sampled(p: torch.Tensor, q: torch.Tensor | None, tokens: torch.Tensor, cu_rows: torch.Tensor,
+                       u_accept: torch.Tensor, u_sample: torch.Tensor, accepted: torch.Tensor | None = None,
+                       next_token: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """(accepted, next_token), int32 [seqs]: how many drafts of each sequence hold, and the token after them."""
+    ldp, dt = _need_probs(p, "p")
+    ldq = 0 if q is None else _need_probs(q, "q", p)[0]
+    seqs, accepted, next_token, ws = _verify_outputs(p, tokens, cu_rows, accepted, next_token, ws, stream)
+    _need(u_accept, torch.float32, "u_accept")
+    _need(u_sample, torch.float32, "u_sample")
+    if u_accept.numel() != p.shape[0] or u_sample.numel() != seqs:
+        raise ValueError("u_accept, u_sample: expected one value per row and one per sequence")
+    _check(lib().moe_verify_sampled(_ptr(p), ldp, _ptr(q), ldq, dt, p.shape[0], p.shape[1], _ptr(tokens), _ptr(cu_rows),
+                                    seqs, _ptr(u_accept), _ptr(u_sample), _ptr(accepted), _ptr(next_token), _ptr(ws),
+                                    ws.numel(), _stream(stream)), "moe_verify_sampled")
+    return accepted, next_token
+
+
+def moe_verify_greedy(logits: torch.Tensor, tokens: torch.Tensor, cu_rows: torch.Tensor,
+                      accepted: torch.Tensor | None = None, next_token: torch.Tensor | None = None,
+                      ws: torch.Tensor | None = None, stream=None):
+    """(accepted, next_token), int32 [seqs]: drafts that equal the arg max, and the arg max after them."""
+    ld, dt = _need_probs(logits, "logits")
+    seqs, accepted, next_token, ws = _verify_outputs(logits, tokens, cu_rows, accepted, next_token, ws, stream)
+    _check(lib().moe_verify_greedy(_ptr(logits), ld, dt, logits.shape[0], logits.shape[1], _ptr(tokens), _ptr(cu_rows),
+                                   seqs, _ptr(accepted), _ptr(next_token), _ptr(ws), ws.numel(), _stream(stream)),
+           "moe_verify_greedy")
+    return accepted, next_token
 
 
 # ---------------------------------------------------------- test support

@@ -3,6 +3,7 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include "kv_internal.cuh"
 #include "moe_internal.cuh"
 
 using namespace moe;
@@ -53,6 +54,31 @@ struct Trace {
 } g_trace;
 
 bool aligned(const void *p, size_t a) { return ((uintptr_t)p % a) == 0; }
+
+// ------------------------------------------------------ key/value cache
+bool kv_shape_ok(int n_layers, int heads, int head_dim, int page_tokens) {
+    return n_layers >= 1 && n_layers <= 4096 && heads >= 1 && heads <= 1024 && (head_dim == 64 || head_dim == 128) &&
+           (page_tokens == 16 || page_tokens == 32 || page_tokens == 64 || page_tokens == 128);
+}
+
+KvView make_kv_view(uint8_t *base, int n_pages, int n_layers, int heads, int head_dim, int page_tokens) {
+    KvView v;
+    v.base = base;
+    v.n_pages = n_pages;
+    v.n_layers = n_layers;
+    v.heads = heads;
+    v.dim = head_dim;
+    v.page = page_tokens;
+    v.off_scale = (uint64_t)2 * heads * page_tokens * head_dim;
+    v.layer_rec = align_up(v.off_scale + (uint64_t)2 * heads * sizeof(float), 128);
+    v.page_rec = (uint64_t)n_layers * v.layer_rec;
+    return v;
+}
+
+// A [rows][heads][head_dim] bf16 argument with `ld` elements between rows.
+bool rows_ok(const void *p, size_t ld, int heads, int dim) {
+    return p != nullptr && aligned(p, 16) && ld % 8 == 0 && ld >= (size_t)heads * dim;
+}
 
 }  // namespace
 
@@ -201,6 +227,7 @@ const char *moe_status_string(moe_status s) {
         case MOE_ERR_BAD_INDEX: return "expert index out of range";
         case MOE_ERR_TIMEOUT: return "bounded device wait expired";
         case MOE_ERR_NONFINITE: return "non-finite router input";
+        case MOE_ERR_BAD_PAGE: return "page, length, row range or token out of range";
         default: return "unknown status";
     }
 }
@@ -280,6 +307,123 @@ moe_status moe_grouped_read_h(const moe_pool *pool, int T, int k, int act_mode, 
     if (!aligned(ws, 256) || !aligned(hq, 16)) return MOE_ERR_INVALID_ARG;
     if (ws_bytes < grouped_workspace_bytes(pool->v.E, pool->v.H, pool->v.I, T, k)) return MOE_ERR_WORKSPACE;
     return cuda_status(launch_read_h(pool->v, T, k, act_mode, offsets, ws, hq, hs, (cudaStream_t)stream));
+}
+
+size_t moe_kv_page_bytes(int n_layers, int heads, int head_dim, int page_tokens) {
+    if (!kv_shape_ok(n_layers, heads, head_dim, page_tokens)) return 0;
+    return (size_t)make_kv_view(nullptr, 1, n_layers, heads, head_dim, page_tokens).page_rec;
+}
+
+moe_status moe_kv_create(moe_kv **out, void *dev_mem, size_t bytes, int n_pages, int n_layers, int heads, int head_dim,
+                         int page_tokens) {
+    if (out == nullptr || dev_mem == nullptr) return MOE_ERR_INVALID_ARG;
+    *out = nullptr;
+    if (!kv_shape_ok(n_layers, heads, head_dim, page_tokens)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (n_pages < 1 || !aligned(dev_mem, 128)) return MOE_ERR_INVALID_ARG;
+    if (n_pages > (1 << 24)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    const KvView v = make_kv_view((uint8_t *)dev_mem, n_pages, n_layers, heads, head_dim, page_tokens);
+    if (bytes / v.page_rec < (size_t)n_pages) return MOE_ERR_INVALID_ARG;
+    moe_kv *kv = (moe_kv *)malloc(sizeof(moe_kv));
+    if (kv == nullptr) return MOE_ERR_INVALID_ARG;
+    kv->v = v;
+    *out = kv;
+    return MOE_OK;
+}
+
+void moe_kv_destroy(moe_kv *kv) { free(kv); }
+
+size_t moe_kv_append_workspace_size(void) { return sizeof(StatusWord); }
+
+moe_status moe_kv_append(const moe_kv *kv, int layer, const uint16_t *k, size_t ldk, const uint16_t *v, size_t ldv,
+                         int rows, const int32_t *cu_rows, const int32_t *start, const int32_t *page_table,
+                         int table_width, int seqs, void *ws, size_t ws_bytes, moe_stream_t stream) {
+    if (kv == nullptr || ws == nullptr) return MOE_ERR_INVALID_ARG;
+    if (layer < 0 || layer >= kv->v.n_layers || rows < 0 || seqs < 0 || table_width < 0) return MOE_ERR_INVALID_ARG;
+    if (rows == 0 || seqs == 0 || table_width == 0) return MOE_OK;  // nothing to write (arrays may be null)
+    if (cu_rows == nullptr || start == nullptr || page_table == nullptr) return MOE_ERR_INVALID_ARG;
+    if (!rows_ok(k, ldk, kv->v.heads, kv->v.dim) || !rows_ok(v, ldv, kv->v.heads, kv->v.dim) || !aligned(ws, 256))
+        return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < sizeof(StatusWord)) return MOE_ERR_WORKSPACE;
+    KvAppendArgs a = {kv->v, layer, k, v, ldk, ldv, rows, cu_rows, start, page_table, table_width, seqs,
+                      (StatusWord *)ws};
+    return cuda_status(launch_kv_append(a, (cudaStream_t)stream));
+}
+
+moe_status moe_kv_attention_workspace_size(const moe_kv *kv, int max_rows, int heads_q, size_t *bytes) {
+    if (kv == nullptr || bytes == nullptr) return MOE_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (max_rows < 0 || heads_q < 1 || heads_q % kv->v.heads != 0) return MOE_ERR_INVALID_ARG;
+    if (heads_q > 32768 || max_rows > (1 << 20)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    return cuda_status(kv_attention_workspace_bytes(kv->v, max_rows, heads_q, bytes));
+}
+
+moe_status moe_kv_attention(const moe_kv *kv, int layer, const uint16_t *q, size_t ldq, int rows, int heads_q,
+                            const int32_t *cu_rows, const int32_t *kv_len, const int32_t *page_table, int table_width,
+                            int seqs, int max_rows, float scale, uint16_t *out, size_t ldo, float *lse, void *ws,
+                            size_t ws_bytes, moe_stream_t stream) {
+    if (kv == nullptr || ws == nullptr) return MOE_ERR_INVALID_ARG;
+    if (layer < 0 || layer >= kv->v.n_layers || rows < 0 || seqs < 0 || table_width < 0) return MOE_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !(scale <= 3.4028235e38f)) return MOE_ERR_INVALID_ARG;
+    size_t need = 0;
+    const moe_status s = moe_kv_attention_workspace_size(kv, max_rows, heads_q, &need);
+    if (s != MOE_OK) return s;
+    if (rows == 0 || seqs == 0) return MOE_OK;  // nothing to write (arrays may be null)
+    if (cu_rows == nullptr || kv_len == nullptr || (page_table == nullptr && table_width > 0)) return MOE_ERR_INVALID_ARG;
+    if (!rows_ok(q, ldq, heads_q, kv->v.dim) || !rows_ok(out, ldo, heads_q, kv->v.dim) || !aligned(ws, 256))
+        return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+    KvAttentionArgs a = {kv->v,      layer, q,        ldq,   rows, heads_q, cu_rows, kv_len,          page_table,
+                         table_width, seqs,  max_rows, scale, out,  ldo,     lse,     (StatusWord *)ws};
+    return cuda_status(launch_kv_attention(a, ws, (cudaStream_t)stream));
+}
+
+moe_status moe_verify_workspace_size(int seqs, int rows, size_t *bytes) {
+    if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (seqs < 0 || rows < 0) return MOE_ERR_INVALID_ARG;
+    *bytes = verify_workspace_bytes(seqs, rows);
+    return MOE_OK;
+}
+
+namespace {
+
+// What both kinds of verification check.
+moe_status verify_check(const VerifyArgs &a, int dtype, const void *ws, size_t ws_bytes) {
+    if (ws == nullptr || (a.seqs > 0 && (a.cu_rows == nullptr || a.accepted == nullptr || a.next == nullptr)))
+        return MOE_ERR_INVALID_ARG;
+    if (a.seqs > 0 && a.rows > 0 && (a.p == nullptr || a.tokens == nullptr)) return MOE_ERR_INVALID_ARG;
+    if (dtype != MOE_PROB_F32 && dtype != MOE_PROB_BF16) return MOE_ERR_INVALID_ARG;
+    if (a.rows < 0 || a.seqs < 0 || a.vocab < 1 || a.ldp < (size_t)a.vocab) return MOE_ERR_INVALID_ARG;
+    if (a.vocab > (1 << 20)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    const size_t size = a.bf16 ? 2 : 4;
+    if (!aligned(ws, 256) || !aligned(a.p, size) || (a.q != nullptr && !aligned(a.q, size))) return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < verify_workspace_bytes(a.seqs, a.rows)) return MOE_ERR_WORKSPACE;
+    return MOE_OK;
+}
+
+}  // namespace
+
+moe_status moe_verify_sampled(const void *p, size_t ldp, const void *q, size_t ldq, int dtype, int rows, int vocab,
+                              const int32_t *tokens, const int32_t *cu_rows, int seqs, const float *u_accept,
+                              const float *u_sample, int32_t *accepted, int32_t *next, void *ws, size_t ws_bytes,
+                              moe_stream_t stream) {
+    if (seqs > 0 && rows > 0 && (u_accept == nullptr || u_sample == nullptr)) return MOE_ERR_INVALID_ARG;
+    VerifyArgs a = {p,       q,    ldp,      ldq,      dtype == MOE_PROB_BF16, rows, vocab, tokens,
+                    cu_rows, seqs, u_accept, u_sample, accepted,               next, (StatusWord *)ws};
+    const moe_status s = verify_check(a, dtype, ws, ws_bytes);
+    if (s != MOE_OK) return s;
+    if (q != nullptr && ldq < (size_t)vocab) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_verify_sampled(a, ws, (cudaStream_t)stream));
+}
+
+moe_status moe_verify_greedy(const void *logits, size_t ld, int dtype, int rows, int vocab, const int32_t *tokens,
+                             const int32_t *cu_rows, int seqs, int32_t *accepted, int32_t *next, void *ws,
+                             size_t ws_bytes, moe_stream_t stream) {
+    VerifyArgs a = {logits,  nullptr, ld,      0,       dtype == MOE_PROB_BF16, rows, vocab, tokens,
+                    cu_rows, seqs,    nullptr, nullptr, accepted,               next, (StatusWord *)ws};
+    const moe_status s = verify_check(a, dtype, ws, ws_bytes);
+    if (s != MOE_OK) return s;
+    return cuda_status(launch_verify_greedy(a, ws, (cudaStream_t)stream));
 }
 
 moe_status moe_debug_set_wait_limit(uint64_t ns) {
