@@ -364,8 +364,8 @@ moe_status moe_kv_append(const moe_kv *kv, int layer, const uint16_t *k, size_t 
  * included).  q: [rows][heads_q][head_dim] bf16, row r at q + r * ldq elements (ldq a
  * multiple of 8, 16-byte aligned); heads_q a multiple of heads, query heads
  * g * (heads_q / heads) .. share key/value head g.  Sequence b has the rows cu_rows[b] ..
- * cu_rows[b+1]-1, n of them, at most max_rows (any number: more rows take more tiles), and
- * kv_len[b] tokens.  Row i of it stands at token kv_len[b] - n + i and sees tokens 0 up to
+ * cu_rows[b+1]-1, n of them, at most max_rows (more rows take more tiles; max_rows * heads_q /
+ * heads <= 2^24), and kv_len[b] tokens (at most 2^30).  Row i of it stands at token kv_len[b] - n + i and sees tokens 0 up to
  * and with that one: causal among the new rows.  Out: out (like q, ldo) =
  * sum_t softmax_t(scale * q . k_t) v_t in bf16; lse [rows][heads_q] fp32 (or NULL) = the
  * natural logarithm of sum_t exp(scale * q . k_t).  A row that sees no token gives out = 0

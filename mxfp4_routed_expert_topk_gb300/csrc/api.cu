@@ -353,7 +353,8 @@ moe_status moe_kv_attention_workspace_size(const moe_kv *kv, int max_rows, int h
     if (kv == nullptr || bytes == nullptr) return MOE_ERR_INVALID_ARG;
     *bytes = 0;
     if (max_rows < 0 || heads_q < 1 || heads_q % kv->v.heads != 0) return MOE_ERR_INVALID_ARG;
-    if (heads_q > 32768 || max_rows > (1 << 20)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if (heads_q > 32768 || max_rows > (1 << 20) || (int64_t)max_rows * (heads_q / kv->v.heads) > (1 << 24))
+        return MOE_ERR_UNSUPPORTED_SHAPE;
     return cuda_status(kv_attention_workspace_bytes(kv->v, max_rows, heads_q, bytes));
 }
 
@@ -430,6 +431,7 @@ moe_status moe_debug_set_wait_limit(uint64_t ns) {
     const uint64_t lim = ns == 0 ? 1000ull * 1000ull * 1000ull : ns;
     if (set_wait_limit_decode_fused(lim) != cudaSuccess) return MOE_ERR_CUDA;
     if (set_wait_limit_gemm(lim) != cudaSuccess) return MOE_ERR_CUDA;
+    if (set_wait_limit_kv_attention(lim) != cudaSuccess) return MOE_ERR_CUDA;
     return MOE_OK;
 }
 

@@ -82,6 +82,7 @@ struct KvAttentionArgs {
 };
 cudaError_t kv_attention_workspace_bytes(const KvView &kv, int max_rows, int heads_q, size_t *bytes);
 cudaError_t launch_kv_attention(const KvAttentionArgs &a, void *ws, cudaStream_t st);
+cudaError_t set_wait_limit_kv_attention(uint64_t ns);
 
 struct VerifyArgs {
     const void *p, *q;  // (greedy: p = the logits)

@@ -360,7 +360,7 @@ def test_attention_page_offsets_beyond_32_bits():
 def test_attention_reports_bad_pages_and_lengths():
     c = Case([2, 2], [100, 100], 2, 7, 128, 32)
     good, _ = c.run()
-    ws = moe.workspace(moe.moe_kv_attention_workspace_size(c.cache, 2, 14))
+    ws = moe.workspace(moe.moe_kv_attention_workspace_size(c.cache, 4, 14))
 
     def call(table=None, lens=None, cu=None, max_rows=2):
         out = torch.full_like(c.q, 9.0)
