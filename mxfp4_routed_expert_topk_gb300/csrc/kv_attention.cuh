@@ -1,0 +1,788 @@
+// What the two forms of the cache attention share: the division of work, the copy and
+// query-loading roles, and the joining of results that several CTAs hold parts of.
+//
+//   s[t][r] = ks_t * (k_t . q_r),  m_r = max_t s,  o_r = sum_t 2^(s - m) vs_t v_t / sum_t 2^(s - m)
+//
+// (log2 units: scale * log2(e) is folded into the scores).  Few rows, many tokens: the cache
+// is read once, and everything else must hide behind that read.
+//
+//   - Codes go from HBM to shared memory to the tensor cores (kind::f8f6f4) as they lie in
+//     the cache, with no conversion.  What multiplies them must be E4M3 too: a bf16 query is
+//     exactly the sum of two E4M3 parts (4 + 4 significant bits) after a power of two per
+//     row, and a weight is written as two parts as well (8 bits, as bf16 has).  Each product
+//     runs twice into the same accumulator; the tensor pipe has room for it.
+//   - Weights are taken relative to their 128-token tile's own maximum, and each tile's output
+//     is a fresh accumulator joined with the running one in registers: what E4M3's range
+//     cannot hold is then below 2^-17 of the tile's largest term, however far another token
+//     stands above the tile.  The pages' value scales, relative to the tile's largest,
+//     multiply the weights before they are split.
+//   - Work: the (sequence, row tile, head, 128-token tile) units of the call in one line, cut
+//     into equal shares, one per SM.  A share may begin and end inside a sequence: such
+//     partial results go to the workspace and, after a grid barrier (cooperative launch), the
+//     CTAs that worked on the sequence join it, each some rows.  Shares are cut by the lengths
+//     on the device, so a captured graph serves any lengths.
+//
+// Roles of a CTA: warp 0 copies keys, warp 2 values and scales; warp 1 issues MMAs; warp 3
+// loads the next segment's queries; the rest are softmax warpgroups.
+#pragma once
+
+#include "kv_internal.cuh"
+#include "sm100_tensor.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kTokens = 128;             // tokens per tile
+constexpr int kMaxStages = 8;            // per ring
+constexpr int kMaxSlots = kTokens / 16;  // pages per tile
+constexpr int kMaxLen = 1 << 30;         // tokens of a sequence
+constexpr uint32_t kSwizzle64B = 4;
+constexpr int kStKvArrive = 40, kStKvExit = 5;  // StatusWord::pad
+constexpr int kFirstSoft = 4;            // first softmax warp
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr float kNan = __builtin_nanf("");
+
+}  // namespace
+
+struct AttnArgs {
+    KvAttentionArgs k;
+    int group;      // query heads per key/value head
+    int rpt;        // rows per row tile
+    int nrt;        // row tiles of max_rows rows
+    int nk, nv;     // stages of the key and value rings
+    int over;       // what starting a unit costs, in tiles
+    float scale2;   // scale * log2(e)
+    float *part;    // partial results: 2 slots per CTA of [rpt][dim] + [rpt][2]
+};
+
+namespace {
+
+// A segment: consecutive tiles of one (sequence, row tile, head) in a CTA's share.
+struct Seg {
+    int b, rt, n, len, row0, head, tile0;
+    int count;             // tiles; 0: the share ends here
+    int see_all, see_max;  // tokens that every row of the tile sees, and that any row sees
+    int c0, parts;         // the CTAs that share the unit: the first, and how many (1: this one has it all)
+};
+constexpr int kSegs = 4;   // ring of segments
+
+// One row of a row tile.
+struct RowInfo {
+    int row, head;  // row of q (-1: none), query head
+    float qs;       // power of two: query = qs * (sum of its parts)
+    int pos;        // the token it stands at (-1: sees nothing)
+};
+
+// One (sequence, row tile): its rows, tokens and tiles.
+struct Item {
+    int b, rt, row0, n, len, nt;
+    bool ok;
+};
+
+__device__ __forceinline__ Item load_item(const AttnArgs &a, int it) {
+    Item x;
+    x.b = it / a.nrt;
+    x.rt = it - x.b * a.nrt;
+    int hi;
+    x.ok = seq_rows(a.k.cu_rows, x.b, a.k.rows, x.row0, hi);
+    x.n = hi - x.row0;
+    if (x.n > a.k.max_rows) {
+        x.n = a.k.max_rows;
+        x.ok = false;
+    }
+    const int64_t room = min((int64_t)a.k.table_width * a.k.kv.page, (int64_t)kMaxLen);
+    const int len = max(a.k.kv_len[x.b], 0);
+    if ((int64_t)len > room) x.ok = false;
+    x.len = (int)min((int64_t)len, room);
+    x.nt = 0;
+    if (x.rt * a.rpt < x.n * a.group) {
+        const int last = min(x.n - 1, ((x.rt + 1) * a.rpt - 1) / a.group);  // last row of the tile
+        const int see = min(x.len, max(0, x.len - x.n + last + 1));
+        x.nt = max(1, (see + kTokens - 1) / kTokens);
+    }
+    return x;
+}
+
+// The CTA whose share of `total` positions over `ctas` CTAs holds position w.
+__device__ __forceinline__ int cta_of(int64_t w, int64_t total, int ctas) {
+    return (int)(((w + 1) * ctas - 1) / total);
+}
+
+// A CTA's share [lo, hi) and where it starts.
+struct Share {
+    int64_t total, lo, hi;
+    int ctas;
+};
+
+// The line of units: a unit is one (item, head), `over` positions that stand for its fixed
+// cost, then its tiles.  Cut it into equal shares (all threads; `mem`: 2 + NT / 32 words of
+// shared memory, the first two of which then hold the first position and number of the item
+// that lo lies in, after the caller's next barrier).
+__device__ __forceinline__ int unit_length(const AttnArgs &a, const Item &x) { return x.nt == 0 ? 0 : x.nt + a.over; }
+
+template <int NT>
+__device__ __forceinline__ Share cut_shares(const AttnArgs &a, int64_t *mem) {
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    int64_t *sums = mem + 2;
+    const int items = a.k.seqs * a.nrt;
+    const int per = (items + NT - 1) / NT;
+    const int i0 = min(tid * per, items), i1 = min(i0 + per, items);
+    // two rounds over the thread's items: their sum, then the item that holds lo
+    Share s;
+    int64_t mine = 0, pre = 0;
+#pragma unroll 1
+    for (int round = 0; round < 2; round++) {
+        int64_t at = pre;
+        bool good = true;
+#pragma unroll 1
+        for (int i = i0; i < i1; i++) {
+            const Item x = load_item(a, i);
+            good &= x.ok;
+            const int64_t u = (int64_t)unit_length(a, x) * a.k.kv.heads;
+            if (round == 1 && s.lo >= at && s.lo < at + u) {
+                mem[0] = at;
+                mem[1] = i;
+            }
+            at += u;
+        }
+        if (round == 1) break;
+        mine = at;
+        if (!good && blockIdx.x == 0) set_status(a.k.st, MOE_ERR_BAD_PAGE, 1);
+        pre = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t o = __shfl_up_sync(0xffffffffu, pre, d);
+            if (lane >= d) pre += o;
+        }
+        if (lane == 31) sums[warp] = pre;
+        __syncthreads();
+        s.total = 0;
+#pragma unroll 1
+        for (int w = 0; w < NT / 32; w++) {
+            if (w < warp) pre += sums[w];
+            s.total += sums[w];
+        }
+        pre -= mine;
+        s.ctas = (int)min((int64_t)gridDim.x, s.total);
+        s.lo = s.hi = 0;
+        const int cta = (int)blockIdx.x;
+        if (cta >= s.ctas) break;
+        s.lo = s.total * cta / s.ctas;
+        s.hi = s.total * (cta + 1) / s.ctas;
+        if (s.lo < pre || s.lo >= pre + mine) break;
+    }
+    return s;
+}
+
+// ------------------------------------------------------------ PTX
+
+// Instruction descriptor of kind::f8f6f4, E4M3 x E4M3 -> fp32; tm, tn: operand M / N-major.
+__device__ __forceinline__ uint32_t idesc_f8(int m, int n, bool tm, bool tn) {
+    uint32_t d = 1u << 4;
+    if (tm) d |= 1u << 15;
+    if (tn) d |= 1u << 16;
+    d |= (uint32_t)(n >> 3) << 17;
+    d |= (uint32_t)(m >> 4) << 24;
+    return d;
+}
+
+// An MMA issued by the one lane with `elected` set, in converged code: the predicate stands on
+// the instruction itself, so its operands stay in uniform registers.  (Inside an `if` of one
+// lane each MMA took 107 clocks to issue whatever its size; this form issues M = 128, K = 32 at
+// 39 clocks for N = 16 and 64 for N = 128, the rate of the tensor pipe.)
+__device__ __forceinline__ void tc_mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc,
+                                          uint32_t accumulate, uint32_t elected) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected)
+        : "memory");
+}
+
+// A in TMEM: row = lane, four 8-bit values along K per 32-bit column.
+__device__ __forceinline__ void tc_mma_f8_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                                             uint32_t accumulate, uint32_t elected) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "setp.ne.b32 q, %5, 0;\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(elected)
+        : "memory");
+}
+
+__device__ __forceinline__ void tc_commit_elected(uint64_t *bar, uint32_t elected) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %1, 0;\n\t"
+        "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}" ::"r"(smem_u32(bar)),
+        "r"(elected)
+        : "memory");
+}
+
+// Accumulator columns of this warp's 32 lanes, not waited for.
+__device__ __forceinline__ void tmem_ld8(uint32_t taddr, float *v) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7])
+                 : "r"(taddr)
+                 : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float *v) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=f"(v[0]), "=f"(v[1]), "=f"(v[2]), "=f"(v[3]), "=f"(v[4]), "=f"(v[5]), "=f"(v[6]), "=f"(v[7]), "=f"(v[8]),
+          "=f"(v[9]), "=f"(v[10]), "=f"(v[11]), "=f"(v[12]), "=f"(v[13]), "=f"(v[14]), "=f"(v[15]), "=f"(v[16]),
+          "=f"(v[17]), "=f"(v[18]), "=f"(v[19]), "=f"(v[20]), "=f"(v[21]), "=f"(v[22]), "=f"(v[23]), "=f"(v[24]),
+          "=f"(v[25]), "=f"(v[26]), "=f"(v[27]), "=f"(v[28]), "=f"(v[29]), "=f"(v[30]), "=f"(v[31])
+        : "r"(taddr)
+        : "memory");
+}
+// Wait for them; the registers pass through, so that no use moves before the wait.
+template <int N>
+__device__ __forceinline__ void tmem_ld_wait(float (&v)[N]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory");
+#pragma unroll
+    for (int i = 0; i < N; i++) asm volatile("" : "+f"(v[i]));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, "
+        "%15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// log2 and division to a few units of the last place.
+__device__ __forceinline__ float lg2(float x) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 2^x to 2 units of the last place, 0 below 2^-126.
+__device__ __forceinline__ float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 4 bytes global -> shared, asynchronously; zero without reading if !ok.
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool ok) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
+}
+// One arrival on `bar` once this thread's cp.async copies so far have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
+}
+
+// The first of a value's two E4M3 parts: its nearest of 4 significant bits.  (NaN gives some
+// number; the second part, value - first, is then NaN.)
+__device__ __forceinline__ float part_hi(float x) {
+    return __uint_as_float((__float_as_uint(x) + 0x80000u) & 0xfff00000u);
+}
+
+// A ring of stages: slot and phase parity of the next use.
+struct Ring {
+    int s = 0;
+    uint32_t ph = 0;
+    __device__ __forceinline__ void next(int n) {
+        if (++s == n) {
+            s = 0;
+            ph ^= 1u;
+        }
+    }
+};
+
+// Whether the phase of parity `parity` is complete, without waiting (try_wait may suspend the
+// thread for a while).
+__device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity)
+        : "memory");
+    return ok != 0;
+}
+
+// Whether a wait has gone on for too long (t0: its start, 0 before the first call) or another
+// role has given up; lane 0 of the converged warp records a timeout.
+__device__ __noinline__ bool gave_up(uint64_t &t0, StatusWord *st, unsigned where, int *abort_flag) {
+    const uint64_t now = global_timer_ns();
+    if (t0 == 0) t0 = now;
+    if (__any_sync(0xffffffffu, now - t0 > g_wait_limit_ns)) {
+        if ((threadIdx.x & 31) == 0) {
+            set_status(st, MOE_ERR_TIMEOUT, where);
+            *abort_flag = 1;
+        }
+        __syncwarp();
+        return true;
+    }
+    return __any_sync(0xffffffffu, *(const volatile int *)abort_flag != 0);
+}
+
+// A wait of a whole converged warp.  False after an abort or timeout.  The vote makes the
+// outcome uniform, so that what follows (descriptors, copies, MMAs) stays in uniform registers.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, StatusWord *st, unsigned where,
+                                          int *abort_flag) {
+    uint64_t t0 = 0;
+    for (uint32_t i = 1; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); i++)
+        if ((i & 31u) == 0u && gave_up(t0, st, where, abort_flag)) return false;
+    return true;
+}
+
+// The slow paths stay out of line: all roles of a CTA share one instruction cache, and the
+// kernel is bound by it as soon as their loops do not fit (measured with the waits inlined: 84%
+// of the fetches hit, and fetching was the largest stall).
+__device__ __noinline__ void soft_wait_slow(uint64_t *bar, uint32_t parity, StatusWord *st, unsigned where,
+                                            int *abort_flag) {
+    if (!mbar_wait_or_abort(bar, parity, st, where, abort_flag)) *abort_flag = 1;
+}
+
+// A wait in the softmax warps, whose warpgroup barriers must match: after an abort nothing
+// waits, and the code runs on to its end.
+__device__ __forceinline__ void soft_wait(uint64_t *bar, uint32_t parity, StatusWord *st, unsigned where,
+                                          int *abort_flag) {
+    if (!mbar_try_wait(bar, parity)) soft_wait_slow(bar, parity, st, where, abort_flag);
+    __syncwarp();
+}
+
+// Shared memory that both forms have, in bytes.
+struct CommonSmem {
+    uint32_t k, v, q, scales, seg, split, rows, bars, misc, total;
+    __host__ __device__ CommonSmem(int dim, int rows_, int nk, int nv) {
+        uint32_t o = 0;
+        k = o;      o += (uint32_t)nk * kTokens * dim;
+        v = o;      o += (uint32_t)nv * kTokens * dim;
+        q = o;      o += 4u * (uint32_t)rows_ * dim;                     // [2 buffers][2 parts][rows][dim]
+        scales = o; o += (uint32_t)kMaxStages * 2u * kMaxSlots * 4u;     // per value stage: keys', values'
+        seg = o;    o += (uint32_t)kSegs * (uint32_t)sizeof(Seg);
+        split = o;  o += 2u * (uint32_t)sizeof(Seg);                       // units shared with other CTAs
+        rows = o;   o += 2u * (uint32_t)rows_ * (uint32_t)sizeof(RowInfo);
+        bars = o;   o += 64u * 8u;
+        misc = o;   o += 512u;
+        total = o;
+    }
+};
+
+// Barriers, by index.
+struct Bars {
+    uint64_t *b;
+    __device__ uint64_t *k_full(int s) const { return b + s; }
+    __device__ uint64_t *k_empty(int s) const { return b + kMaxStages + s; }
+    __device__ uint64_t *v_full(int s) const { return b + 2 * kMaxStages + s; }
+    __device__ uint64_t *v_empty(int s) const { return b + 3 * kMaxStages + s; }
+    __device__ uint64_t *q_full(int s) const { return b + 4 * kMaxStages + s; }
+    __device__ uint64_t *q_empty(int s) const { return b + 4 * kMaxStages + 2 + s; }
+    __device__ uint64_t *s_full(int s) const { return b + 4 * kMaxStages + 4 + s; }   // scores in TMEM
+    __device__ uint64_t *p_ready(int s) const { return b + 4 * kMaxStages + 8 + s; }  // weights written, scores read
+    __device__ uint64_t *o_full(int s) const { return b + 4 * kMaxStages + 12 + s; }  // outputs in TMEM
+    __device__ uint64_t *o_empty(int s) const { return b + 4 * kMaxStages + 16 + s; }
+    __device__ uint64_t *mma_done() const { return b + 4 * kMaxStages + 20; }
+    __device__ uint64_t *seg_full(int s) const { return b + 4 * kMaxStages + 21 + s; }
+    __device__ uint64_t *seg_empty(int s) const { return b + 4 * kMaxStages + 25 + s; }
+};
+
+// ------------------------------------------- copies (warp 0: keys, warp 2: values, scales)
+// As with the MMAs, the predicate stands on the copy itself and the warp stays converged.
+__device__ __forceinline__ void tma_load_3d_elected(void *dst, const CUtensorMap *map, int c0, int c1, int c2,
+                                                    uint64_t *bar, uint32_t elected) {
+    asm volatile(
+        "{\n\t.reg .pred q;\n\t"
+        "setp.ne.b32 q, %6, 0;\n\t"
+        "@q cp.async.bulk.tensor.3d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];\n\t}" ::"r"(smem_u32(dst)),
+        "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar)), "r"(elected)
+        : "memory");
+}
+
+// SIDE 0: keys, 1: values; P: page size (a constant, as the warp's time per tile counts).
+template <int D, int SIDE, int P>
+__device__ __forceinline__ void copy_pages(const AttnArgs &a, const CUtensorMap *tm, unsigned char *smem,
+                                           const CommonSmem &L, const Bars &B, int *abort_flag) {
+    constexpr uint32_t kTile = kTokens * D;
+    constexpr int kSlots = kTokens / P;
+    const int lane = threadIdx.x & 31;
+    const KvView &kv = a.k.kv;
+    StatusWord *st = a.k.st;
+    const int n = SIDE ? a.nv : a.nk;
+    unsigned char *ring = smem + (SIDE ? L.v : L.k);
+    const uint32_t elected = elect_one();
+    Ring R;
+    int issued = 0;
+    bool run = true;
+#pragma unroll 1
+    for (int seg = 0; run; seg++) {
+        const int ss = seg % kSegs;
+        if (!warp_wait(B.seg_full(ss), (uint32_t)(seg / kSegs) & 1u, st, 0xa60u + SIDE, abort_flag)) break;
+        const Seg *sg = reinterpret_cast<const Seg *>(smem + L.seg) + ss;
+        const int count = sg->count;
+        if (count == 0) break;
+        const int32_t *row = a.k.page_table + (size_t)sg->b * a.k.table_width;
+        const int c0 = sg->tile0 * kSlots, c1 = min((sg->see_max + P - 1) / P, (sg->tile0 + count) * kSlots);
+        const int y = (SIDE * kv.heads + sg->head) * P;
+        const uint8_t *scale = reinterpret_cast<const uint8_t *>(kv.scale(0, a.k.layer, 0, sg->head));
+        __syncwarp();
+        if (elected) mbar_arrive(B.seg_empty(ss));
+        // page numbers, 32 columns at a time: lane l holds column base + l, and the next 32.  One
+        // past the last stands for a page outside the cache (it lies outside the tensor: zeros
+        // arrive) and for columns past the sequence's end.
+        auto number = [&](int col) {
+            if (col >= c1) return kv.n_pages;
+            const int page = row[col];
+            if (page >= 0 && page < kv.n_pages) return page;
+            set_status(st, MOE_ERR_BAD_PAGE, 3);
+            return kv.n_pages;
+        };
+        int at = 0, left = c1 - c0;  // column of the tile in the 32; columns from the tile on
+        int id = number(c0 + lane), id2 = number(c0 + 32 + lane), ahead = c0 + 64;
+#pragma unroll 1
+        for (int t = 0; t < count; t++) {
+            uint64_t *full = SIDE ? B.v_full(R.s) : B.k_full(R.s);
+            if (!(run = warp_wait(SIDE ? B.v_empty(R.s) : B.k_empty(R.s), R.ph ^ 1u, st, 0xa00u + 16 * SIDE + R.s,
+                                  abort_flag)))
+                break;
+            unsigned char *dst = ring + (uint32_t)R.s * kTile;
+            if (left >= kSlots) {
+                if (elected) mbar_arrive_expect_tx(full, kTile);
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < kSlots; j++)
+                    tma_load_3d_elected(dst + j * (P * D), tm, 0, y, __shfl_sync(0xffffffffu, id, at + j), full, elected);
+            } else {  // the sequence ends in this tile
+                if (elected) mbar_arrive_expect_tx(full, (uint32_t)max(left, 0) * (uint32_t)(P * D));
+                __syncwarp();
+                for (int j = 0; j < left; j++)
+                    tma_load_3d_elected(dst + j * (P * D), tm, 0, y, __shfl_sync(0xffffffffu, id, at + j), full, elected);
+            }
+            if constexpr (SIDE == 1) {
+                const int page = __shfl_sync(0xffffffffu, id, (at + lane) & 31);
+                if (lane < kSlots) {
+                    const bool ok = lane < left && page < kv.n_pages;
+                    const uint32_t sc = smem_u32(smem + L.scales) + (uint32_t)(R.s * 2 * kMaxSlots + lane) * 4u;
+                    const uint8_t *src = scale + (uint64_t)(ok ? page : 0) * kv.page_rec;
+                    cp_async4(sc, src, ok);
+                    cp_async4(sc + kMaxSlots * 4u, src + 4 * kv.heads, ok);
+                    cp_async_arrive(full);
+                }
+            }
+            at += kSlots;
+            left -= kSlots;
+            if (at == 32) {
+                at = 0;
+                id = id2;
+                id2 = number(ahead + lane);
+                ahead += 32;
+            }
+            issued++;
+            R.next(n);
+        }
+    }
+    // nothing may be in flight when the CTA exits
+    if (lane == 0) {
+        for (int i = max(0, issued - n); i < issued; i++)
+            mbar_wait(SIDE ? B.v_full(i % n) : B.k_full(i % n), (uint32_t)(i / n) & 1u, st, 0xa40u);
+    }
+    __syncwarp();
+}
+
+template <int D, int SIDE>
+__device__ __forceinline__ void copy_role(const AttnArgs &a, const CUtensorMap *tm, unsigned char *smem,
+                                          const CommonSmem &L, const Bars &B, int *abort_flag) {
+    switch (a.k.kv.page) {
+        case 16: return copy_pages<D, SIDE, 16>(a, tm, smem, L, B, abort_flag);
+        case 32: return copy_pages<D, SIDE, 32>(a, tm, smem, L, B, abort_flag);
+        case 64: return copy_pages<D, SIDE, 64>(a, tm, smem, L, B, abort_flag);
+        case 128: return copy_pages<D, SIDE, 128>(a, tm, smem, L, B, abort_flag);
+    }
+}
+
+// ------------------------------------------------------------- queries (warp 3)
+// Walks the CTA's share and publishes its segments (a few ahead), and loads each segment's row
+// data and queries, one segment ahead of the softmax: a row's values as two E4M3 parts, after a
+// power of two that puts its largest into [128, 256).
+template <int D, int R>
+__device__ __forceinline__ void query_role(const AttnArgs &a, unsigned char *smem, const CommonSmem &L, const Bars &B,
+                                           const Share &S, const int64_t *plan, int *abort_flag) {
+    constexpr int V = D / 32;  // values per lane
+    constexpr int U = 8;       // rows whose loads are in flight together
+    const int lane = threadIdx.x & 31;
+    Seg *ring = reinterpret_cast<Seg *>(smem + L.seg);
+    int64_t w = S.lo, first = plan[0];  // next position; first position of the item
+    int it = (int)plan[1];
+    Item x = load_item(a, it);
+    int published = 0;
+    bool ended = false;  // the end has been published
+#pragma unroll 1
+    for (int seg = 0;; seg++) {
+        // publish this segment and the next, and more if there is room
+#pragma unroll 1
+        while (!ended && published < seg + kSegs) {
+            const int ss = published % kSegs;
+            const uint32_t parity = ((uint32_t)(published / kSegs) & 1u) ^ 1u;
+            if (published > seg + 1) {
+                if (!__all_sync(0xffffffffu, mbar_test(B.seg_empty(ss), parity))) break;
+            } else if (!warp_wait(B.seg_empty(ss), parity, a.k.st, 0xe10u, abort_flag)) {
+                return;
+            }
+            Seg g;
+            g.count = 0;
+#pragma unroll 1
+            while (w < S.hi) {  // the next positions with tiles
+                const int64_t units = (int64_t)unit_length(a, x) * a.k.kv.heads;
+                if (w - first >= units) {
+                    first += units;
+                    x = load_item(a, ++it);
+                    continue;
+                }
+                const int len = unit_length(a, x);
+                // (w - first) / len; a division of 32 bits wherever the numbers allow
+                const int64_t local = w - first;
+                g.head = (local >> 31) == 0 ? (int)((uint32_t)local / (uint32_t)len) : (int)(local / len);
+                const int pos = (int)(local - (int64_t)g.head * len);
+                const int end = (int)min((int64_t)len, pos + (S.hi - w));
+                w += end - pos;
+                g.tile0 = max(0, pos - a.over);
+                g.count = max(0, end - a.over) - g.tile0;
+                if (g.count > 0) break;
+            }
+            if (g.count > 0) {
+                g.b = x.b;
+                g.rt = x.rt;
+                g.n = x.n;
+                g.len = x.len;
+                g.row0 = x.row0;
+                const int q0 = x.rt * a.rpt / a.group, q1 = min(x.n - 1, ((x.rt + 1) * a.rpt - 1) / a.group);
+                g.see_all = min(x.len, max(0, x.len - x.n + q0 + 1));
+                g.see_max = min(x.len, max(0, x.len - x.n + q1 + 1));
+                g.c0 = (int)blockIdx.x;
+                g.parts = 1;
+                if (g.count < x.nt) {
+                    const int64_t u0 = first + (int64_t)g.head * unit_length(a, x) + a.over;  // the unit's first tile
+                    g.c0 = cta_of(u0, S.total, S.ctas);
+                    g.parts = cta_of(u0 + x.nt - 1, S.total, S.ctas) - g.c0 + 1;
+                }
+            } else {
+                g.count = 0;
+                ended = true;
+            }
+            if (lane == 0) {
+                ring[ss] = g;
+                mbar_arrive(B.seg_full(ss));
+            }
+            __syncwarp();
+            published++;
+        }
+        const int buf = seg & 1;
+        if (!warp_wait(B.q_empty(buf), ((uint32_t)(seg >> 1) & 1u) ^ 1u, a.k.st, 0xe00u + buf, abort_flag)) return;
+        const Seg *sg = ring + seg % kSegs;
+        RowInfo *rows = reinterpret_cast<RowInfo *>(smem + L.rows) + buf * R;
+        unsigned char *q0 = smem + L.q + (uint32_t)buf * (2u * R * D);
+        const int rt = sg->rt, head = sg->head, row0 = sg->row0, before = sg->len - sg->n;
+        const int live = sg->count == 0 ? 0 : min(a.rpt, sg->n * a.group - rt * a.rpt);  // rows of the tile
+#pragma unroll 1
+        for (int r0 = 0; r0 < R && live > 0; r0 += U) {
+            uint32_t u[U][V / 2];
+            int row[U], hq[U];
+            // (row, head) of the first of them; the others follow without a division
+            int qi = (rt * a.rpt + r0) / a.group, hd = rt * a.rpt + r0 - qi * a.group;
+#pragma unroll
+            for (int i = 0; i < U; i++) {
+                row[i] = r0 + i < live ? row0 + qi : -1;
+                hq[i] = head * a.group + hd;
+                if (++hd == a.group) {
+                    hd = 0;
+                    qi++;
+                }
+                const uint16_t *src = a.k.q + (size_t)max(row[i], 0) * a.k.ldq + (size_t)hq[i] * D + lane * V;
+                if constexpr (V == 4) {
+                    const uint2 x2 = row[i] >= 0 ? *reinterpret_cast<const uint2 *>(src) : make_uint2(0u, 0u);
+                    u[i][0] = x2.x;
+                    u[i][1] = x2.y;
+                } else {
+                    u[i][0] = row[i] >= 0 ? *reinterpret_cast<const uint32_t *>(src) : 0u;
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < U; i++) {
+                const int r = r0 + i;
+                float h[V], l[V];
+                uint32_t amax = 0;  // over finite values
+#pragma unroll
+                for (int j = 0; j < V / 2; j++) {
+                    const uint32_t m = u[i][j] & 0x7fff7fffu;
+                    amax = __vmaxu2(amax, m & ~__vcmpgeu2(m, 0x7f807f80u));
+                }
+                amax = __reduce_max_sync(0xffffffffu, max(amax & 0xffffu, amax >> 16));
+                const int up = amax == 0 ? 0 : min(126, 7 - ((int)(amax >> 7) - 127));
+                const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+#pragma unroll
+                for (int j = 0; j < V; j++) {
+                    const uint32_t v = u[i][j / 2];
+                    const float y = __uint_as_float((j & 1) ? v & 0xffff0000u : v << 16) * f;
+                    h[j] = part_hi(y);
+                    l[j] = y - h[j];
+                }
+                // 16-byte chunks of a row are permuted as the tensor copies permute the keys'
+                const uint32_t byte = (uint32_t)(lane * V), chunk = byte >> 4;
+                const uint32_t swz = D == 128 ? (uint32_t)(r & 7) : (uint32_t)((r >> 1) & 3);
+                unsigned char *dst = q0 + (uint32_t)r * D + ((chunk ^ swz) << 4) + (byte & 15u);
+                if constexpr (V == 4) {
+                    *reinterpret_cast<uint32_t *>(dst) = e4m3x4_rn(h[0], h[1], h[2], h[3]);
+                    *reinterpret_cast<uint32_t *>(dst + R * D) = e4m3x4_rn(l[0], l[1], l[2], l[3]);
+                } else {
+                    *reinterpret_cast<uint16_t *>(dst) = (uint16_t)e4m3x2_rn(h[0], h[1]);
+                    *reinterpret_cast<uint16_t *>(dst + R * D) = (uint16_t)e4m3x2_rn(l[0], l[1]);
+                }
+                if (lane == 0) {
+                    RowInfo ri;
+                    ri.row = row[i];
+                    ri.head = hq[i];
+                    ri.qs = __uint_as_float((uint32_t)(127 - up) << 23);
+                    ri.pos = row[i] < 0 ? -1 : before + (row[i] - row0);
+                    rows[r] = ri;
+                }
+            }
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(B.q_full(buf));
+        if (live == 0) return;  // the end
+    }
+}
+
+// Value rows of the tile's tokens in shared memory, for one tile that not every row sees
+// whole (thread = token `tok` of the tile, which is token t of the sequence): rows that no
+// row sees hold anything and become zero; NaN in rows that only some rows see must not reach
+// the others, so it becomes zero here and is put back in the outputs (the returned truth).
+template <int D>
+__device__ __noinline__ bool clean_values(unsigned char *tile, int tok, int t, int see_all, int see_max) {
+    bool bad = false;
+    if (t < see_all) return false;
+#pragma unroll 1
+    for (int j = 0; j < D / 16; j++) {
+        uint4 *q = reinterpret_cast<uint4 *>(tile + (uint32_t)tok * D) + j;
+        uint4 z = make_uint4(0u, 0u, 0u, 0u);
+        if (t < see_max) {
+            z = *q;
+            uint32_t w[4] = {z.x, z.y, z.z, z.w};
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                const uint32_t n = __vcmpeq4(w[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                bad |= n != 0;
+                w[k] &= ~n;
+            }
+            z = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+        *q = z;
+    }
+    return bad;
+}
+
+// Code of value d of token t as it lies in the cache (0 if its page is outside).
+__device__ __noinline__ const uint8_t *value_codes(const AttnArgs &a, int b, int head, int t) {
+    const int P = a.k.kv.page;
+    const int page = a.k.page_table[(size_t)b * a.k.table_width + t / P];
+    if (page < 0 || page >= a.k.kv.n_pages) return nullptr;
+    return a.k.kv.codes(page, a.k.layer, 1, head) + (size_t)(t % P) * a.k.kv.dim;
+}
+
+// ---------------------------------------- sequences shared with other CTAs
+// All NSOFT softmax threads, after the CTA's last segment: partial results are published,
+// and once every CTA has done so the CTA joins its rows of the (at most two) units it shares,
+// `shared` of which stand in `list`.
+template <int D, int NSOFT>
+__device__ __forceinline__ void join_role(const AttnArgs &a, const Share &S, const Seg *list, int shared, int bar_id,
+                                          int *abort_flag) {
+    StatusWord *st = a.k.st;
+    const int tid = (int)threadIdx.x - 32 * kFirstSoft, lane = tid & 31, sw = tid >> 5, cta = (int)blockIdx.x;
+    const size_t slot_floats = (size_t)a.rpt * D + 2 * a.rpt;
+    unsigned int *arrive = &st->pad[kStKvArrive], *leave = &st->pad[kStKvExit];
+    __threadfence();
+    named_barrier(bar_id, NSOFT);
+    if (tid == 0) red_release_gpu_add(arrive, 1u);
+    if (shared > 0) {
+        if (tid == 0 && *(volatile int *)abort_flag == 0) {
+            const uint64_t t0 = global_timer_ns(), lim = g_wait_limit_ns;
+            while (ld_acquire_gpu(arrive) < (unsigned)S.ctas) {
+                if (global_timer_ns() - t0 > lim) {
+                    set_status(st, MOE_ERR_TIMEOUT, 0xd00u);
+                    *abort_flag = 1;
+                    break;
+                }
+            }
+        }
+        named_barrier(bar_id, NSOFT);
+    }
+#pragma unroll 1
+    for (int i = 0; i < shared; i++) {
+        if (*(volatile int *)abort_flag) break;
+        const Seg &g = list[i];
+        const int c0 = g.c0, parts = g.parts;
+        const int nrows = min(a.rpt, g.n * a.group - g.rt * a.rpt);
+        // rows cta - c0, + parts, ...: a warp per row, lanes over the head's values
+#pragma unroll 1
+        for (int r = (cta - c0) + parts * sw; r < nrows; r += parts * (NSOFT / 32)) {
+            constexpr int V = D / 32;
+            float m = -INFINITY;
+            for (int p = lane; p < parts; p += 32) {
+                const float *slot = a.part + (size_t)(2 * (c0 + p) + (p == 0 ? 1 : 0)) * slot_floats;
+                m = fmaxf(m, __ldcg(slot + (size_t)a.rpt * D + 2 * r));
+            }
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+            float l = 0.f, acc[V];
+#pragma unroll
+            for (int j = 0; j < V; j++) acc[j] = 0.f;
+#pragma unroll 4
+            for (int p = 0; p < parts; p++) {
+                const float *slot = a.part + (size_t)(2 * (c0 + p) + (p == 0 ? 1 : 0)) * slot_floats;
+                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(slot + (size_t)a.rpt * D + 2 * r));
+                const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+                l += ml.y * f;
+                const float *v = slot + (size_t)r * D + lane * V;
+                if constexpr (V == 4) {
+                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(v));
+                    acc[0] = fmaf(x.x, f, acc[0]);
+                    acc[1] = fmaf(x.y, f, acc[1]);
+                    acc[2] = fmaf(x.z, f, acc[2]);
+                    acc[3] = fmaf(x.w, f, acc[3]);
+                } else {
+                    const float2 x = __ldcg(reinterpret_cast<const float2 *>(v));
+                    acc[0] = fmaf(x.x, f, acc[0]);
+                    acc[1] = fmaf(x.y, f, acc[1]);
+                }
+            }
+            const int R = g.rt * a.rpt + r, qi = R / a.group, row = g.row0 + qi;
+            const int hq = g.head * a.group + R - qi * a.group;
+            const float inv = m == -INFINITY ? 0.f : 1.f / l;
+            uint16_t *out = a.k.out + (size_t)row * a.k.ldo + (size_t)hq * D + lane * V;
+#pragma unroll
+            for (int j = 0; j < V; j++) out[j] = __bfloat16_as_ushort(__float2bfloat16(acc[j] * inv));
+            if (a.k.lse != nullptr && lane == 0)
+                a.k.lse[(size_t)row * a.k.heads_q + hq] = m == -INFINITY ? -INFINITY : kLn2 * (m + log2f(l));
+        }
+    }
+    named_barrier(bar_id, NSOFT);
+    if (tid == 0 && atomicAdd(leave, 1u) == (unsigned)S.ctas - 1u) {
+        // every CTA has arrived and has stopped polling
+        *(volatile unsigned int *)arrive = 0u;
+        *(volatile unsigned int *)leave = 0u;
+    }
+}
+
+}  // namespace
+
+// The two forms, by the number of rows of a row tile: tokens along the tensor cores' M for
+// up to 32 rows (kv_attention.cu), rows along M for up to 128 (kv_attention_rows.cu).
+cudaError_t launch_attention_rows(const CUtensorMap &tm, AttnArgs a, int sms, int smem_max, cudaStream_t st);
+cudaError_t set_wait_limit_kv_attention_rows(uint64_t ns);
+
+}  // namespace moe

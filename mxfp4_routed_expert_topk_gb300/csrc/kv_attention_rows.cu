@@ -1,0 +1,491 @@
+// Cache attention, the form for row tiles of more than 32 rows (a verification batch's rows
+// times the query heads of a key/value head, or a prompt's).
+//
+// Rows lie along M: S = Q K^T (M = 128 rows, N = 128 tokens, both operands K-major) and
+// O = P V (M = 128 rows, N = head_dim, K = 128 tokens; P is the A operand in TMEM, V is read
+// N-major).  The TMEM lane of a score is its row, so a row's maximum and sum need no exchange
+// between lanes and its reference is one register; the pages' key scales and the logarithm of
+// their value scales are constants of a run of 16 tokens and go into the exponent's multiply-
+// add.  Weights replace the scores they came from in TMEM.
+//
+// What bounds it is instruction issue: 128 x 128 scores a tile at 7 to 8 instructions each are
+// about 1000 clocks of all four schedulers, next to 1400 that the tile's 32 KB take from HBM
+// and 1024 of the tensor pipe.  Two warpgroups take tiles in turn (a thread per row); the
+// joining of a tile's output is shared by columns, half of them in each warpgroup, so a thread
+// keeps 64 running outputs; each tile's reference and sum pass through shared memory.
+#include <algorithm>
+
+#include "kv_attention.cuh"
+
+namespace moe {
+namespace {
+
+constexpr int kSoft = 256;
+constexpr int kThreads = 32 * kFirstSoft + kSoft;
+constexpr int kRows = 128;
+constexpr int kBarAll = 7;
+
+struct RowsSmem {
+    CommonSmem c;
+    uint32_t ml, fac, chunk, nan, total;
+    __host__ __device__ RowsSmem(int dim, int nk, int nv) : c(dim, kRows, nk, nv) {
+        uint32_t o = (c.total + 127u) & ~127u;
+        ml = o;    o += 4u * kRows * 8u;         // [4 tiles][row] (reference, sum)
+        fac = o;   o += 4u * 4u;                 // [4 tiles] value of a weight unit
+        nan = o;   o += 4u * 4u * 4u;            // [4 tiles][warp] tokens whose values hold partial NaN
+        o = (o + 15u) & ~15u;
+        chunk = o; o += 8u * kMaxSlots * 16u;    // [warp][page] (key scale, log2 weight scale, 1 / weight scale)
+        total = o;
+    }
+};
+
+__device__ __forceinline__ uint64_t pack2(float a, float b) {
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(uint64_t v, float &a, float &b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
+// A pair of weights as E4M3 parts: first = the value to 4 significant bits (Veltkamp's
+// splitting: x * (2^20 + 1) minus its difference from x), second = what is left.
+__device__ __forceinline__ void split2(uint64_t x, float &h0, float &h1, float &l0, float &l1) {
+    const uint64_t c = pack2(1048577.f, 1048577.f), neg = pack2(-1.f, -1.f);
+    const uint64_t t = mul2(x, c);
+    const uint64_t d = fma2(x, neg, t);    // t - x
+    const uint64_t h = fma2(d, neg, t);    // t - (t - x)
+    unpack2(h, h0, h1);
+    unpack2(fma2(h, neg, x), l0, l1);
+}
+
+template <int D>
+__global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __grid_constant__ CUtensorMap tm,
+                                                                         const AttnArgs a) {
+    constexpr uint32_t kTile = kTokens * D;
+    constexpr uint32_t kSwz = D == 128 ? kSwizzle128B : kSwizzle64B;
+    constexpr uint32_t kGroup8 = 8 * D;
+    constexpr int DH = D / 2;  // columns of the output that a warpgroup joins
+    extern __shared__ __align__(1024) unsigned char smem_raw[];
+    unsigned char *smem = (unsigned char *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
+    const RowsSmem F(D, a.nk, a.nv);
+    const CommonSmem &L = F.c;
+    const Bars B{reinterpret_cast<uint64_t *>(smem + L.bars)};
+    uint32_t *misc = reinterpret_cast<uint32_t *>(smem + L.misc);
+    uint32_t *tmem_slot = misc;
+    int *abort_flag = reinterpret_cast<int *>(misc + 1);
+    int *go = reinterpret_cast<int *>(misc + 2);
+    int64_t *plan = reinterpret_cast<int64_t *>(misc + 8);
+    StatusWord *st = a.k.st;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+
+    const Share S = cut_shares<kThreads>(a, plan);
+    if ((int)blockIdx.x >= S.ctas) return;  // the whole CTA: nothing set up yet
+    if (tid == 0) {
+        for (int s = 0; s < a.nk; s++) {
+            mbar_init(B.k_full(s), 1);
+            mbar_init(B.k_empty(s), 1);
+        }
+        for (int s = 0; s < a.nv; s++) {
+            mbar_init(B.v_full(s), 1 + kTokens / a.k.kv.page);
+            mbar_init(B.v_empty(s), 1);
+        }
+        for (int b = 0; b < 2; b++) {
+            mbar_init(B.q_full(b), 1);
+            mbar_init(B.q_empty(b), kSoft / 32);
+            mbar_init(B.s_full(b), 1);
+            mbar_init(B.p_ready(b), 4);
+            mbar_init(B.o_full(b), 1);
+            mbar_init(B.o_empty(b), kSoft / 32);
+        }
+        for (int b = 0; b < kSegs; b++) {
+            mbar_init(B.seg_full(b), 1);
+            mbar_init(B.seg_empty(b), 2 + kSoft / 32);  // the copying warps, and the softmax
+        }
+        mbar_init(B.mma_done(), 1);
+        *abort_flag = 0;
+        fence_mbar_init();
+    }
+    if (warp == 1) tmem_alloc(tmem_slot, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tmem_slot;        // scores, then weights: two buffers of 128 columns
+    const uint32_t tmem_o = tmem + 2 * kTokens;
+
+    if (warp == 0) {
+        copy_role<D, 0>(a, &tm, smem, L, B, abort_flag);
+    } else if (warp == 2) {
+        copy_role<D, 1>(a, &tm, smem, L, B, abort_flag);
+    } else if (warp == 1) {
+        // ------------------------------------------------------ MMA issue
+        const uint32_t id_s = idesc_f8(kRows, kTokens, false, false), id_o = idesc_f8(kRows, D, false, true);
+        const uint64_t kd = smem_desc(smem_u32(smem + L.k), 16, kGroup8, kSwz);
+        const uint64_t vd = smem_desc(smem_u32(smem + L.v), kGroup8, kGroup8, kSwz);
+        const uint64_t qd = smem_desc(smem_u32(smem + L.q), 16, kGroup8, kSwz);
+        Ring K, V;
+        int ns = 0, np = 0, seg = 0, seg_end = 0, qb = 0;  // scores / outputs issued
+        bool last = false;                                 // seg_end is the share's end
+        const uint32_t elected = elect_one();
+        // Whichever is ready: the outputs of tile np, the scores of tile ns (over the weights of
+        // tile ns - 2, whose outputs have been issued; with the segment's queries).  Lanes 0 to 4
+        // look at one barrier each; a vote makes the outcome uniform, which keeps the descriptors
+        // in uniform registers.
+        uint64_t idle = 0;  // since when nothing has been ready
+        uint32_t rounds = 0;
+        while (!(last && np == seg_end)) {
+            const uint32_t ph = (uint32_t)(np >> 1) & 1u;
+            uint64_t *look = lane == 0   ? B.p_ready(np & 1)
+                             : lane == 1 ? B.v_full(V.s)
+                             : lane == 2 ? B.o_empty(np & 1)
+                             : lane == 3 ? B.k_full(K.s)
+                                         : B.q_full(seg & 1);
+            const uint32_t parity = lane == 0 ? ph : lane == 1 ? V.ph : lane == 2 ? ph ^ 1u : lane == 3 ? K.ph : (uint32_t)(seg >> 1) & 1u;
+            const uint32_t m = __ballot_sync(0xffffffffu, lane < 5 && mbar_test(look, parity));
+            const bool out = np < ns && (m & 7u) == 7u;
+            if (ns == seg_end && !last && (m & 16u) != 0u) {  // the next segment's queries are there
+                const volatile Seg *sg = reinterpret_cast<const volatile Seg *>(smem + L.seg) + seg % kSegs;
+                const int count = __shfl_sync(0xffffffffu, sg->count, 0);
+                qb = seg & 1;
+                seg_end += count;
+                last = __any_sync(0xffffffffu, count == 0);
+                seg++;
+            }
+            const bool scores = ns < seg_end && ns < np + (out ? 3 : 2) && (m & 8u) != 0u;
+            if (!out && !scores) {
+                if ((++rounds & 63u) == 0u && gave_up(idle, st, 0xb00u, abort_flag)) break;
+                continue;
+            }
+            idle = 0;
+            tc_fence_after();
+            if (out) {
+                const int buf = np & 1;
+                const uint64_t va = vd + (uint64_t)((uint32_t)V.s * kTile >> 4);
+                const uint32_t p = tmem + (uint32_t)(buf * kTokens);
+                // 32 tokens take 8 columns per part: the parts of each 32 lie side by side
+#pragma unroll
+                for (int part = 0; part < 2; part++)
+#pragma unroll
+                    for (int k = 0; k < kTokens / 32; k++)
+                        tc_mma_f8_ts(tmem_o + (uint32_t)(buf * D), p + (uint32_t)(16 * k + 8 * part),
+                                     va + (uint64_t)(k * (32 * D) >> 4), id_o, (part > 0 || k > 0) ? 1u : 0u, elected);
+                tc_commit_elected(B.v_empty(V.s), elected);
+                tc_commit_elected(B.o_full(buf), elected);
+                V.next(a.nv);
+                np++;
+            }
+            if (scores) {
+                const uint64_t ka = kd + (uint64_t)((uint32_t)K.s * kTile >> 4);
+                const uint64_t qa = qd + (uint64_t)((uint32_t)qb * (2u * kRows * D) >> 4);
+#pragma unroll
+                for (int part = 0; part < 2; part++)
+#pragma unroll
+                    for (int k = 0; k < D / 32; k++)
+                        tc_mma_f8(tmem + (uint32_t)((ns & 1) * kTokens),
+                                  qa + (uint64_t)(part * (kRows * D) >> 4) + (uint64_t)(2 * k), ka + (uint64_t)(2 * k),
+                                  id_s, (part > 0 || k > 0) ? 1u : 0u, elected);
+                tc_commit_elected(B.k_empty(K.s), elected);
+                tc_commit_elected(B.s_full(ns & 1), elected);
+                K.next(a.nk);
+                ns++;
+            }
+        }
+        if (elect_one()) tc_commit(B.mma_done());
+        __syncwarp();
+        if (lane == 0) mbar_wait(B.mma_done(), 0u, st, 0xb30u);
+        __syncwarp();
+    } else if (warp < kFirstSoft) {
+        query_role<D, kRows>(a, smem, L, B, S, plan, abort_flag);
+    } else {
+        // -------------------------------------------------------- softmax
+        const int sw = warp - kFirstSoft, wg = sw >> 2, ew = sw & 3, stid = tid - 32 * kFirstSoft;
+        const int row = 32 * ew + lane;  // row of the tile (TMEM lane); also the token it cleans
+        const uint32_t lanes = (uint32_t)(32 * ew) << 16;
+        float2 *ml = reinterpret_cast<float2 *>(smem + F.ml);
+        float *fac = reinterpret_cast<float *>(smem + F.fac);
+        uint32_t *nan = reinterpret_cast<uint32_t *>(smem + F.nan);
+        float4 *chunk = reinterpret_cast<float4 *>(smem + F.chunk) + sw * kMaxSlots;
+        const float *scales = reinterpret_cast<const float *>(smem + L.scales);
+        const int page_shift = 31 - __clz(a.k.kv.page), slots = kTokens >> page_shift;
+        const size_t slot_floats = (size_t)a.rpt * D + 2 * a.rpt;
+        float o[DH];
+        int done = 0;  // tiles of earlier segments
+        int shared = 0;  // units shared with other CTAs
+        if (stid == 0) *go = mbar_wait_or_abort(B.q_full(0), 0u, st, 0xc30u, abort_flag) ? 1 : 0;
+        named_barrier(kBarAll, kSoft);
+
+#pragma unroll 1
+        for (int seg = 0;; seg++) {
+            // after an abort the segment's description may be missing: all leave together
+            if (*(volatile int *)go == 0) break;
+            const int buf = seg & 1;
+            soft_wait(B.q_full(buf), (uint32_t)(seg >> 1) & 1u, st, 0xc31u, abort_flag);
+            const Seg *sg = reinterpret_cast<const Seg *>(smem + L.seg) + seg % kSegs;
+            const RowInfo ri = reinterpret_cast<const RowInfo *>(smem + L.rows)[buf * kRows + row];
+            const int count = sg->count, tile0 = sg->tile0, see_all = sg->see_all, see_max = sg->see_max;
+            if (count == 0) break;
+            float m_run = -INFINITY, l_run = 0.f;
+#pragma unroll
+            for (int i = 0; i < DH; i++) o[i] = 0.f;
+
+            // Scores of tile t of the segment -> weights; its reference and sum.
+            auto softmax = [&](int t) {
+                const int u = done + t, sb = u & 1, vb = u % a.nv;
+                soft_wait(B.v_full(vb), (uint32_t)(u / a.nv) & 1u, st, 0xc10u + vb, abort_flag);
+                // constants of the tile's pages: lane j has page j
+                {
+                    const float *sc = scales + vb * 2 * kMaxSlots;
+                    const float ks = sc[lane & 7] * a.scale2, vs = lane < slots ? sc[kMaxSlots + lane] : 0.f;
+                    const bool fin = vs < INFINITY;
+                    float vone = fin ? vs : 0.f;
+#pragma unroll
+                    for (int d = 4; d > 0; d >>= 1) vone = fmaxf(vone, __shfl_xor_sync(0xffffffffu, vone, d));
+                    vone = vone > 0.f ? vone : 1.f;
+                    const float c = fmaxf(256.f * __fdividef(vs, vone), 8.67361738e-19f);  // at least 2^-60
+                    if (lane < kMaxSlots)
+                        chunk[lane] = make_float4(ks, fin ? lg2(c) : kNan, fin ? __fdividef(1.f, c) : 1.f, 0.f);
+                    if (lane == 0) fac[u & 3] = vone * (1.f / 256.f);
+                }
+                const bool special = (tile0 + t + 1) * kTokens > see_all;
+                const int lim = min(max(ri.pos + 1 - (tile0 + t) * kTokens, 0), kTokens);  // tokens the row sees
+                uint32_t word = 0;
+                if (special) {
+                    const int tk = (tile0 + t) * kTokens + row;
+                    const bool bad = clean_values<D>(smem + L.v + (uint32_t)vb * kTile, row, tk, see_all, see_max);
+                    word = __ballot_sync(0xffffffffu, bad);
+                    fence_proxy_async_smem();
+                }
+                if (lane == 0) nan[(u & 3) * 4 + ew] = word;
+                soft_wait(B.s_full(sb), (uint32_t)(u >> 1) & 1u, st, 0xc00u + sb, abort_flag);
+                tc_fence_after();
+                const uint32_t ts = tmem + (uint32_t)(sb * kTokens) + lanes;
+                // loops over 32 tokens are not unrolled: the body must stay in the instruction cache
+                float mx = -INFINITY;
+#pragma unroll 1
+                for (int h = 0; h < kTokens; h += 32) {
+                    float x[32];
+                    tmem_ld32(ts + h, x);
+                    tmem_ld_wait(x);
+                    if (special) {
+#pragma unroll
+                        for (int i = 0; i < 32; i++) x[i] = h + i < lim ? x[i] : -INFINITY;
+                    }
+#pragma unroll
+                    for (int q = 0; q < 2; q++) {
+                        float m4[4];
+#pragma unroll
+                        for (int i = 0; i < 4; i++)
+                            m4[i] = fmaxf(fmaxf(x[16 * q + i], x[16 * q + 4 + i]), fmaxf(x[16 * q + 8 + i], x[16 * q + 12 + i]));
+                        mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * chunk[(h + 16 * q) >> page_shift].x);
+                    }
+                }
+                const float mt = mx * ri.qs, base = mt == -INFINITY ? 0.f : mt;
+                float l = 0.f;
+#pragma unroll 1
+                for (int h = 0; h < kTokens; h += 32) {
+                    float x[32];
+                    tmem_ld32(ts + h, x);
+                    uint64_t A2[2], C2[2];
+                    float r[2];
+#pragma unroll
+                    for (int q = 0; q < 2; q++) {
+                        const float4 c = chunk[(h + 16 * q) >> page_shift];
+                        const float A = c.x * ri.qs, C = c.y - base;
+                        A2[q] = pack2(A, A);
+                        C2[q] = pack2(C, C);
+                        r[q] = c.z;
+                    }
+                    tmem_ld_wait(x);
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2) {
+                        unpack2(fma2(pack2(x[i], x[i + 1]), A2[i >> 4], C2[i >> 4]), x[i], x[i + 1]);
+                        x[i] = ex2(x[i]);
+                        x[i + 1] = ex2(x[i + 1]);
+                    }
+                    if (special) {
+#pragma unroll
+                        for (int i = 0; i < 32; i++) x[i] = h + i < lim ? x[i] : 0.f;
+                    }
+                    uint32_t w[16];  // the 32 tokens' first parts, then their second parts
+#pragma unroll
+                    for (int q = 0; q < 2; q++) {
+                        uint64_t s0 = 0, s1 = 0;
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            const int i = 16 * q + 4 * j;
+                            const uint64_t e0 = pack2(x[i], x[i + 1]), e1 = pack2(x[i + 2], x[i + 3]);
+                            s0 = add2(s0, e0);
+                            s1 = add2(s1, e1);
+                            float hi[4], lo[4];
+                            split2(e0, hi[0], hi[1], lo[0], lo[1]);
+                            split2(e1, hi[2], hi[3], lo[2], lo[3]);
+                            w[4 * q + j] = e4m3x4_rn(hi[0], hi[1], hi[2], hi[3]);
+                            w[8 + 4 * q + j] = e4m3x4_rn(lo[0], lo[1], lo[2], lo[3]);
+                        }
+                        float a0, a1;
+                        unpack2(add2(s0, s1), a0, a1);
+                        l = fmaf(a0 + a1, r[q], l);
+                    }
+                    tmem_st16(ts + (h >> 1), w);  // over scores that have been read
+                }
+                tmem_st_wait();
+                ml[(u & 3) * kRows + row] = make_float2(mt, l);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(B.p_ready(sb));
+            };
+
+            // Add this warpgroup's columns of tile t's output to the running output.
+            auto join_tile = [&](int t) {
+                const int u = done + t, ob = u & 1;
+                soft_wait(B.o_full(ob), (uint32_t)(u >> 1) & 1u, st, 0xc20u + ob, abort_flag);
+                tc_fence_after();
+                float y[DH];
+#pragma unroll
+                for (int i = 0; i < DH; i += 32) tmem_ld32(tmem_o + (uint32_t)(ob * D + wg * DH + i) + lanes, y + i);
+                const float2 v = ml[(u & 3) * kRows + row];
+                const float m = fmaxf(m_run, v.x);
+                const float f_old = m_run == -INFINITY ? 0.f : ex2(m_run - m), f_new = v.x == -INFINITY ? 0.f : ex2(v.x - m);
+                m_run = m;
+                l_run = fmaf(l_run, f_old, v.y * f_new);
+                const float g = f_new * fac[u & 3];
+                const uint64_t g2 = pack2(g, g), k2 = pack2(f_old, f_old);
+                if (__any_sync(0xffffffffu, f_old != 1.f)) {  // some row's maximum has moved
+#pragma unroll
+                    for (int i = 0; i < DH; i += 2) unpack2(mul2(pack2(o[i], o[i + 1]), k2), o[i], o[i + 1]);
+                }
+                tmem_ld_wait(y);
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(B.o_empty(ob));
+#pragma unroll
+                for (int i = 0; i < DH; i += 2)
+                    unpack2(fma2(pack2(y[i], y[i + 1]), g2, pack2(o[i], o[i + 1])), o[i], o[i + 1]);
+                // NaN values that only some rows see, back into those rows' outputs
+#pragma unroll 1
+                for (int w = 0; w < 4; w++) {
+                    for (uint32_t word = nan[(u & 3) * 4 + w]; word != 0u; word &= word - 1u) {
+                        const int tn = (tile0 + t) * kTokens + 32 * w + __ffs((int)word) - 1;
+                        const uint8_t *code = value_codes(a, sg->b, sg->head, tn);
+                        if (code == nullptr || tn > ri.pos) continue;
+#pragma unroll
+                        for (int i = 0; i < DH; i++)
+                            if ((code[wg * DH + i] & 0x7fu) == 0x7fu) o[i] = kNan;
+                    }
+                }
+            };
+
+            int next = 0;
+            for (int t = (wg ^ done) & 1; t < count; t += 2) {
+                softmax(t);
+                for (; next < t; next++) join_tile(next);
+            }
+            for (; next < count; next++) join_tile(next);
+
+            float *part = sg->parts > 1 ? a.part + (size_t)(2 * (int)blockIdx.x + (tile0 == 0 ? 1 : 0)) * slot_floats
+                                         : nullptr;
+            if (ri.row >= 0 && !*(volatile int *)abort_flag) {
+                if (part != nullptr) {
+                    float *d = part + (size_t)row * D + wg * DH;
+#pragma unroll
+                    for (int i = 0; i < DH; i += 4)
+                        *reinterpret_cast<float4 *>(d + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    if (wg == 0)
+                        *reinterpret_cast<float2 *>(part + (size_t)a.rpt * D + 2 * row) = make_float2(m_run, l_run);
+                } else {
+                    const float inv = m_run == -INFINITY ? 0.f : 1.f / l_run;
+                    uint16_t *d = a.k.out + (size_t)ri.row * a.k.ldo + (size_t)ri.head * D + wg * DH;
+#pragma unroll
+                    for (int i = 0; i < DH; i += 8) {
+                        uint32_t b[4];
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            const __nv_bfloat162 z = __floats2bfloat162_rn(o[i + 2 * j] * inv, o[i + 2 * j + 1] * inv);
+                            b[j] = *reinterpret_cast<const uint32_t *>(&z);
+                        }
+                        *reinterpret_cast<uint4 *>(d + i) = make_uint4(b[0], b[1], b[2], b[3]);
+                    }
+                    if (wg == 0 && a.k.lse != nullptr)
+                        a.k.lse[(size_t)ri.row * a.k.heads_q + ri.head] =
+                            m_run == -INFINITY ? -INFINITY : kLn2 * (m_run + log2f(l_run));
+                }
+            }
+            if (part != nullptr) {
+                if (stid == 0) reinterpret_cast<Seg *>(smem + L.split)[shared] = *sg;
+                shared++;
+            }
+            done += count;
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(B.q_empty(buf));
+                mbar_arrive(B.seg_empty(seg % kSegs));
+            }
+            named_barrier(kBarAll, kSoft);  // nobody still reads the last decision
+            if (stid == 0)
+                *go = mbar_wait_or_abort(B.q_full(buf ^ 1), (uint32_t)((seg + 1) >> 1) & 1u, st, 0xc32u, abort_flag) ? 1 : 0;
+            named_barrier(kBarAll, kSoft);
+        }
+        join_role<D, kSoft>(a, S, reinterpret_cast<const Seg *>(smem + L.split), shared, kBarAll, abort_flag);
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (warp == 1) tmem_dealloc(tmem, 512);
+}
+
+template <int D>
+cudaError_t launch(const CUtensorMap &tm, AttnArgs a, int sms, int smem_max, cudaStream_t st) {
+    static PerDevice smem_set(0);
+    a.over = 4;
+    a.nk = a.nv = 2;
+    while (true) {  // as many stages as fit, values first
+        AttnArgs b = a;
+        if (b.nv < kMaxStages && b.nv < b.nk + 1)
+            b.nv++;
+        else if (b.nk < kMaxStages)
+            b.nk++;
+        else
+            break;
+        if (RowsSmem(D, b.nk, b.nv).total + 1024u > (uint32_t)smem_max) break;
+        a = b;
+    }
+    const size_t smem = RowsSmem(D, a.nk, a.nv).total + 1024;
+    if (smem > (size_t)smem_max) return cudaErrorNotSupported;
+    cudaError_t e = ensure_dynamic_smem(kv_attention_rows_kernel<D>, smem, smem_set);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)sms);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeCooperative;  // the join waits for all CTAs
+    attr[0].val.cooperative = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kv_attention_rows_kernel<D>, tm, a);
+}
+
+}  // namespace
+
+cudaError_t set_wait_limit_kv_attention_rows(uint64_t ns) { return set_wait_limit_here(ns); }
+
+cudaError_t launch_attention_rows(const CUtensorMap &tm, AttnArgs a, int sms, int smem_max, cudaStream_t st) {
+    return a.k.kv.dim == 128 ? launch<128>(tm, a, sms, smem_max, st) : launch<64>(tm, a, sms, smem_max, st);
+}
+
+}  // namespace moe
