@@ -138,9 +138,8 @@ __global__ void __launch_bounds__(32 * kFirstSoft + 128 * groups_of(R), 1)
         // weights: N-major without swizzle, 16 rows x 8 tokens (128 bytes) per core matrix,
         // 8-token groups 128 bytes and 16-row chunks 2 KB apart
         const uint64_t pd = smem_desc(smem_u32(smem + F.p), 128, kTokens * 16, kSwizzleNone);
-        Ring K, V;
+        int ks = 0, vs = 0;  // stages
         int ns = 0, np = 0, ws = 0, wp = 0;  // scores / outputs issued, and their warpgroups
-        uint32_t pp = 0;                     // phase of p_ready
         int seg = 0, seg_end = 0, qb = 0;
         bool last = false;                   // seg_end is the share's end
         const uint32_t elected = elect_one();
@@ -148,12 +147,13 @@ __global__ void __launch_bounds__(32 * kFirstSoft + 128 * groups_of(R), 1)
         // scores once its last weights have been read, and only with the segment's queries).
         // Lanes 0 to 3 look at one barrier each; a vote makes the outcome uniform, which keeps
         // the descriptors in uniform registers.
+        Watch eye = lane == 0   ? Watch{B.p_ready(0), kGroups, 0, 0u}
+                    : lane == 1 ? Watch{B.v_full(0), a.nv, 0, 0u}
+                    : lane == 2 ? Watch{B.k_full(0), a.nk, 0, 0u}
+                                : Watch{B.q_full(0), 2, 0, 0u};
         uint64_t idle = 0;  // since when nothing has been ready
-        uint32_t rounds = 0;
         while (!(last && np == seg_end)) {
-            uint64_t *look = lane == 0 ? B.p_ready(wp) : lane == 1 ? B.v_full(V.s) : lane == 2 ? B.k_full(K.s) : B.q_full(seg & 1);
-            const uint32_t parity = lane == 0 ? pp : lane == 1 ? V.ph : lane == 2 ? K.ph : (uint32_t)(seg >> 1) & 1u;
-            const uint32_t m = __ballot_sync(0xffffffffu, lane < 4 && mbar_test(look, parity));
+            const uint32_t m = __ballot_sync(0xffffffffu, lane < 4 && eye.ready());
             const bool out = np < ns && (m & 3u) == 3u;
             if (ns == seg_end && !last && (m & 8u) != 0u) {  // the next segment's queries are there
                 const volatile Seg *sg = reinterpret_cast<const volatile Seg *>(smem + L.seg) + seg % kSegs;
@@ -162,48 +162,48 @@ __global__ void __launch_bounds__(32 * kFirstSoft + 128 * groups_of(R), 1)
                 seg_end += count;
                 last = __any_sync(0xffffffffu, count == 0);
                 seg++;
+                if (lane == 3) eye.next();
             }
             const bool scores = ns < seg_end && ns < np + kGroups && (m & 4u) != 0u;
             if (!out && !scores) {
-                if ((++rounds & 63u) == 0u && gave_up(idle, st, 0xb00u, abort_flag)) break;
+                if (__any_sync(0xffffffffu, expired(idle, 0xb00u, abort_flag))) break;
                 continue;
             }
             idle = 0;
             tc_fence_after();
             if (out) {
-                const uint64_t va = vd + (uint64_t)((uint32_t)V.s * kTile >> 4);
+                const uint64_t va = vd + (uint64_t)((uint32_t)vs * kTile >> 4);
                 const uint64_t pb = pd + (uint64_t)((uint32_t)wp * (2u * kPBytes) >> 4);
 #pragma unroll
                 for (int k = 0; k < kTokens / 32; k++)
                     tc_mma_f8(tmem_o + (uint32_t)(wp * 2 * R), va + (uint64_t)(k * (32 * D) >> 4), pb + (uint64_t)(k * 32),
                               id_o, k > 0 ? 1u : 0u, elected);
-                tc_commit_elected(B.v_empty(V.s), elected);
+                tc_commit_elected(B.v_empty(vs), elected);
                 tc_commit_elected(B.o_full(wp), elected);
-                V.next(a.nv);
+                if (++vs == a.nv) vs = 0;
+                if (++wp == kGroups) wp = 0;
                 np++;
-                if (++wp == kGroups) {
-                    wp = 0;
-                    pp ^= 1u;
-                }
+                if (lane < 2) eye.next();
             }
             if (scores) {
-                const uint64_t ka = kd + (uint64_t)((uint32_t)K.s * kTile >> 4);
+                const uint64_t ka = kd + (uint64_t)((uint32_t)ks * kTile >> 4);
                 const uint64_t qa = qd + (uint64_t)((uint32_t)qb * (2u * R * D) >> 4);
 #pragma unroll
                 for (int k = 0; k < D / 32; k++)
                     tc_mma_f8(tmem + (uint32_t)(ws * 2 * R), ka + (uint64_t)(2 * k), qa + (uint64_t)(2 * k), id_s,
                               k > 0 ? 1u : 0u, elected);
-                tc_commit_elected(B.k_empty(K.s), elected);
+                tc_commit_elected(B.k_empty(ks), elected);
                 tc_commit_elected(B.s_full(ws), elected);
-                K.next(a.nk);
-                ns++;
+                if (++ks == a.nk) ks = 0;
                 if (++ws == kGroups) ws = 0;
+                ns++;
+                if (lane == 2) eye.next();
             }
         }
         // every MMA has finished before TMEM is released
         if (elect_one()) tc_commit(B.mma_done());
         __syncwarp();
-        if (lane == 0) mbar_wait(B.mma_done(), 0u, st, 0xb30u);
+        if (lane == 0) drain(B.mma_done(), 0u, abort_flag);
         __syncwarp();
     } else if (warp < kFirstSoft) {
         query_role<D, R>(a, smem, L, B, S, plan, abort_flag);
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(32 * kFirstSoft + 128 * groups_of(R), 1)
         int done = 0, mine = 0;  // tiles of earlier segments; tiles this warpgroup has taken
         int shared = 0;          // units shared with other CTAs
         // the first segment's data is there (one thread decides for all: see below)
-        if (stid == 0) *go = mbar_wait_or_abort(B.q_full(0), 0u, st, 0xc30u, abort_flag) ? 1 : 0;
+        if (stid == 0) *go = lane_wait(B.q_full(0), 0u, 0xc30u, abort_flag) ? 1 : 0;
         named_barrier(kBarAll, kSoft);
 
 #pragma unroll 1
@@ -236,7 +236,7 @@ __global__ void __launch_bounds__(32 * kFirstSoft + 128 * groups_of(R), 1)
             // after an abort the segment's description may be missing: all leave together
             if (*(volatile int *)go == 0) break;
             const int buf = seg & 1;
-            soft_wait(B.q_full(buf), (uint32_t)(seg >> 1) & 1u, st, 0xc31u, abort_flag);
+            soft_wait(B.q_full(buf), (uint32_t)(seg >> 1) & 1u, 0xc31u, abort_flag);
             const Seg *sg = reinterpret_cast<const Seg *>(smem + L.seg) + seg % kSegs;
             const RowInfo *rows = reinterpret_cast<const RowInfo *>(smem + L.rows) + buf * R;
             const int count = sg->count, tile0 = sg->tile0, see_all = sg->see_all, see_max = sg->see_max;
@@ -250,7 +250,7 @@ __global__ void __launch_bounds__(32 * kFirstSoft + 128 * groups_of(R), 1)
 
             // Add O^T of the outstanding tile to the running output.
             auto join_tile = [&]() {
-                soft_wait(B.o_full(wg), (uint32_t)(mine - 1) & 1u, st, 0xc20u + wg, abort_flag);
+                soft_wait(B.o_full(wg), (uint32_t)(mine - 1) & 1u, 0xc20u + wg, abort_flag);
                 tc_fence_after();
                 // (16 rows at a time: the first parts' product, then the second parts')
 #pragma unroll
@@ -292,7 +292,7 @@ __global__ void __launch_bounds__(32 * kFirstSoft + 128 * groups_of(R), 1)
                 const int u = done + t;              // tile of the share
                 const int vs_ = u % a.nv;
                 const int tk = (tile0 + t) * kTokens + tok;
-                soft_wait(B.s_full(wg), (uint32_t)mine & 1u, st, 0xc00u + wg, abort_flag);
+                soft_wait(B.s_full(wg), (uint32_t)mine & 1u, 0xc00u + wg, abort_flag);
                 tc_fence_after();
                 // scores with the queries' first parts, then with their second parts
                 float x[R], x2[R];
@@ -301,7 +301,7 @@ __global__ void __launch_bounds__(32 * kFirstSoft + 128 * groups_of(R), 1)
                     tmem_ld8(tmem + (uint32_t)(wg * 2 * R + i) + lanes, x + i);
                     tmem_ld8(tmem + (uint32_t)(wg * 2 * R + R + i) + lanes, x2 + i);
                 }
-                soft_wait(B.v_full(vs_), (uint32_t)(u / a.nv) & 1u, st, 0xc10u + vs_, abort_flag);
+                soft_wait(B.v_full(vs_), (uint32_t)(u / a.nv) & 1u, 0xc10u + vs_, abort_flag);
                 const float *sc = scales + vs_ * 2 * kMaxSlots;
                 const float ks = sc[tok >> page_shift] * a.scale2;
                 // value scales relative to the tile's largest (finite) one
@@ -416,16 +416,19 @@ __global__ void __launch_bounds__(32 * kFirstSoft + 128 * groups_of(R), 1)
                     for (int i = 0; i < R; i++) o[i] += merge[i * D + dcol];
                 }
             }
-            if (wg == 0 && dlive && *(volatile int *)abort_flag == 0) {
+            if (wg == 0 && dlive) {
 #pragma unroll
+                for (int i = 0; i < R; i++) merge[i * D + dcol] = o[i];  // (this thread's own places)
+#pragma unroll 1
                 for (int i = 0; i < R; i++) {
                     const RowInfo ri = rows[i];
-                    if (ri.row < 0) continue;
+                    if (ri.row < 0 || *(volatile int *)abort_flag != 0) continue;
+                    const float y = merge[i * D + dcol];
                     if (part != nullptr)
-                        part[(size_t)i * D + dcol] = o[i];
+                        part[(size_t)i * D + dcol] = y;
                     else
                         a.k.out[(size_t)ri.row * a.k.ldo + (size_t)ri.head * D + dcol] =
-                            __bfloat16_as_ushort(__float2bfloat16(o[i] * ab[i].y));
+                            __bfloat16_as_ushort(__float2bfloat16(y * ab[i].y));
                 }
             }
             if (part != nullptr) {
@@ -439,13 +442,14 @@ __global__ void __launch_bounds__(32 * kFirstSoft + 128 * groups_of(R), 1)
                 mbar_arrive(B.seg_empty(seg % kSegs));
             }
             if (stid == 0)
-                *go = mbar_wait_or_abort(B.q_full(buf ^ 1), (uint32_t)((seg + 1) >> 1) & 1u, st, 0xc32u, abort_flag) ? 1 : 0;
+                *go = lane_wait(B.q_full(buf ^ 1), (uint32_t)((seg + 1) >> 1) & 1u, 0xc32u, abort_flag) ? 1 : 0;
             named_barrier(kBarAll, kSoft);  // the merged values are read
         }
         join_role<D, kSoft>(a, S, reinterpret_cast<const Seg *>(smem + L.split), shared, kBarAll, abort_flag);
     }
     __syncthreads();
     tc_fence_after();
+    if (tid == 0 && *abort_flag != 0) set_status(st, MOE_ERR_TIMEOUT, (unsigned)*abort_flag);
     if (warp == 1) tmem_dealloc(tmem, kTmemCols);
 }
 

@@ -312,47 +312,69 @@ __device__ __forceinline__ bool mbar_test(uint64_t *bar, uint32_t parity) {
     return ok != 0;
 }
 
-// Whether a wait has gone on for too long (t0: its start, 0 before the first call) or another
-// role has given up; lane 0 of the converged warp records a timeout.
-__device__ __noinline__ bool gave_up(uint64_t &t0, StatusWord *st, unsigned where, int *abort_flag) {
+// Waits.  A wait that outlasts the limit writes `where` (not 0) to *abort_flag and gives up, as
+// does every other wait of the CTA once the flag is set; the CTA reports it at its end.  All
+// roles share one instruction cache and the kernel feels it when their loops do not fit, so
+// these are kept short.
+__device__ __forceinline__ bool expired(uint64_t &t0, unsigned where, int *abort_flag) {
+    if (*(const volatile int *)abort_flag != 0) return true;
     const uint64_t now = global_timer_ns();
     if (t0 == 0) t0 = now;
-    if (__any_sync(0xffffffffu, now - t0 > g_wait_limit_ns)) {
-        if ((threadIdx.x & 31) == 0) {
-            set_status(st, MOE_ERR_TIMEOUT, where);
-            *abort_flag = 1;
-        }
-        __syncwarp();
-        return true;
-    }
-    return __any_sync(0xffffffffu, *(const volatile int *)abort_flag != 0);
-}
-
-// A wait of a whole converged warp.  False after an abort or timeout.  The vote makes the
-// outcome uniform, so that what follows (descriptors, copies, MMAs) stays in uniform registers.
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, StatusWord *st, unsigned where,
-                                          int *abort_flag) {
-    uint64_t t0 = 0;
-    for (uint32_t i = 1; !__all_sync(0xffffffffu, mbar_try_wait(bar, parity)); i++)
-        if ((i & 31u) == 0u && gave_up(t0, st, where, abort_flag)) return false;
+    if (now - t0 <= g_wait_limit_ns) return false;
+    *(volatile int *)abort_flag = (int)where;
     return true;
 }
 
-// The slow paths stay out of line: all roles of a CTA share one instruction cache, and the
-// kernel is bound by it as soon as their loops do not fit (measured with the waits inlined: 84%
-// of the fetches hit, and fetching was the largest stall).
-__device__ __noinline__ void soft_wait_slow(uint64_t *bar, uint32_t parity, StatusWord *st, unsigned where,
-                                            int *abort_flag) {
-    if (!mbar_wait_or_abort(bar, parity, st, where, abort_flag)) *abort_flag = 1;
+// A wait of a whole converged warp.  False after an abort or timeout.  The votes make the
+// outcome uniform, so that what follows (descriptors, copies, MMAs) stays in uniform registers.
+__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsigned where, int *abort_flag) {
+    uint64_t t0 = 0;
+    while (!__all_sync(0xffffffffu, mbar_try_wait(bar, parity)))
+        if (__any_sync(0xffffffffu, expired(t0, where, abort_flag))) return false;
+    return true;
 }
 
 // A wait in the softmax warps, whose warpgroup barriers must match: after an abort nothing
 // waits, and the code runs on to its end.
-__device__ __forceinline__ void soft_wait(uint64_t *bar, uint32_t parity, StatusWord *st, unsigned where,
-                                          int *abort_flag) {
-    if (!mbar_try_wait(bar, parity)) soft_wait_slow(bar, parity, st, where, abort_flag);
+__device__ __forceinline__ void soft_wait(uint64_t *bar, uint32_t parity, unsigned where, int *abort_flag) {
+    uint64_t t0 = 0;
+    while (!mbar_try_wait(bar, parity))
+        if (expired(t0, where, abort_flag)) break;
     __syncwarp();
 }
+
+// One thread's wait; false after an abort or timeout.
+__device__ __forceinline__ bool lane_wait(uint64_t *bar, uint32_t parity, unsigned where, int *abort_flag) {
+    uint64_t t0 = 0;
+    while (!mbar_try_wait(bar, parity))
+        if (expired(t0, where, abort_flag)) return false;
+    return true;
+}
+
+// Wait for copies or MMAs in flight, before the CTA exits, even after an abort (within the limit).
+__device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity, int *abort_flag) {
+    const uint64_t t0 = global_timer_ns();
+    while (!mbar_try_wait(bar, parity)) {
+        if (global_timer_ns() - t0 > g_wait_limit_ns) {
+            *(volatile int *)abort_flag = 0xfff;
+            break;
+        }
+    }
+}
+
+// What one lane of the MMA warp watches: a ring of barriers.
+struct Watch {
+    uint64_t *base;
+    int n, i;
+    uint32_t parity;
+    __device__ __forceinline__ bool ready() const { return mbar_test(base + i, parity); }
+    __device__ __forceinline__ void next() {
+        if (++i == n) {
+            i = 0;
+            parity ^= 1u;
+        }
+    }
+};
 
 // Shared memory that both forms have, in bytes.
 struct CommonSmem {
@@ -421,7 +443,7 @@ __device__ __forceinline__ void copy_pages(const AttnArgs &a, const CUtensorMap 
 #pragma unroll 1
     for (int seg = 0; run; seg++) {
         const int ss = seg % kSegs;
-        if (!warp_wait(B.seg_full(ss), (uint32_t)(seg / kSegs) & 1u, st, 0xa60u + SIDE, abort_flag)) break;
+        if (!warp_wait(B.seg_full(ss), (uint32_t)(seg / kSegs) & 1u, 0xa60u + SIDE, abort_flag)) break;
         const Seg *sg = reinterpret_cast<const Seg *>(smem + L.seg) + ss;
         const int count = sg->count;
         if (count == 0) break;
@@ -446,8 +468,7 @@ __device__ __forceinline__ void copy_pages(const AttnArgs &a, const CUtensorMap 
 #pragma unroll 1
         for (int t = 0; t < count; t++) {
             uint64_t *full = SIDE ? B.v_full(R.s) : B.k_full(R.s);
-            if (!(run = warp_wait(SIDE ? B.v_empty(R.s) : B.k_empty(R.s), R.ph ^ 1u, st, 0xa00u + 16 * SIDE + R.s,
-                                  abort_flag)))
+            if (!(run = warp_wait(SIDE ? B.v_empty(R.s) : B.k_empty(R.s), R.ph ^ 1u, 0xa00u + 16 * SIDE + R.s, abort_flag)))
                 break;
             unsigned char *dst = ring + (uint32_t)R.s * kTile;
             if (left >= kSlots) {
@@ -488,7 +509,7 @@ __device__ __forceinline__ void copy_pages(const AttnArgs &a, const CUtensorMap 
     // nothing may be in flight when the CTA exits
     if (lane == 0) {
         for (int i = max(0, issued - n); i < issued; i++)
-            mbar_wait(SIDE ? B.v_full(i % n) : B.k_full(i % n), (uint32_t)(i / n) & 1u, st, 0xa40u);
+            drain(SIDE ? B.v_full(i % n) : B.k_full(i % n), (uint32_t)(i / n) & 1u, abort_flag);
     }
     __syncwarp();
 }
@@ -529,7 +550,7 @@ __device__ __forceinline__ void query_role(const AttnArgs &a, unsigned char *sme
             const uint32_t parity = ((uint32_t)(published / kSegs) & 1u) ^ 1u;
             if (published > seg + 1) {
                 if (!__all_sync(0xffffffffu, mbar_test(B.seg_empty(ss), parity))) break;
-            } else if (!warp_wait(B.seg_empty(ss), parity, a.k.st, 0xe10u, abort_flag)) {
+            } else if (!warp_wait(B.seg_empty(ss), parity, 0xe10u, abort_flag)) {
                 return;
             }
             Seg g;
@@ -581,7 +602,7 @@ __device__ __forceinline__ void query_role(const AttnArgs &a, unsigned char *sme
             published++;
         }
         const int buf = seg & 1;
-        if (!warp_wait(B.q_empty(buf), ((uint32_t)(seg >> 1) & 1u) ^ 1u, a.k.st, 0xe00u + buf, abort_flag)) return;
+        if (!warp_wait(B.q_empty(buf), ((uint32_t)(seg >> 1) & 1u) ^ 1u, 0xe00u + buf, abort_flag)) return;
         const Seg *sg = ring + seg % kSegs;
         RowInfo *rows = reinterpret_cast<RowInfo *>(smem + L.rows) + buf * R;
         unsigned char *q0 = smem + L.q + (uint32_t)buf * (2u * R * D);
@@ -663,7 +684,7 @@ __device__ __forceinline__ void query_role(const AttnArgs &a, unsigned char *sme
 // row sees hold anything and become zero; NaN in rows that only some rows see must not reach
 // the others, so it becomes zero here and is put back in the outputs (the returned truth).
 template <int D>
-__device__ __noinline__ bool clean_values(unsigned char *tile, int tok, int t, int see_all, int see_max) {
+__device__ __forceinline__ bool clean_values(unsigned char *tile, int tok, int t, int see_all, int see_max) {
     bool bad = false;
     if (t < see_all) return false;
 #pragma unroll 1
@@ -687,7 +708,7 @@ __device__ __noinline__ bool clean_values(unsigned char *tile, int tok, int t, i
 }
 
 // Code of value d of token t as it lies in the cache (0 if its page is outside).
-__device__ __noinline__ const uint8_t *value_codes(const AttnArgs &a, int b, int head, int t) {
+__device__ __forceinline__ const uint8_t *value_codes(const AttnArgs &a, int b, int head, int t) {
     const int P = a.k.kv.page;
     const int page = a.k.page_table[(size_t)b * a.k.table_width + t / P];
     if (page < 0 || page >= a.k.kv.n_pages) return nullptr;
@@ -713,8 +734,7 @@ __device__ __forceinline__ void join_role(const AttnArgs &a, const Share &S, con
             const uint64_t t0 = global_timer_ns(), lim = g_wait_limit_ns;
             while (ld_acquire_gpu(arrive) < (unsigned)S.ctas) {
                 if (global_timer_ns() - t0 > lim) {
-                    set_status(st, MOE_ERR_TIMEOUT, 0xd00u);
-                    *abort_flag = 1;
+                    *(volatile int *)abort_flag = 0xd00;
                     break;
                 }
             }

@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         const uint64_t kd = smem_desc(smem_u32(smem + L.k), 16, kGroup8, kSwz);
         const uint64_t vd = smem_desc(smem_u32(smem + L.v), kGroup8, kGroup8, kSwz);
         const uint64_t qd = smem_desc(smem_u32(smem + L.q), 16, kGroup8, kSwz);
-        Ring K, V;
+        int ks = 0, vs = 0;  // stages
         int ns = 0, np = 0, seg = 0, seg_end = 0, qb = 0;  // scores / outputs issued
         bool last = false;                                 // seg_end is the share's end
         const uint32_t elected = elect_one();
@@ -146,17 +146,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         // tile ns - 2, whose outputs have been issued; with the segment's queries).  Lanes 0 to 4
         // look at one barrier each; a vote makes the outcome uniform, which keeps the descriptors
         // in uniform registers.
+        Watch eye = lane == 0   ? Watch{B.p_ready(0), 2, 0, 0u}
+                    : lane == 1 ? Watch{B.v_full(0), a.nv, 0, 0u}
+                    : lane == 2 ? Watch{B.o_empty(0), 2, 0, 1u}
+                    : lane == 3 ? Watch{B.k_full(0), a.nk, 0, 0u}
+                                : Watch{B.q_full(0), 2, 0, 0u};
         uint64_t idle = 0;  // since when nothing has been ready
-        uint32_t rounds = 0;
         while (!(last && np == seg_end)) {
-            const uint32_t ph = (uint32_t)(np >> 1) & 1u;
-            uint64_t *look = lane == 0   ? B.p_ready(np & 1)
-                             : lane == 1 ? B.v_full(V.s)
-                             : lane == 2 ? B.o_empty(np & 1)
-                             : lane == 3 ? B.k_full(K.s)
-                                         : B.q_full(seg & 1);
-            const uint32_t parity = lane == 0 ? ph : lane == 1 ? V.ph : lane == 2 ? ph ^ 1u : lane == 3 ? K.ph : (uint32_t)(seg >> 1) & 1u;
-            const uint32_t m = __ballot_sync(0xffffffffu, lane < 5 && mbar_test(look, parity));
+            const uint32_t m = __ballot_sync(0xffffffffu, lane < 5 && eye.ready());
             const bool out = np < ns && (m & 7u) == 7u;
             if (ns == seg_end && !last && (m & 16u) != 0u) {  // the next segment's queries are there
                 const volatile Seg *sg = reinterpret_cast<const volatile Seg *>(smem + L.seg) + seg % kSegs;
@@ -165,17 +162,18 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                 seg_end += count;
                 last = __any_sync(0xffffffffu, count == 0);
                 seg++;
+                if (lane == 4) eye.next();
             }
             const bool scores = ns < seg_end && ns < np + (out ? 3 : 2) && (m & 8u) != 0u;
             if (!out && !scores) {
-                if ((++rounds & 63u) == 0u && gave_up(idle, st, 0xb00u, abort_flag)) break;
+                if (__any_sync(0xffffffffu, expired(idle, 0xb00u, abort_flag))) break;
                 continue;
             }
             idle = 0;
             tc_fence_after();
             if (out) {
                 const int buf = np & 1;
-                const uint64_t va = vd + (uint64_t)((uint32_t)V.s * kTile >> 4);
+                const uint64_t va = vd + (uint64_t)((uint32_t)vs * kTile >> 4);
                 const uint32_t p = tmem + (uint32_t)(buf * kTokens);
                 // 32 tokens take 8 columns per part: the parts of each 32 lie side by side
 #pragma unroll
@@ -184,13 +182,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                     for (int k = 0; k < kTokens / 32; k++)
                         tc_mma_f8_ts(tmem_o + (uint32_t)(buf * D), p + (uint32_t)(16 * k + 8 * part),
                                      va + (uint64_t)(k * (32 * D) >> 4), id_o, (part > 0 || k > 0) ? 1u : 0u, elected);
-                tc_commit_elected(B.v_empty(V.s), elected);
+                tc_commit_elected(B.v_empty(vs), elected);
                 tc_commit_elected(B.o_full(buf), elected);
-                V.next(a.nv);
+                if (++vs == a.nv) vs = 0;
                 np++;
+                if (lane < 3) eye.next();
             }
             if (scores) {
-                const uint64_t ka = kd + (uint64_t)((uint32_t)K.s * kTile >> 4);
+                const uint64_t ka = kd + (uint64_t)((uint32_t)ks * kTile >> 4);
                 const uint64_t qa = qd + (uint64_t)((uint32_t)qb * (2u * kRows * D) >> 4);
 #pragma unroll
                 for (int part = 0; part < 2; part++)
@@ -199,15 +198,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                         tc_mma_f8(tmem + (uint32_t)((ns & 1) * kTokens),
                                   qa + (uint64_t)(part * (kRows * D) >> 4) + (uint64_t)(2 * k), ka + (uint64_t)(2 * k),
                                   id_s, (part > 0 || k > 0) ? 1u : 0u, elected);
-                tc_commit_elected(B.k_empty(K.s), elected);
+                tc_commit_elected(B.k_empty(ks), elected);
                 tc_commit_elected(B.s_full(ns & 1), elected);
-                K.next(a.nk);
+                if (++ks == a.nk) ks = 0;
                 ns++;
+                if (lane == 3) eye.next();
             }
         }
         if (elect_one()) tc_commit(B.mma_done());
         __syncwarp();
-        if (lane == 0) mbar_wait(B.mma_done(), 0u, st, 0xb30u);
+        if (lane == 0) drain(B.mma_done(), 0u, abort_flag);
         __syncwarp();
     } else if (warp < kFirstSoft) {
         query_role<D, kRows>(a, smem, L, B, S, plan, abort_flag);
@@ -226,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         float o[DH];
         int done = 0;  // tiles of earlier segments
         int shared = 0;  // units shared with other CTAs
-        if (stid == 0) *go = mbar_wait_or_abort(B.q_full(0), 0u, st, 0xc30u, abort_flag) ? 1 : 0;
+        if (stid == 0) *go = lane_wait(B.q_full(0), 0u, 0xc30u, abort_flag) ? 1 : 0;
         named_barrier(kBarAll, kSoft);
 
 #pragma unroll 1
@@ -234,7 +234,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             // after an abort the segment's description may be missing: all leave together
             if (*(volatile int *)go == 0) break;
             const int buf = seg & 1;
-            soft_wait(B.q_full(buf), (uint32_t)(seg >> 1) & 1u, st, 0xc31u, abort_flag);
+            soft_wait(B.q_full(buf), (uint32_t)(seg >> 1) & 1u, 0xc31u, abort_flag);
             const Seg *sg = reinterpret_cast<const Seg *>(smem + L.seg) + seg % kSegs;
             const RowInfo ri = reinterpret_cast<const RowInfo *>(smem + L.rows)[buf * kRows + row];
             const int count = sg->count, tile0 = sg->tile0, see_all = sg->see_all, see_max = sg->see_max;
@@ -246,7 +246,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             // Scores of tile t of the segment -> weights; its reference and sum.
             auto softmax = [&](int t) {
                 const int u = done + t, sb = u & 1, vb = u % a.nv;
-                soft_wait(B.v_full(vb), (uint32_t)(u / a.nv) & 1u, st, 0xc10u + vb, abort_flag);
+                soft_wait(B.v_full(vb), (uint32_t)(u / a.nv) & 1u, 0xc10u + vb, abort_flag);
                 // constants of the tile's pages: lane j has page j
                 {
                     const float *sc = scales + vb * 2 * kMaxSlots;
@@ -271,7 +271,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                     fence_proxy_async_smem();
                 }
                 if (lane == 0) nan[(u & 3) * 4 + ew] = word;
-                soft_wait(B.s_full(sb), (uint32_t)(u >> 1) & 1u, st, 0xc00u + sb, abort_flag);
+                soft_wait(B.s_full(sb), (uint32_t)(u >> 1) & 1u, 0xc00u + sb, abort_flag);
                 tc_fence_after();
                 const uint32_t ts = tmem + (uint32_t)(sb * kTokens) + lanes;
                 // loops over 32 tokens are not unrolled: the body must stay in the instruction cache
@@ -353,7 +353,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             // Add this warpgroup's columns of tile t's output to the running output.
             auto join_tile = [&](int t) {
                 const int u = done + t, ob = u & 1;
-                soft_wait(B.o_full(ob), (uint32_t)(u >> 1) & 1u, st, 0xc20u + ob, abort_flag);
+                soft_wait(B.o_full(ob), (uint32_t)(u >> 1) & 1u, 0xc20u + ob, abort_flag);
                 tc_fence_after();
                 float y[DH];
 #pragma unroll
@@ -437,13 +437,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             }
             named_barrier(kBarAll, kSoft);  // nobody still reads the last decision
             if (stid == 0)
-                *go = mbar_wait_or_abort(B.q_full(buf ^ 1), (uint32_t)((seg + 1) >> 1) & 1u, st, 0xc32u, abort_flag) ? 1 : 0;
+                *go = lane_wait(B.q_full(buf ^ 1), (uint32_t)((seg + 1) >> 1) & 1u, 0xc32u, abort_flag) ? 1 : 0;
             named_barrier(kBarAll, kSoft);
         }
         join_role<D, kSoft>(a, S, reinterpret_cast<const Seg *>(smem + L.split), shared, kBarAll, abort_flag);
     }
     __syncthreads();
     tc_fence_after();
+    if (tid == 0 && *abort_flag != 0) set_status(st, MOE_ERR_TIMEOUT, (unsigned)*abort_flag);
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
