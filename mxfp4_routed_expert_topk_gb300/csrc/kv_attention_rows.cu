@@ -8,11 +8,13 @@
 // their value scales are constants of a run of 16 tokens and go into the exponent's multiply-
 // add.  Weights replace the scores they came from in TMEM.
 //
-// What bounds it is instruction issue: 128 x 128 scores a tile at 7 to 8 instructions each are
-// about 1000 clocks of all four schedulers, next to 1400 that the tile's 32 KB take from HBM
-// and 1024 of the tensor pipe.  Two warpgroups take tiles in turn (a thread per row); the
-// joining of a tile's output is shared by columns, half of them in each warpgroup, so a thread
-// keeps 64 running outputs; each tile's reference and sum pass through shared memory.
+// What bounds it is instruction issue and latency: 128 x 128 scores a tile at 7 to 8
+// instructions each are about 1000 clocks of all four schedulers, next to 1400 that the tile's
+// 32 KB take from HBM and 1024 of the tensor pipe.  So the work is split by role: softmax
+// warpgroups take tiles in turn (a thread per row) over three score buffers, so that the next
+// scores are ready when a warpgroup comes for them, and one more warpgroup joins each tile's
+// output with the running one as soon as it is there, which frees the single output buffer.
+// Registers go to the warpgroups by need (setmaxnreg).
 #include <algorithm>
 
 #include "kv_attention.cuh"
@@ -20,9 +22,16 @@
 namespace moe {
 namespace {
 
-constexpr int kSoft = 256;
+constexpr int kGroups = 2;                     // softmax warpgroups
+constexpr int kSBufs = 3;                      // score buffers
+constexpr int kJoinWarp = kFirstSoft + 4 * kGroups;
+constexpr int kSoft = 128 * kGroups + 128;     // with the joining warpgroup
 constexpr int kThreads = 32 * kFirstSoft + kSoft;
 constexpr int kRows = 128;
+// Registers of a thread: at launch, then by role; the sum over the warpgroups is no more than
+// what the launch allocated (512 x 128).
+constexpr int kRegsIssue = 96, kRegsSoft = 112, kRegsJoin = 192;
+static_assert(kRegsIssue + kGroups * kRegsSoft + kRegsJoin <= 4 * 128 && kThreads == 512, "register split");
 constexpr int kBarAll = 7;
 
 struct RowsSmem {
@@ -34,7 +43,7 @@ struct RowsSmem {
         fac = o;   o += 4u * 4u;                 // [4 tiles] value of a weight unit
         nan = o;   o += 4u * 4u * 4u;            // [4 tiles][warp] tokens whose values hold partial NaN
         o = (o + 15u) & ~15u;
-        chunk = o; o += 8u * kMaxSlots * 16u;    // [warp][page] (key scale, log2 weight scale, 1 / weight scale)
+        chunk = o; o += 4u * kGroups * kMaxSlots * 16u;    // [warp][page] (key scale, log2 weight scale, 1 / weight scale)
         total = o;
     }
 };
@@ -63,15 +72,22 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
     return r;
 }
 
-// A pair of weights as E4M3 parts: first = the value to 4 significant bits (Veltkamp's
-// splitting: x * (2^20 + 1) minus its difference from x), second = what is left.
+// A pair of weights as E4M3 parts: the value to 4 significant bits, and what is left.
 __device__ __forceinline__ void split2(uint64_t x, float &h0, float &h1, float &l0, float &l1) {
-    const uint64_t c = pack2(1048577.f, 1048577.f), neg = pack2(-1.f, -1.f);
-    const uint64_t t = mul2(x, c);
-    const uint64_t d = fma2(x, neg, t);    // t - x
-    const uint64_t h = fma2(d, neg, t);    // t - (t - x)
-    unpack2(h, h0, h1);
-    unpack2(fma2(h, neg, x), l0, l1);
+    float x0, x1;
+    unpack2(x, x0, x1);
+    h0 = part_hi(x0);
+    h1 = part_hi(x1);
+    unpack2(fma2(pack2(h0, h1), pack2(-1.f, -1.f), x), l0, l1);
+}
+
+template <int N>
+__device__ __forceinline__ void regs_inc() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void regs_dec() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
 template <int D>
@@ -80,7 +96,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
     constexpr uint32_t kTile = kTokens * D;
     constexpr uint32_t kSwz = D == 128 ? kSwizzle128B : kSwizzle64B;
     constexpr uint32_t kGroup8 = 8 * D;
-    constexpr int DH = D / 2;  // columns of the output that a warpgroup joins
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = (unsigned char *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
     const RowsSmem F(D, a.nk, a.nv);
@@ -89,7 +104,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + L.misc);
     uint32_t *tmem_slot = misc;
     int *abort_flag = reinterpret_cast<int *>(misc + 1);
-    int *go = reinterpret_cast<int *>(misc + 2);
+    int *n_shared = reinterpret_cast<int *>(misc + 2);
     int64_t *plan = reinterpret_cast<int64_t *>(misc + 8);
     StatusWord *st = a.k.st;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
@@ -108,26 +123,31 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         for (int b = 0; b < 2; b++) {
             mbar_init(B.q_full(b), 1);
             mbar_init(B.q_empty(b), kSoft / 32);
+        }
+        for (int b = 0; b < kSBufs; b++) {
             mbar_init(B.s_full(b), 1);
             mbar_init(B.p_ready(b), 4);
-            mbar_init(B.o_full(b), 1);
-            mbar_init(B.o_empty(b), kSoft / 32);
         }
+        mbar_init(B.o_full(0), 1);
+        mbar_init(B.o_empty(0), 4);
         for (int b = 0; b < kSegs; b++) {
             mbar_init(B.seg_full(b), 1);
             mbar_init(B.seg_empty(b), 2 + kSoft / 32);  // the copying warps, and the softmax
         }
         mbar_init(B.mma_done(), 1);
         *abort_flag = 0;
+        *n_shared = 0;
         fence_mbar_init();
     }
     if (warp == 1) tmem_alloc(tmem_slot, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = *tmem_slot;        // scores, then weights: two buffers of 128 columns
-    const uint32_t tmem_o = tmem + 2 * kTokens;
+    const uint32_t tmem = *tmem_slot;        // scores, then weights: buffers of 128 columns
+    const uint32_t tmem_o = tmem + kSBufs * kTokens;
 
+    if (warp < kFirstSoft) {
+        regs_dec<kRegsIssue>();
     if (warp == 0) {
         copy_role<D, 0>(a, &tm, smem, L, B, abort_flag);
     } else if (warp == 2) {
@@ -140,15 +160,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         const uint64_t qd = smem_desc(smem_u32(smem + L.q), 16, kGroup8, kSwz);
         int ks = 0, vs = 0;  // stages
         int ns = 0, np = 0, seg = 0, seg_end = 0, qb = 0;  // scores / outputs issued
+        int bs = 0, bp = 0;                                // and their buffers
         bool last = false;                                 // seg_end is the share's end
         const uint32_t elected = elect_one();
         // Whichever is ready: the outputs of tile np, the scores of tile ns (over the weights of
-        // tile ns - 2, whose outputs have been issued; with the segment's queries).  Lanes 0 to 4
+        // tile ns - 3, whose outputs have been issued; with the segment's queries).  Lanes 0 to 4
         // look at one barrier each; a vote makes the outcome uniform, which keeps the descriptors
         // in uniform registers.
-        Watch eye = lane == 0   ? Watch{B.p_ready(0), 2, 0, 0u}
+        Watch eye = lane == 0   ? Watch{B.p_ready(0), kSBufs, 0, 0u}
                     : lane == 1 ? Watch{B.v_full(0), a.nv, 0, 0u}
-                    : lane == 2 ? Watch{B.o_empty(0), 2, 0, 1u}
+                    : lane == 2 ? Watch{B.o_empty(0), 1, 0, 1u}
                     : lane == 3 ? Watch{B.k_full(0), a.nk, 0, 0u}
                                 : Watch{B.q_full(0), 2, 0, 0u};
         uint64_t idle = 0;  // since when nothing has been ready
@@ -164,7 +185,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                 seg++;
                 if (lane == 4) eye.next();
             }
-            const bool scores = ns < seg_end && ns < np + (out ? 3 : 2) && (m & 8u) != 0u;
+            const bool scores = ns < seg_end && ns < np + (out ? 1 : 0) + kSBufs && (m & 8u) != 0u;
             if (!out && !scores) {
                 if (__any_sync(0xffffffffu, expired(idle, 0xb00u, abort_flag))) break;
                 continue;
@@ -172,19 +193,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             idle = 0;
             tc_fence_after();
             if (out) {
-                const int buf = np & 1;
                 const uint64_t va = vd + (uint64_t)((uint32_t)vs * kTile >> 4);
-                const uint32_t p = tmem + (uint32_t)(buf * kTokens);
+                const uint32_t p = tmem + (uint32_t)(bp * kTokens);
                 // 32 tokens take 8 columns per part: the parts of each 32 lie side by side
 #pragma unroll
                 for (int part = 0; part < 2; part++)
 #pragma unroll
                     for (int k = 0; k < kTokens / 32; k++)
-                        tc_mma_f8_ts(tmem_o + (uint32_t)(buf * D), p + (uint32_t)(16 * k + 8 * part),
+                        tc_mma_f8_ts(tmem_o, p + (uint32_t)(16 * k + 8 * part),
                                      va + (uint64_t)(k * (32 * D) >> 4), id_o, (part > 0 || k > 0) ? 1u : 0u, elected);
                 tc_commit_elected(B.v_empty(vs), elected);
-                tc_commit_elected(B.o_full(buf), elected);
+                tc_commit_elected(B.o_full(0), elected);
                 if (++vs == a.nv) vs = 0;
+                if (++bp == kSBufs) bp = 0;
                 np++;
                 if (lane < 3) eye.next();
             }
@@ -195,12 +216,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                 for (int part = 0; part < 2; part++)
 #pragma unroll
                     for (int k = 0; k < D / 32; k++)
-                        tc_mma_f8(tmem + (uint32_t)((ns & 1) * kTokens),
+                        tc_mma_f8(tmem + (uint32_t)(bs * kTokens),
                                   qa + (uint64_t)(part * (kRows * D) >> 4) + (uint64_t)(2 * k), ka + (uint64_t)(2 * k),
                                   id_s, (part > 0 || k > 0) ? 1u : 0u, elected);
                 tc_commit_elected(B.k_empty(ks), elected);
-                tc_commit_elected(B.s_full(ns & 1), elected);
+                tc_commit_elected(B.s_full(bs), elected);
                 if (++ks == a.nk) ks = 0;
+                if (++bs == kSBufs) bs = 0;
                 ns++;
                 if (lane == 3) eye.next();
             }
@@ -209,11 +231,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         __syncwarp();
         if (lane == 0) drain(B.mma_done(), 0u, abort_flag);
         __syncwarp();
-    } else if (warp < kFirstSoft) {
-        query_role<D, kRows>(a, smem, L, B, S, plan, abort_flag);
     } else {
+        query_role<D, kRows>(a, smem, L, B, S, plan, abort_flag);
+    }
+    } else if (warp < kJoinWarp) {
+        regs_dec<kRegsSoft>();
         // -------------------------------------------------------- softmax
-        const int sw = warp - kFirstSoft, wg = sw >> 2, ew = sw & 3, stid = tid - 32 * kFirstSoft;
+        const int sw = warp - kFirstSoft, wg = sw >> 2, ew = sw & 3;
         const int row = 32 * ew + lane;  // row of the tile (TMEM lane); also the token it cleans
         const uint32_t lanes = (uint32_t)(32 * ew) << 16;
         float2 *ml = reinterpret_cast<float2 *>(smem + F.ml);
@@ -222,30 +246,22 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         float4 *chunk = reinterpret_cast<float4 *>(smem + F.chunk) + sw * kMaxSlots;
         const float *scales = reinterpret_cast<const float *>(smem + L.scales);
         const int page_shift = 31 - __clz(a.k.kv.page), slots = kTokens >> page_shift;
-        const size_t slot_floats = (size_t)a.rpt * D + 2 * a.rpt;
-        float o[DH];
         int done = 0;  // tiles of earlier segments
-        int shared = 0;  // units shared with other CTAs
-        if (stid == 0) *go = lane_wait(B.q_full(0), 0u, 0xc30u, abort_flag) ? 1 : 0;
-        named_barrier(kBarAll, kSoft);
 
 #pragma unroll 1
         for (int seg = 0;; seg++) {
-            // after an abort the segment's description may be missing: all leave together
-            if (*(volatile int *)go == 0) break;
             const int buf = seg & 1;
-            soft_wait(B.q_full(buf), (uint32_t)(seg >> 1) & 1u, 0xc31u, abort_flag);
+            // (no barrier stands between these warps: after an abort each leaves by itself)
+            if (!warp_wait(B.q_full(buf), (uint32_t)(seg >> 1) & 1u, 0xc31u, abort_flag)) break;
             const Seg *sg = reinterpret_cast<const Seg *>(smem + L.seg) + seg % kSegs;
             const RowInfo ri = reinterpret_cast<const RowInfo *>(smem + L.rows)[buf * kRows + row];
             const int count = sg->count, tile0 = sg->tile0, see_all = sg->see_all, see_max = sg->see_max;
             if (count == 0) break;
-            float m_run = -INFINITY, l_run = 0.f;
-#pragma unroll
-            for (int i = 0; i < DH; i++) o[i] = 0.f;
 
-            // Scores of tile t of the segment -> weights; its reference and sum.
-            auto softmax = [&](int t) {
-                const int u = done + t, sb = u & 1, vb = u % a.nv;
+            // scores of tile t of the segment -> weights; its reference and sum
+#pragma unroll 1
+            for (int t = (wg + kGroups - done % kGroups) % kGroups; t < count; t += kGroups) {
+                const int u = done + t, sb = u % kSBufs, vb = u % a.nv;
                 soft_wait(B.v_full(vb), (uint32_t)(u / a.nv) & 1u, 0xc10u + vb, abort_flag);
                 // constants of the tile's pages: lane j has page j
                 {
@@ -271,7 +287,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                     fence_proxy_async_smem();
                 }
                 if (lane == 0) nan[(u & 3) * 4 + ew] = word;
-                soft_wait(B.s_full(sb), (uint32_t)(u >> 1) & 1u, 0xc00u + sb, abort_flag);
+                soft_wait(B.s_full(sb), (uint32_t)(u / kSBufs) & 1u, 0xc00u + sb, abort_flag);
                 tc_fence_after();
                 const uint32_t ts = tmem + (uint32_t)(sb * kTokens) + lanes;
                 // loops over 32 tokens are not unrolled: the body must stay in the instruction cache
@@ -348,70 +364,98 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(B.p_ready(sb));
-            };
+            }
 
-            // Add this warpgroup's columns of tile t's output to the running output.
-            auto join_tile = [&](int t) {
-                const int u = done + t, ob = u & 1;
-                soft_wait(B.o_full(ob), (uint32_t)(u >> 1) & 1u, 0xc20u + ob, abort_flag);
-                tc_fence_after();
-                float y[DH];
+            done += count;
+            if (lane == 0) {
+                mbar_arrive(B.q_empty(buf));
+                mbar_arrive(B.seg_empty(seg % kSegs));
+            }
+        }
+    } else {
+        regs_inc<kRegsJoin>();
+        // ------------------------------------------------- joining of outputs
+        const int ew = warp & 3, row = 32 * ew + lane;
+        const uint32_t lanes = (uint32_t)(32 * ew) << 16;
+        const float2 *ml = reinterpret_cast<const float2 *>(smem + F.ml) + row;
+        const float *fac = reinterpret_cast<const float *>(smem + F.fac);
+        const uint32_t *nan = reinterpret_cast<const uint32_t *>(smem + F.nan);
+        const size_t slot_floats = (size_t)a.rpt * D + 2 * a.rpt;
+        float o[D];
+        int u = 0, shared = 0;  // tiles joined; units shared with other CTAs
+
+#pragma unroll 1
+        for (int seg = 0;; seg++) {
+            const int buf = seg & 1;
+            if (!warp_wait(B.q_full(buf), (uint32_t)(seg >> 1) & 1u, 0xc32u, abort_flag)) break;
+            const Seg *sg = reinterpret_cast<const Seg *>(smem + L.seg) + seg % kSegs;
+            const RowInfo ri = reinterpret_cast<const RowInfo *>(smem + L.rows)[buf * kRows + row];
+            const int count = sg->count, tile0 = sg->tile0;
+            if (count == 0) break;
+            float m_run = -INFINITY, l_run = 0.f;
 #pragma unroll
-                for (int i = 0; i < DH; i += 32) tmem_ld32(tmem_o + (uint32_t)(ob * D + wg * DH + i) + lanes, y + i);
-                const float2 v = ml[(u & 3) * kRows + row];
+            for (int i = 0; i < D; i++) o[i] = 0.f;
+#pragma unroll 1
+            for (int t = 0; t < count; t++, u++) {
+                soft_wait(B.o_full(0), (uint32_t)u & 1u, 0xc20u, abort_flag);
+                tc_fence_after();
+                const float2 v = ml[(u & 3) * kRows];
+                const uint4 nm = *reinterpret_cast<const uint4 *>(nan + (u & 3) * 4);
                 const float m = fmaxf(m_run, v.x);
                 const float f_old = m_run == -INFINITY ? 0.f : ex2(m_run - m), f_new = v.x == -INFINITY ? 0.f : ex2(v.x - m);
                 m_run = m;
                 l_run = fmaf(l_run, f_old, v.y * f_new);
                 const float g = f_new * fac[u & 3];
-                const uint64_t g2 = pack2(g, g), k2 = pack2(f_old, f_old);
+                const uint64_t g2 = pack2(g, g);
                 if (__any_sync(0xffffffffu, f_old != 1.f)) {  // some row's maximum has moved
+                    const uint64_t k2 = pack2(f_old, f_old);
 #pragma unroll
-                    for (int i = 0; i < DH; i += 2) unpack2(mul2(pack2(o[i], o[i + 1]), k2), o[i], o[i + 1]);
+                    for (int i = 0; i < D; i += 2) unpack2(mul2(pack2(o[i], o[i + 1]), k2), o[i], o[i + 1]);
                 }
-                tmem_ld_wait(y);
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(B.o_empty(ob));
 #pragma unroll
-                for (int i = 0; i < DH; i += 2)
-                    unpack2(fma2(pack2(y[i], y[i + 1]), g2, pack2(o[i], o[i + 1])), o[i], o[i + 1]);
+                for (int h = 0; h < D; h += 32) {
+                    float y[32];
+                    tmem_ld32(tmem_o + (uint32_t)h + lanes, y);
+                    tmem_ld_wait(y);
+                    if (h + 32 == D) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(B.o_empty(0));
+                    }
+#pragma unroll
+                    for (int i = 0; i < 32; i += 2)
+                        unpack2(fma2(pack2(y[i], y[i + 1]), g2, pack2(o[h + i], o[h + i + 1])), o[h + i], o[h + i + 1]);
+                }
                 // NaN values that only some rows see, back into those rows' outputs
+                if ((nm.x | nm.y | nm.z | nm.w) != 0u) {
 #pragma unroll 1
-                for (int w = 0; w < 4; w++) {
-                    for (uint32_t word = nan[(u & 3) * 4 + w]; word != 0u; word &= word - 1u) {
-                        const int tn = (tile0 + t) * kTokens + 32 * w + __ffs((int)word) - 1;
+                    for (int k = 0; k < kTokens; k++) {
+                        const uint32_t word = k < 32 ? nm.x : k < 64 ? nm.y : k < 96 ? nm.z : nm.w;
+                        const int tn = (tile0 + t) * kTokens + k;
+                        if (((word >> (k & 31)) & 1u) == 0u || tn > ri.pos) continue;
                         const uint8_t *code = value_codes(a, sg->b, sg->head, tn);
-                        if (code == nullptr || tn > ri.pos) continue;
+                        if (code == nullptr) continue;
 #pragma unroll
-                        for (int i = 0; i < DH; i++)
-                            if ((code[wg * DH + i] & 0x7fu) == 0x7fu) o[i] = kNan;
+                        for (int i = 0; i < D; i++)
+                            if ((code[i] & 0x7fu) == 0x7fu) o[i] = kNan;
                     }
                 }
-            };
-
-            int next = 0;
-            for (int t = (wg ^ done) & 1; t < count; t += 2) {
-                softmax(t);
-                for (; next < t; next++) join_tile(next);
             }
-            for (; next < count; next++) join_tile(next);
 
             float *part = sg->parts > 1 ? a.part + (size_t)(2 * (int)blockIdx.x + (tile0 == 0 ? 1 : 0)) * slot_floats
-                                         : nullptr;
+                                        : nullptr;
             if (ri.row >= 0 && !*(volatile int *)abort_flag) {
                 if (part != nullptr) {
-                    float *d = part + (size_t)row * D + wg * DH;
+                    float *d = part + (size_t)row * D;
 #pragma unroll
-                    for (int i = 0; i < DH; i += 4)
+                    for (int i = 0; i < D; i += 4)
                         *reinterpret_cast<float4 *>(d + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
-                    if (wg == 0)
-                        *reinterpret_cast<float2 *>(part + (size_t)a.rpt * D + 2 * row) = make_float2(m_run, l_run);
+                    *reinterpret_cast<float2 *>(part + (size_t)a.rpt * D + 2 * row) = make_float2(m_run, l_run);
                 } else {
                     const float inv = m_run == -INFINITY ? 0.f : 1.f / l_run;
-                    uint16_t *d = a.k.out + (size_t)ri.row * a.k.ldo + (size_t)ri.head * D + wg * DH;
+                    uint16_t *d = a.k.out + (size_t)ri.row * a.k.ldo + (size_t)ri.head * D;
 #pragma unroll
-                    for (int i = 0; i < DH; i += 8) {
+                    for (int i = 0; i < D; i += 8) {
                         uint32_t b[4];
 #pragma unroll
                         for (int j = 0; j < 4; j++) {
@@ -420,27 +464,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                         }
                         *reinterpret_cast<uint4 *>(d + i) = make_uint4(b[0], b[1], b[2], b[3]);
                     }
-                    if (wg == 0 && a.k.lse != nullptr)
+                    if (a.k.lse != nullptr)
                         a.k.lse[(size_t)ri.row * a.k.heads_q + ri.head] =
                             m_run == -INFINITY ? -INFINITY : kLn2 * (m_run + log2f(l_run));
                 }
             }
             if (part != nullptr) {
-                if (stid == 0) reinterpret_cast<Seg *>(smem + L.split)[shared] = *sg;
+                if (row == 0) {
+                    reinterpret_cast<Seg *>(smem + L.split)[shared] = *sg;
+                    *n_shared = shared + 1;
+                }
                 shared++;
             }
-            done += count;
             __syncwarp();
             if (lane == 0) {
                 mbar_arrive(B.q_empty(buf));
                 mbar_arrive(B.seg_empty(seg % kSegs));
             }
-            named_barrier(kBarAll, kSoft);  // nobody still reads the last decision
-            if (stid == 0)
-                *go = lane_wait(B.q_full(buf ^ 1), (uint32_t)((seg + 1) >> 1) & 1u, 0xc32u, abort_flag) ? 1 : 0;
-            named_barrier(kBarAll, kSoft);
         }
-        join_role<D, kSoft>(a, S, reinterpret_cast<const Seg *>(smem + L.split), shared, kBarAll, abort_flag);
+    }
+    if (warp >= kFirstSoft) {
+        named_barrier(kBarAll, kSoft);  // the list of shared units is complete
+        join_role<D, kSoft>(a, S, reinterpret_cast<const Seg *>(smem + L.split), *n_shared, kBarAll, abort_flag);
     }
     __syncthreads();
     tc_fence_after();
