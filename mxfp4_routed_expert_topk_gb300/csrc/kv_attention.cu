@@ -206,7 +206,7 @@ __global__ void __launch_bounds__(32 * kFirstSoft + 128 * groups_of(R), 1)
         if (lane == 0) drain(B.mma_done(), 0u, abort_flag);
         __syncwarp();
     } else if (warp < kFirstSoft) {
-        query_role<D, R>(a, smem, L, B, S, plan, abort_flag);
+        segment_query_role<D, R>(a, smem, L, B, S, plan, abort_flag);
     } else {
         // -------------------------------------------------------- softmax
         const int sw = warp - kFirstSoft, wg = sw >> 2, ew = sw & 3, stid = tid - 32 * kFirstSoft;

@@ -525,157 +525,196 @@ __device__ __forceinline__ void copy_role(const AttnArgs &a, const CUtensorMap *
     }
 }
 
-// ------------------------------------------------------------- queries (warp 3)
-// Walks the CTA's share and publishes its segments (a few ahead), and loads each segment's row
-// data and queries, one segment ahead of the softmax: a row's values as two E4M3 parts, after a
-// power of two that puts its largest into [128, 256).
+// ------------------------------------------------------------------ queries
+// Rows r0 .. r1-1 of a segment's row tile (one warp): their data, and their queries as two E4M3
+// parts, after a power of two that puts a row's largest value into [128, 256).
 template <int D, int R>
-__device__ __forceinline__ void query_role(const AttnArgs &a, unsigned char *smem, const CommonSmem &L, const Bars &B,
-                                           const Share &S, const int64_t *plan, int *abort_flag) {
+__device__ __forceinline__ void load_queries(const AttnArgs &a, unsigned char *smem, const CommonSmem &L, const Seg *sg,
+                                             int buf, int r0, int r1) {
     constexpr int V = D / 32;  // values per lane
     constexpr int U = 8;       // rows whose loads are in flight together
     const int lane = threadIdx.x & 31;
+    RowInfo *rows = reinterpret_cast<RowInfo *>(smem + L.rows) + buf * R;
+    unsigned char *q0 = smem + L.q + (uint32_t)buf * (2u * R * D);
+    const int rt = sg->rt, head = sg->head, row0 = sg->row0, before = sg->len - sg->n;
+    const int live = sg->count == 0 ? 0 : min(a.rpt, sg->n * a.group - rt * a.rpt);  // rows of the tile
+    // rows past the tile see nothing (their queries are what was there: nobody reads their results)
+    for (int r = max(r0, live) + lane; r < r1; r += 32) {
+        RowInfo none = {-1, 0, 1.f, -1};
+        rows[r] = none;
+    }
+#pragma unroll 1
+    for (; r0 < min(r1, live); r0 += U) {
+        uint32_t u[U][V / 2];
+        int row[U], hq[U];
+        // (row, head) of the first of them; the others follow without a division
+        int qi = (rt * a.rpt + r0) / a.group, hd = rt * a.rpt + r0 - qi * a.group;
+#pragma unroll
+        for (int i = 0; i < U; i++) {
+            row[i] = r0 + i < live ? row0 + qi : -1;
+            hq[i] = head * a.group + hd;
+            if (++hd == a.group) {
+                hd = 0;
+                qi++;
+            }
+            const uint16_t *src = a.k.q + (size_t)max(row[i], 0) * a.k.ldq + (size_t)hq[i] * D + lane * V;
+            if constexpr (V == 4) {
+                const uint2 x2 = row[i] >= 0 ? *reinterpret_cast<const uint2 *>(src) : make_uint2(0u, 0u);
+                u[i][0] = x2.x;
+                u[i][1] = x2.y;
+            } else {
+                u[i][0] = row[i] >= 0 ? *reinterpret_cast<const uint32_t *>(src) : 0u;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < U; i++) {
+            const int r = r0 + i;
+            float h[V], l[V];
+            uint32_t amax = 0;  // over finite values
+#pragma unroll
+            for (int j = 0; j < V / 2; j++) {
+                const uint32_t m = u[i][j] & 0x7fff7fffu;
+                amax = __vmaxu2(amax, m & ~__vcmpgeu2(m, 0x7f807f80u));
+            }
+            amax = __reduce_max_sync(0xffffffffu, max(amax & 0xffffu, amax >> 16));
+            const int up = amax == 0 ? 0 : min(126, 7 - ((int)(amax >> 7) - 127));
+            const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+#pragma unroll
+            for (int j = 0; j < V; j++) {
+                const uint32_t v = u[i][j / 2];
+                const float y = __uint_as_float((j & 1) ? v & 0xffff0000u : v << 16) * f;
+                h[j] = part_hi(y);
+                l[j] = y - h[j];
+            }
+            // 16-byte chunks of a row are permuted as the tensor copies permute the keys'
+            const uint32_t byte = (uint32_t)(lane * V), chunk = byte >> 4;
+            const uint32_t swz = D == 128 ? (uint32_t)(r & 7) : (uint32_t)((r >> 1) & 3);
+            unsigned char *dst = q0 + (uint32_t)r * D + ((chunk ^ swz) << 4) + (byte & 15u);
+            if constexpr (V == 4) {
+                *reinterpret_cast<uint32_t *>(dst) = e4m3x4_rn(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint32_t *>(dst + R * D) = e4m3x4_rn(l[0], l[1], l[2], l[3]);
+            } else {
+                *reinterpret_cast<uint16_t *>(dst) = (uint16_t)e4m3x2_rn(h[0], h[1]);
+                *reinterpret_cast<uint16_t *>(dst + R * D) = (uint16_t)e4m3x2_rn(l[0], l[1]);
+            }
+            if (lane == 0 && row[i] >= 0) {
+                RowInfo ri;
+                ri.row = row[i];
+                ri.head = hq[i];
+                ri.qs = __uint_as_float((uint32_t)(127 - up) << 23);
+                ri.pos = before + (row[i] - row0);
+                rows[r] = ri;
+            }
+        }
+    }
+    fence_proxy_async_smem();
+    __syncwarp();
+}
+
+// ------------------------------------------------------------- segments (warp 3)
+// Walks the CTA's share and publishes its segments, then one with count 0.
+struct Walk {
+    const AttnArgs &a;
+    const Share &S;
+    int64_t w, first;  // next position; first position of the item
+    int it;
+    Item x;
+    int published;
+    bool ended;  // the end has been published
+
+    __device__ __forceinline__ Walk(const AttnArgs &a_, const Share &S_, const int64_t *plan)
+        : a(a_), S(S_), w(S_.lo), first(plan[0]), it((int)plan[1]), published(0), ended(false) {
+        x = load_item(a, it);
+    }
+
+    __device__ __forceinline__ void publish(Seg *ring, const Bars &B) {
+        const int ss = published % kSegs;
+        Seg g;
+        g.count = 0;
+#pragma unroll 1
+        while (w < S.hi) {  // the next positions with tiles
+            const int len = unit_length(a, x);
+            const int64_t units = (int64_t)len * a.k.kv.heads, local = w - first;
+            if (local >= units) {
+                first += units;
+                x = load_item(a, ++it);
+                continue;
+            }
+            // (a division of 32 bits wherever the numbers allow)
+            g.head = (local >> 31) == 0 ? (int)((uint32_t)local / (uint32_t)len) : (int)(local / len);
+            const int pos = (int)(local - (int64_t)g.head * len);
+            const int end = (int)min((int64_t)len, pos + (S.hi - w));
+            w += end - pos;
+            g.tile0 = max(0, pos - a.over);
+            g.count = max(0, end - a.over) - g.tile0;
+            if (g.count > 0) break;
+        }
+        g.count = max(g.count, 0);
+        ended = g.count == 0;
+        if (!ended) {
+            g.b = x.b;
+            g.rt = x.rt;
+            g.n = x.n;
+            g.len = x.len;
+            g.row0 = x.row0;
+            const int q0 = x.rt * a.rpt / a.group, q1 = min(x.n - 1, ((x.rt + 1) * a.rpt - 1) / a.group);
+            g.see_all = min(x.len, max(0, x.len - x.n + q0 + 1));
+            g.see_max = min(x.len, max(0, x.len - x.n + q1 + 1));
+            g.c0 = (int)blockIdx.x;
+            g.parts = 1;
+            if (g.count < x.nt) {
+                const int64_t u0 = first + (int64_t)g.head * unit_length(a, x) + a.over;  // the unit's first tile
+                g.c0 = cta_of(u0, S.total, S.ctas);
+                g.parts = cta_of(u0 + x.nt - 1, S.total, S.ctas) - g.c0 + 1;
+            }
+        }
+        if ((threadIdx.x & 31) == 0) {
+            ring[ss] = g;
+            mbar_arrive(B.seg_full(ss));
+        }
+        __syncwarp();
+        published++;
+    }
+};
+
+// Publishes segments a few ahead and loads each one's queries, one segment ahead of the softmax.
+template <int D, int R>
+__device__ __forceinline__ void segment_query_role(const AttnArgs &a, unsigned char *smem, const CommonSmem &L,
+                                                   const Bars &B, const Share &S, const int64_t *plan, int *abort_flag) {
     Seg *ring = reinterpret_cast<Seg *>(smem + L.seg);
-    int64_t w = S.lo, first = plan[0];  // next position; first position of the item
-    int it = (int)plan[1];
-    Item x = load_item(a, it);
-    int published = 0;
-    bool ended = false;  // the end has been published
+    Walk W(a, S, plan);
 #pragma unroll 1
     for (int seg = 0;; seg++) {
-        // publish this segment and the next, and more if there is room
+        // this segment and the next, and more if there is room
 #pragma unroll 1
-        while (!ended && published < seg + kSegs) {
-            const int ss = published % kSegs;
-            const uint32_t parity = ((uint32_t)(published / kSegs) & 1u) ^ 1u;
-            if (published > seg + 1) {
-                if (!__all_sync(0xffffffffu, mbar_test(B.seg_empty(ss), parity))) break;
-            } else if (!warp_wait(B.seg_empty(ss), parity, 0xe10u, abort_flag)) {
+        while (!W.ended && W.published < seg + kSegs) {
+            uint64_t *bar = B.seg_empty(W.published % kSegs);
+            const uint32_t parity = ((uint32_t)(W.published / kSegs) & 1u) ^ 1u;
+            if (W.published > seg + 1) {
+                if (!__all_sync(0xffffffffu, mbar_test(bar, parity))) break;
+            } else if (!warp_wait(bar, parity, 0xe10u, abort_flag)) {
                 return;
             }
-            Seg g;
-            g.count = 0;
-#pragma unroll 1
-            while (w < S.hi) {  // the next positions with tiles
-                const int64_t units = (int64_t)unit_length(a, x) * a.k.kv.heads;
-                if (w - first >= units) {
-                    first += units;
-                    x = load_item(a, ++it);
-                    continue;
-                }
-                const int len = unit_length(a, x);
-                // (w - first) / len; a division of 32 bits wherever the numbers allow
-                const int64_t local = w - first;
-                g.head = (local >> 31) == 0 ? (int)((uint32_t)local / (uint32_t)len) : (int)(local / len);
-                const int pos = (int)(local - (int64_t)g.head * len);
-                const int end = (int)min((int64_t)len, pos + (S.hi - w));
-                w += end - pos;
-                g.tile0 = max(0, pos - a.over);
-                g.count = max(0, end - a.over) - g.tile0;
-                if (g.count > 0) break;
-            }
-            if (g.count > 0) {
-                g.b = x.b;
-                g.rt = x.rt;
-                g.n = x.n;
-                g.len = x.len;
-                g.row0 = x.row0;
-                const int q0 = x.rt * a.rpt / a.group, q1 = min(x.n - 1, ((x.rt + 1) * a.rpt - 1) / a.group);
-                g.see_all = min(x.len, max(0, x.len - x.n + q0 + 1));
-                g.see_max = min(x.len, max(0, x.len - x.n + q1 + 1));
-                g.c0 = (int)blockIdx.x;
-                g.parts = 1;
-                if (g.count < x.nt) {
-                    const int64_t u0 = first + (int64_t)g.head * unit_length(a, x) + a.over;  // the unit's first tile
-                    g.c0 = cta_of(u0, S.total, S.ctas);
-                    g.parts = cta_of(u0 + x.nt - 1, S.total, S.ctas) - g.c0 + 1;
-                }
-            } else {
-                g.count = 0;
-                ended = true;
-            }
-            if (lane == 0) {
-                ring[ss] = g;
-                mbar_arrive(B.seg_full(ss));
-            }
-            __syncwarp();
-            published++;
+            W.publish(ring, B);
         }
         const int buf = seg & 1;
         if (!warp_wait(B.q_empty(buf), ((uint32_t)(seg >> 1) & 1u) ^ 1u, 0xe00u + buf, abort_flag)) return;
-        const Seg *sg = ring + seg % kSegs;
-        RowInfo *rows = reinterpret_cast<RowInfo *>(smem + L.rows) + buf * R;
-        unsigned char *q0 = smem + L.q + (uint32_t)buf * (2u * R * D);
-        const int rt = sg->rt, head = sg->head, row0 = sg->row0, before = sg->len - sg->n;
-        const int live = sg->count == 0 ? 0 : min(a.rpt, sg->n * a.group - rt * a.rpt);  // rows of the tile
+        load_queries<D, R>(a, smem, L, ring + seg % kSegs, buf, 0, R);
+        if ((threadIdx.x & 31) == 0) mbar_arrive(B.q_full(buf));
+        if (ring[seg % kSegs].count == 0) return;
+    }
+}
+
+// Publishes segments only.
+__device__ __forceinline__ void segment_role(const AttnArgs &a, unsigned char *smem, const CommonSmem &L, const Bars &B,
+                                             const Share &S, const int64_t *plan, int *abort_flag) {
+    Seg *ring = reinterpret_cast<Seg *>(smem + L.seg);
+    Walk W(a, S, plan);
 #pragma unroll 1
-        for (int r0 = 0; r0 < R && live > 0; r0 += U) {
-            uint32_t u[U][V / 2];
-            int row[U], hq[U];
-            // (row, head) of the first of them; the others follow without a division
-            int qi = (rt * a.rpt + r0) / a.group, hd = rt * a.rpt + r0 - qi * a.group;
-#pragma unroll
-            for (int i = 0; i < U; i++) {
-                row[i] = r0 + i < live ? row0 + qi : -1;
-                hq[i] = head * a.group + hd;
-                if (++hd == a.group) {
-                    hd = 0;
-                    qi++;
-                }
-                const uint16_t *src = a.k.q + (size_t)max(row[i], 0) * a.k.ldq + (size_t)hq[i] * D + lane * V;
-                if constexpr (V == 4) {
-                    const uint2 x2 = row[i] >= 0 ? *reinterpret_cast<const uint2 *>(src) : make_uint2(0u, 0u);
-                    u[i][0] = x2.x;
-                    u[i][1] = x2.y;
-                } else {
-                    u[i][0] = row[i] >= 0 ? *reinterpret_cast<const uint32_t *>(src) : 0u;
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < U; i++) {
-                const int r = r0 + i;
-                float h[V], l[V];
-                uint32_t amax = 0;  // over finite values
-#pragma unroll
-                for (int j = 0; j < V / 2; j++) {
-                    const uint32_t m = u[i][j] & 0x7fff7fffu;
-                    amax = __vmaxu2(amax, m & ~__vcmpgeu2(m, 0x7f807f80u));
-                }
-                amax = __reduce_max_sync(0xffffffffu, max(amax & 0xffffu, amax >> 16));
-                const int up = amax == 0 ? 0 : min(126, 7 - ((int)(amax >> 7) - 127));
-                const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-#pragma unroll
-                for (int j = 0; j < V; j++) {
-                    const uint32_t v = u[i][j / 2];
-                    const float y = __uint_as_float((j & 1) ? v & 0xffff0000u : v << 16) * f;
-                    h[j] = part_hi(y);
-                    l[j] = y - h[j];
-                }
-                // 16-byte chunks of a row are permuted as the tensor copies permute the keys'
-                const uint32_t byte = (uint32_t)(lane * V), chunk = byte >> 4;
-                const uint32_t swz = D == 128 ? (uint32_t)(r & 7) : (uint32_t)((r >> 1) & 3);
-                unsigned char *dst = q0 + (uint32_t)r * D + ((chunk ^ swz) << 4) + (byte & 15u);
-                if constexpr (V == 4) {
-                    *reinterpret_cast<uint32_t *>(dst) = e4m3x4_rn(h[0], h[1], h[2], h[3]);
-                    *reinterpret_cast<uint32_t *>(dst + R * D) = e4m3x4_rn(l[0], l[1], l[2], l[3]);
-                } else {
-                    *reinterpret_cast<uint16_t *>(dst) = (uint16_t)e4m3x2_rn(h[0], h[1]);
-                    *reinterpret_cast<uint16_t *>(dst + R * D) = (uint16_t)e4m3x2_rn(l[0], l[1]);
-                }
-                if (lane == 0) {
-                    RowInfo ri;
-                    ri.row = row[i];
-                    ri.head = hq[i];
-                    ri.qs = __uint_as_float((uint32_t)(127 - up) << 23);
-                    ri.pos = row[i] < 0 ? -1 : before + (row[i] - row0);
-                    rows[r] = ri;
-                }
-            }
-        }
-        fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(B.q_full(buf));
-        if (live == 0) return;  // the end
+    while (!W.ended) {
+        if (!warp_wait(B.seg_empty(W.published % kSegs), ((uint32_t)(W.published / kSegs) & 1u) ^ 1u, 0xe10u, abort_flag))
+            return;
+        W.publish(ring, B);
     }
 }
 
@@ -750,35 +789,57 @@ __device__ __forceinline__ void join_role(const AttnArgs &a, const Share &S, con
         // rows cta - c0, + parts, ...: a warp per row, lanes over the head's values
 #pragma unroll 1
         for (int r = (cta - c0) + parts * sw; r < nrows; r += parts * (NSOFT / 32)) {
-            constexpr int V = D / 32;
-            float m = -INFINITY;
-            for (int p = lane; p < parts; p += 32) {
-                const float *slot = a.part + (size_t)(2 * (c0 + p) + (p == 0 ? 1 : 0)) * slot_floats;
-                m = fmaxf(m, __ldcg(slot + (size_t)a.rpt * D + 2 * r));
-            }
-#pragma unroll
-            for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-            float l = 0.f, acc[V];
+            constexpr int V = D / 32, U = 4;  // values per lane; parts whose loads are in flight together
+            auto slot_of = [&](int p) { return a.part + (size_t)(2 * (c0 + p) + (p == 0 ? 1 : 0)) * slot_floats; };
+            auto load = [&](int p, float (&x)[V]) {
+                const float *v = slot_of(p) + (size_t)r * D + lane * V;
+                if constexpr (V == 4) {
+                    const float4 t = __ldcg(reinterpret_cast<const float4 *>(v));
+                    x[0] = t.x;
+                    x[1] = t.y;
+                    x[2] = t.z;
+                    x[3] = t.w;
+                } else {
+                    const float2 t = __ldcg(reinterpret_cast<const float2 *>(v));
+                    x[0] = t.x;
+                    x[1] = t.y;
+                }
+            };
+            float x[U][V], acc[V], l = 0.f, m = -INFINITY;
 #pragma unroll
             for (int j = 0; j < V; j++) acc[j] = 0.f;
-#pragma unroll 4
-            for (int p = 0; p < parts; p++) {
-                const float *slot = a.part + (size_t)(2 * (c0 + p) + (p == 0 ? 1 : 0)) * slot_floats;
-                const float2 ml = __ldcg(reinterpret_cast<const float2 *>(slot + (size_t)a.rpt * D + 2 * r));
-                const float f = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
-                l += ml.y * f;
-                const float *v = slot + (size_t)r * D + lane * V;
-                if constexpr (V == 4) {
-                    const float4 x = __ldcg(reinterpret_cast<const float4 *>(v));
-                    acc[0] = fmaf(x.x, f, acc[0]);
-                    acc[1] = fmaf(x.y, f, acc[1]);
-                    acc[2] = fmaf(x.z, f, acc[2]);
-                    acc[3] = fmaf(x.w, f, acc[3]);
-                } else {
-                    const float2 x = __ldcg(reinterpret_cast<const float2 *>(v));
-                    acc[0] = fmaf(x.x, f, acc[0]);
-                    acc[1] = fmaf(x.y, f, acc[1]);
+#pragma unroll
+            for (int i = 0; i < U; i++)
+                if (i < parts) load(i, x[i]);
+            // references and sums, a lane per part (the first 32, and what more there is one by one)
+            float2 ml = make_float2(-INFINITY, 0.f);
+            if (lane < parts) ml = __ldcg(reinterpret_cast<const float2 *>(slot_of(lane) + (size_t)a.rpt * D + 2 * r));
+            m = ml.x;
+            for (int p = lane + 32; p < parts; p += 32) m = fmaxf(m, __ldcg(slot_of(p) + (size_t)a.rpt * D + 2 * r));
+#pragma unroll
+            for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
+            const float mine = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+#pragma unroll 1
+            for (int p = 0; p < parts; p += U) {
+#pragma unroll
+                for (int i = 0; i < U; i++) {
+                    if (p + i >= parts) continue;
+                    float f, s;
+                    if (p + i < 32) {
+                        f = __shfl_sync(0xffffffffu, mine, p + i);
+                        s = __shfl_sync(0xffffffffu, ml.y, p + i);
+                    } else {
+                        const float2 t = __ldcg(reinterpret_cast<const float2 *>(slot_of(p + i) + (size_t)a.rpt * D + 2 * r));
+                        f = t.x == -INFINITY ? 0.f : ex2(t.x - m);
+                        s = t.y;
+                    }
+                    l = fmaf(s, f, l);
+#pragma unroll
+                    for (int j = 0; j < V; j++) acc[j] = fmaf(x[i][j], f, acc[j]);
                 }
+#pragma unroll
+                for (int i = 0; i < U; i++)
+                    if (p + U + i < parts) load(p + U + i, x[i]);
             }
             const int R = g.rt * a.rpt + r, qi = R / a.group, row = g.row0 + qi;
             const int hq = g.head * a.group + R - qi * a.group;

@@ -121,7 +121,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             mbar_init(B.v_empty(s), 1);
         }
         for (int b = 0; b < 2; b++) {
-            mbar_init(B.q_full(b), 1);
+            mbar_init(B.q_full(b), 4);
             mbar_init(B.q_empty(b), kSoft / 32);
         }
         for (int b = 0; b < kSBufs; b++) {
@@ -232,7 +232,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         if (lane == 0) drain(B.mma_done(), 0u, abort_flag);
         __syncwarp();
     } else {
-        query_role<D, kRows>(a, smem, L, B, S, plan, abort_flag);
+        segment_role(a, smem, L, B, S, plan, abort_flag);
     }
     } else if (warp < kJoinWarp) {
         regs_dec<kRegsSoft>();
@@ -383,6 +383,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         const size_t slot_floats = (size_t)a.rpt * D + 2 * a.rpt;
         float o[D];
         int u = 0, shared = 0;  // tiles joined; units shared with other CTAs
+        // segment s's queries, 32 rows in each of these warps: loaded at the start of segment s - 1,
+        // whose first output is still far
+        auto queries = [&](int s) {
+            if (!warp_wait(B.seg_full(s % kSegs), (uint32_t)(s / kSegs) & 1u, 0xe20u, abort_flag) ||
+                !warp_wait(B.q_empty(s & 1), ((uint32_t)(s >> 1) & 1u) ^ 1u, 0xe00u, abort_flag))
+                return;
+            load_queries<D, kRows>(a, smem, L, reinterpret_cast<const Seg *>(smem + L.seg) + s % kSegs, s & 1, 32 * ew,
+                                   32 * ew + 32);
+            if (lane == 0) mbar_arrive(B.q_full(s & 1));
+        };
+        queries(0);
 
 #pragma unroll 1
         for (int seg = 0;; seg++) {
@@ -392,6 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             const RowInfo ri = reinterpret_cast<const RowInfo *>(smem + L.rows)[buf * kRows + row];
             const int count = sg->count, tile0 = sg->tile0;
             if (count == 0) break;
+            queries(seg + 1);
             float m_run = -INFINITY, l_run = 0.f;
 #pragma unroll
             for (int i = 0; i < D; i++) o[i] = 0.f;
