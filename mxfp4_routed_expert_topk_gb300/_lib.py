@@ -519,18 +519,40 @@ class KvCache:
             self.handle = None
 
 
+# The calls below are made once per layer and token, so their checks go by as few tensor
+# attributes as they can.
+
+_raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _raw_stream(stream, like):
+    """The stream's handle: `stream`, or the current one of the tensor's device."""
+    if stream is not None:
+        return stream.cuda_stream
+    if _raw_stream_of is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream_of(like.get_device())
+
+
 def _need_heads(t, heads, dim, name):
     """Row stride (in elements) of a bf16 [rows, heads, dim] tensor whose rows are dense."""
-    if not (t.is_cuda and t.dtype == torch.bfloat16 and t.dim() == 3 and t.shape[1:] == (heads, dim)
-            and t.stride(2) == 1 and (heads == 1 or t.stride(1) == dim)):
+    shape, stride = t.shape, t.stride()
+    if not (t.is_cuda and t.dtype == torch.bfloat16 and len(shape) == 3 and shape[1] == heads and shape[2] == dim
+            and stride[2] == 1 and (heads == 1 or stride[1] == dim)):
         raise ValueError(f"{name}: expected a CUDA bfloat16 tensor [rows, {heads}, {dim}] with dense rows")
-    return t.stride(0) if t.shape[0] > 1 else heads * dim
+    return stride[0] if shape[0] > 1 else heads * dim
 
 
 def _need_index(t, n, name):
-    _need(t, torch.int32, name)
-    if t.numel() != n:
-        raise ValueError(f"{name}: expected {n} values")
+    if not (t.is_cuda and t.dtype == torch.int32 and t.is_contiguous() and t.numel() == n):
+        raise ValueError(f"{name}: expected a contiguous CUDA int32 tensor of {n} values")
+
+
+def _need_table(t):
+    """(sequences, columns) of a page table."""
+    if not (t.is_cuda and t.dtype == torch.int32 and t.dim() == 2 and t.is_contiguous()):
+        raise ValueError("page_table: expected a contiguous CUDA int32 tensor [sequences, columns]")
+    return t.shape
 
 
 def _empty(shape, dtype, like, stream):
@@ -555,18 +577,21 @@ def moe_kv_append_workspace_size() -> int:
 def moe_kv_append(cache: KvCache, layer: int, k: torch.Tensor, v: torch.Tensor, cu_rows: torch.Tensor,
                   start: torch.Tensor, page_table: torch.Tensor, ws: torch.Tensor | None = None, stream=None):
     """Append rows k, v [rows, heads, head_dim] (dense rows, any row stride) to the cache."""
+    rows = k.shape[0]
     ldk = _need_heads(k, cache.heads, cache.head_dim, "k")
     ldv = _need_heads(v, cache.heads, cache.head_dim, "v")
-    if v.shape[0] != k.shape[0]:
+    if v.shape[0] != rows:
         raise ValueError("k, v: different row counts")
-    _need(page_table, torch.int32, "page_table")
-    seqs, width = page_table.shape
+    seqs, width = _need_table(page_table)
     _need_index(cu_rows, seqs + 1, "cu_rows")
     _need_index(start, seqs, "start")
     if ws is None:
         ws = _workspace_on(moe_kv_append_workspace_size(), k, stream)
-    _check(lib().moe_kv_append(cache.handle, layer, _ptr(k), ldk, _ptr(v), ldv, k.shape[0], _ptr(cu_rows), _ptr(start),
-                               _ptr(page_table), width, seqs, _ptr(ws), ws.numel(), _stream(stream)), "moe_kv_append")
+    code = lib().moe_kv_append(cache.handle, layer, k.data_ptr(), ldk, v.data_ptr(), ldv, rows, cu_rows.data_ptr(),
+                               start.data_ptr(), page_table.data_ptr(), width, seqs, ws.data_ptr(), ws.numel(),
+                               _raw_stream(stream, k))
+    if code:
+        raise MoeError(code, "moe_kv_append")
 
 
 def moe_kv_attention_workspace_size(cache: KvCache, max_rows: int, heads_q: int) -> int:
@@ -582,28 +607,31 @@ def moe_kv_attention(cache: KvCache, layer: int, q: torch.Tensor, cu_rows: torch
                      ws: torch.Tensor | None = None, stream=None):
     """Attention of q [rows, heads_q, head_dim] over the cache; returns out (bf16, like q).
     scale: head_dim ** -0.5 unless given; lse (float32 [rows, heads_q]) is filled if given."""
-    rows, heads_q = q.shape[:2]
-    ldq = _need_heads(q, heads_q, cache.head_dim, "q")
-    _need(page_table, torch.int32, "page_table")
-    seqs, width = page_table.shape
+    rows, heads_q, _ = q.shape
+    dim = cache.head_dim
+    ldq = _need_heads(q, heads_q, dim, "q")
+    seqs, width = _need_table(page_table)
     _need_index(cu_rows, seqs + 1, "cu_rows")
     _need_index(kv_len, seqs, "kv_len")
     if out is None:
-        out = _empty((rows, heads_q, cache.head_dim), torch.bfloat16, q, stream)
-    ldo = _need_heads(out, heads_q, cache.head_dim, "out")
-    if out.shape[0] != rows:
-        raise ValueError(f"out: expected {rows} rows")
+        out, ldo = _empty((rows, heads_q, dim), torch.bfloat16, q, stream), heads_q * dim
+    else:
+        ldo = _need_heads(out, heads_q, dim, "out")
+        if out.shape[0] != rows:
+            raise ValueError(f"out: expected {rows} rows")
     if lse is not None:
         _need(lse, torch.float32, "lse")
         if lse.numel() != rows * heads_q:
             raise ValueError(f"lse: expected [{rows}, {heads_q}]")
     if ws is None:
         ws = _workspace_on(moe_kv_attention_workspace_size(cache, max_rows, heads_q), q, stream)
-    if scale is None:
-        scale = cache.head_dim ** -0.5
-    _check(lib().moe_kv_attention(cache.handle, layer, _ptr(q), ldq, rows, heads_q, _ptr(cu_rows), _ptr(kv_len),
-                                  _ptr(page_table), width, seqs, max_rows, scale, _ptr(out), ldo, _ptr(lse), _ptr(ws),
-                                  ws.numel(), _stream(stream)), "moe_kv_attention")
+    code = lib().moe_kv_attention(cache.handle, layer, q.data_ptr(), ldq, rows, heads_q, cu_rows.data_ptr(),
+                                  kv_len.data_ptr(), page_table.data_ptr(), width, seqs, max_rows,
+                                  dim ** -0.5 if scale is None else scale, out.data_ptr(), ldo,
+                                  None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
+                                  _raw_stream(stream, q))
+    if code:
+        raise MoeError(code, "moe_kv_attention")
     return out
 
 
@@ -616,23 +644,27 @@ def moe_verify_workspace_size(seqs: int, rows: int) -> int:
     return int(n.value)
 
 
-def _need_probs(t, name, like=None):
-    """Row stride and dtype code of a [rows, vocab] tensor of probabilities or logits."""
-    if not (t.is_cuda and t.dim() == 2 and t.stride(1) == 1 and t.dtype in (torch.float32, torch.bfloat16)):
+def _need_probs(t, name):
+    """(rows, vocab, row stride, dtype code) of a tensor of probabilities or logits."""
+    shape, stride, dtype = t.shape, t.stride(), t.dtype
+    if not (t.is_cuda and len(shape) == 2 and stride[1] == 1 and (dtype == torch.float32 or dtype == torch.bfloat16)):
         raise ValueError(f"{name}: expected a CUDA float32 or bfloat16 tensor [rows, vocab] with dense rows")
-    if like is not None and (t.shape != like.shape or t.dtype != like.dtype):
-        raise ValueError(f"{name}: expected the shape and type of p")
-    return t.stride(0) if t.shape[0] > 1 else t.shape[1], (MOE_PROB_F32 if t.dtype == torch.float32 else MOE_PROB_BF16)
+    rows, vocab = shape
+    return rows, vocab, stride[0] if rows > 1 else vocab, MOE_PROB_F32 if dtype == torch.float32 else MOE_PROB_BF16
 
 
-def _verify_outputs(p, tokens, cu_rows, accepted, next_token, ws, stream):
-    rows, seqs = p.shape[0], cu_rows.numel() - 1
+def _verify_outputs(p, rows, tokens, cu_rows, accepted, next_token, ws, stream):
+    seqs = cu_rows.numel() - 1
     _need_index(tokens, rows, "tokens")
     _need_index(cu_rows, max(seqs, 0) + 1, "cu_rows")
-    accepted = _empty((seqs,), torch.int32, p, stream) if accepted is None else accepted
-    next_token = _empty((seqs,), torch.int32, p, stream) if next_token is None else next_token
-    _need_index(accepted, seqs, "accepted")
-    _need_index(next_token, seqs, "next_token")
+    if accepted is None:
+        accepted = _empty((seqs,), torch.int32, p, stream)
+    else:
+        _need_index(accepted, seqs, "accepted")
+    if next_token is None:
+        next_token = _empty((seqs,), torch.int32, p, stream)
+    else:
+        _need_index(next_token, seqs, "next_token")
     if ws is None:
         ws = _workspace_on(moe_verify_workspace_size(seqs, rows), p, stream)
     return seqs, accepted, next_token, ws
@@ -642,16 +674,23 @@ def moe_verify_sampled(p: torch.Tensor, q: torch.Tensor | None, tokens: torch.Te
                        u_accept: torch.Tensor, u_sample: torch.Tensor, accepted: torch.Tensor | None = None,
                        next_token: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
     """(accepted, next_token), int32 [seqs]: how many drafts of each sequence hold, and the token after them."""
-    ldp, dt = _need_probs(p, "p")
-    ldq = 0 if q is None else _need_probs(q, "q", p)[0]
-    seqs, accepted, next_token, ws = _verify_outputs(p, tokens, cu_rows, accepted, next_token, ws, stream)
+    rows, vocab, ldp, dt = _need_probs(p, "p")
+    ldq = 0
+    if q is not None:
+        rows_q, vocab_q, ldq, dt_q = _need_probs(q, "q")
+        if rows_q != rows or vocab_q != vocab or dt_q != dt:
+            raise ValueError("q: expected the shape and type of p")
+    seqs, accepted, next_token, ws = _verify_outputs(p, rows, tokens, cu_rows, accepted, next_token, ws, stream)
     _need(u_accept, torch.float32, "u_accept")
     _need(u_sample, torch.float32, "u_sample")
-    if u_accept.numel() != p.shape[0] or u_sample.numel() != seqs:
+    if u_accept.numel() != rows or u_sample.numel() != seqs:
         raise ValueError("u_accept, u_sample: expected one value per row and one per sequence")
-    _check(lib().moe_verify_sampled(_ptr(p), ldp, _ptr(q), ldq, dt, p.shape[0], p.shape[1], _ptr(tokens), _ptr(cu_rows),
-                                    seqs, _ptr(u_accept), _ptr(u_sample), _ptr(accepted), _ptr(next_token), _ptr(ws),
-                                    ws.numel(), _stream(stream)), "moe_verify_sampled")
+    code = lib().moe_verify_sampled(p.data_ptr(), ldp, None if q is None else q.data_ptr(), ldq, dt, rows, vocab,
+                                    tokens.data_ptr(), cu_rows.data_ptr(), seqs, u_accept.data_ptr(),
+                                    u_sample.data_ptr(), accepted.data_ptr(), next_token.data_ptr(), ws.data_ptr(),
+                                    ws.numel(), _raw_stream(stream, p))
+    if code:
+        raise MoeError(code, "moe_verify_sampled")
     return accepted, next_token
 
 
@@ -659,11 +698,13 @@ def moe_verify_greedy(logits: torch.Tensor, tokens: torch.Tensor, cu_rows: torch
                       accepted: torch.Tensor | None = None, next_token: torch.Tensor | None = None,
                       ws: torch.Tensor | None = None, stream=None):
     """(accepted, next_token), int32 [seqs]: drafts that equal the arg max, and the arg max after them."""
-    ld, dt = _need_probs(logits, "logits")
-    seqs, accepted, next_token, ws = _verify_outputs(logits, tokens, cu_rows, accepted, next_token, ws, stream)
-    _check(lib().moe_verify_greedy(_ptr(logits), ld, dt, logits.shape[0], logits.shape[1], _ptr(tokens), _ptr(cu_rows),
-                                   seqs, _ptr(accepted), _ptr(next_token), _ptr(ws), ws.numel(), _stream(stream)),
-           "moe_verify_greedy")
+    rows, vocab, ld, dt = _need_probs(logits, "logits")
+    seqs, accepted, next_token, ws = _verify_outputs(logits, rows, tokens, cu_rows, accepted, next_token, ws, stream)
+    code = lib().moe_verify_greedy(logits.data_ptr(), ld, dt, rows, vocab, tokens.data_ptr(), cu_rows.data_ptr(), seqs,
+                                   accepted.data_ptr(), next_token.data_ptr(), ws.data_ptr(), ws.numel(),
+                                   _raw_stream(stream, logits))
+    if code:
+        raise MoeError(code, "moe_verify_greedy")
     return accepted, next_token
 
 

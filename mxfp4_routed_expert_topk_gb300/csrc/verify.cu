@@ -1,20 +1,31 @@
 // Verification of drafted tokens: acceptance in whole numbers, the next token by the
 // inverse of the cumulative weights (sampled), or by the arg max (greedy).
 //
-// Simple form: one block of 1024 threads per sequence.
+// Both read rows of up to 2^20 values once and are bound by that read; small calls are bound
+// by the chain of dependent accesses before it.
+//
+// Sampled: a cluster of CTAs per sequence.  Every CTA finds the deciding row by itself (a lane
+// per draft: two gathers, a whole-number comparison, a vote), so nothing is exchanged for it;
+// then each warp sums the weights of its own consecutive part of that row, the CTAs' sums are
+// exchanged through distributed shared memory, and the one warp whose part holds the drawn
+// point scans it again (it is in L1 / L2).  Weights are whole numbers of 38 bits, so the sums
+// are exact in any order and the result is the definition's, bit for bit.
+//
+// Greedy: a cluster per row finds its arg max (all rows at once: waiting for a row's verdict
+// would cost more than the rows after a mismatch), then a warp per sequence compares.
+#include <algorithm>
+
 #include "kv_internal.cuh"
+#include "sm100_tensor.cuh"
 
 namespace moe {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxCluster = 8;
 constexpr int kGrid = 38;       // probabilities are whole multiples of 2^-38
 constexpr int kUniform = 24;    // uniforms are whole multiples of 2^-24
-
-template <bool BF16>
-__device__ __forceinline__ float load_value(const void *p, size_t i) {
-    return BF16 ? bf16_bits_to_float(static_cast<const uint16_t *>(p)[i]) : static_cast<const float *>(p)[i];
-}
 
 // floor(2^38 min(max(p, 0), 1)), NaN: 0.
 __device__ __forceinline__ uint64_t whole(float p) {
@@ -25,165 +36,346 @@ __device__ __forceinline__ uint64_t whole_uniform(float u) {
     return (uint64_t)__float2uint_rz(fminf(fmaxf(u, 0.f), 0.99999994f) * 16777216.f);
 }
 
-// Weight of token i at the row that decides: P - Q (cut at 0), or P alone (q null), or 0
-// at `drop`.
+// A row of n values, cut into vectors of 16 bytes on 16-byte boundaries: vector 0 is the
+// (possibly partial) one that holds the row's first value.
 template <bool BF16>
-__device__ __forceinline__ uint64_t weight(const void *p, const void *q, int64_t drop, size_t i) {
-    const uint64_t x = whole(load_value<BF16>(p, i));
-    if (q != nullptr) {
-        const uint64_t y = whole(load_value<BF16>(q, i));
-        return x > y ? x - y : 0;
+struct Row {
+    static constexpr int kVec = BF16 ? 8 : 4;
+    static constexpr int kSize = BF16 ? 2 : 4;
+    const uint8_t *p;  // the first value
+    int n, lead;       // values; places of vector 0 before the first value
+
+    __device__ __forceinline__ Row(const void *base, size_t at, int n_) : n(n_) {
+        p = static_cast<const uint8_t *>(base) + at * kSize;
+        lead = (int)(((uintptr_t)p & 15u) / kSize);
     }
-    return (int64_t)i == drop ? 0 : x;
+    __device__ __forceinline__ int vectors() const { return (n + lead + kVec - 1) / kVec; }
+    __device__ __forceinline__ int first(int v) const { return v * kVec - lead; }  // index of its first place
+    __device__ __forceinline__ bool whole_vector(int v) const { return first(v) >= 0 && first(v) + kVec <= n; }
+    __device__ __forceinline__ float at(int i) const {
+        return BF16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t *>(p)[i]) : reinterpret_cast<const float *>(p)[i];
+    }
+    // the values of vector v (`none` outside the row)
+    __device__ __forceinline__ void load(int v, float none, float (&x)[kVec]) const {
+        const int i0 = first(v);
+        if (i0 >= 0 && i0 + kVec <= n) {
+            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p + (ptrdiff_t)i0 * kSize));
+            const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                if constexpr (BF16) {
+                    x[2 * k] = __uint_as_float(w[k] << 16);
+                    x[2 * k + 1] = __uint_as_float(w[k] & 0xffff0000u);
+                } else {
+                    x[k] = __uint_as_float(w[k]);
+                }
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < kVec; k++) x[k] = i0 + k >= 0 && i0 + k < n ? at(i0 + k) : none;
+        }
+    }
+};
+
+__device__ __forceinline__ void store_cluster_u64(uint64_t *mine, uint32_t rank, uint64_t v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(mapa_shared(mine, rank)), "l"(v) : "memory");
 }
 
-template <typename T>
-__device__ T block_scan(T v, T *total) {
-    __shared__ T sums[32];
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    T x = v;
-    for (int d = 1; d < 32; d <<= 1) {
-        const T o = __shfl_up_sync(0xffffffffu, x, d);
-        if (lane >= d) x += o;
+// The deciding row of sequence rows [lo, hi): the first whose draft is not accepted, or the
+// last (one warp; uniform result).
+template <bool BF16>
+__device__ __forceinline__ int deciding_row(const VerifyArgs &a, int lo, int hi, int lane) {
+    constexpr int kSize = BF16 ? 2 : 4;
+    for (int r0 = lo; r0 < hi - 1; r0 += 32) {
+        const int r = r0 + lane;
+        bool ok = true;
+        if (r < hi - 1) {
+            const int d = a.tokens[r + 1];
+            const uint64_t m = whole_uniform(a.u_accept[r]);
+            uint64_t P = 0, Q = 1ull << kGrid;
+            if (d >= 0 && d < a.vocab) {
+                auto get = [&](const void *base, size_t ld) {
+                    const uint8_t *at = static_cast<const uint8_t *>(base) + ((size_t)r * ld + d) * kSize;
+                    return whole(BF16 ? bf16_bits_to_float(__ldg(reinterpret_cast<const uint16_t *>(at)))
+                                      : __ldg(reinterpret_cast<const float *>(at)));
+                };
+                P = get(a.p, a.ldp);
+                if (a.q != nullptr) Q = get(a.q, a.ldq);
+            }
+            ok = m * Q < P << kUniform;
+        }
+        const uint32_t bad = __ballot_sync(0xffffffffu, !ok);
+        if (bad != 0u) return r0 + __ffs((int)bad) - 1;
     }
-    __syncthreads();
-    if (lane == 31) sums[warp] = x;
-    __syncthreads();
-    T all = 0;
-    for (int w = 0; w < kThreads / 32; w++) {
-        if (w < warp) x += sums[w];
-        all += sums[w];
-    }
-    *total = all;
-    return x - v;  // exclusive
+    return hi - 1;
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) verify_sampled_kernel(const VerifyArgs a) {
-    __shared__ int s_row, s_token;
-    constexpr size_t kSize = BF16 ? 2 : 4;
-    const int b = blockIdx.x, tid = threadIdx.x;
+__global__ void __launch_bounds__(kThreads, 2) verify_sampled_kernel(const VerifyArgs a) {
+    constexpr int kVec = Row<BF16>::kVec;
+    __shared__ int s_row;
+    __shared__ uint64_t s_warp[kWarps];
+    __shared__ uint64_t s_cta[2][kMaxCluster];  // [round][rank]: every CTA's sum
+    const uint32_t rank = cluster_ctarank(), ranks = cluster_nctarank();
+    const int b = (int)(blockIdx.x / ranks), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int lo, hi;
     const bool ok = seq_rows(a.cu_rows, b, a.rows, lo, hi);
-    if (!ok || lo == hi) {
-        if (tid == 0) {
+    if (!ok || lo == hi) {  // the whole cluster alike
+        if (rank == 0 && tid == 0) {
             if (!ok) set_status(a.st, MOE_ERR_BAD_PAGE, 1);
             a.accepted[b] = 0;
             a.next[b] = -1;
         }
         return;
     }
-    if (tid == 0) {
-        int r = lo;
-        for (; r < hi - 1; r++) {
-            const int d = a.tokens[r + 1];
-            if (d < 0 || d >= a.vocab) break;
-            const uint64_t P = whole(load_value<BF16>(a.p, (size_t)r * a.ldp + d));
-            const uint64_t Q = a.q ? whole(load_value<BF16>(a.q, (size_t)r * a.ldq + d)) : 1ull << kGrid;
-            if (whole_uniform(a.u_accept[r]) * Q >= P << kUniform) break;
-        }
-        s_row = r;
-        s_token = -1;
+    cluster_arrive();  // waited for before the first remote store: by then every CTA has started
+    if (warp == 0) {
+        const int r = deciding_row<BF16>(a, lo, hi, lane);
+        if (lane == 0) s_row = r;
     }
     __syncthreads();
     const int r = s_row;
-    const char *p = static_cast<const char *>(a.p) + (size_t)r * a.ldp * kSize;
-    const char *q = a.q && r < hi - 1 ? static_cast<const char *>(a.q) + (size_t)r * a.ldq * kSize : nullptr;
-    int64_t drop = a.q == nullptr && r < hi - 1 ? a.tokens[r + 1] : -1;
-    const int per = (a.vocab + kThreads - 1) / kThreads;
-    const int i0 = min(tid * per, a.vocab), i1 = min(i0 + per, a.vocab);
-    for (int pass = 0; pass < 2; pass++) {
-        uint64_t mine = 0, total;
-        for (int i = i0; i < i1; i++) mine += weight<BF16>(p, q, drop, i);
-        uint64_t at = block_scan<uint64_t>(mine, &total);
-        if (total == 0) {  // nothing is left of the target: all of it
-            q = nullptr;
-            drop = -1;
-            continue;
+    const bool rejected = r < hi - 1;
+    const Row<BF16> P(a.p, (size_t)r * a.ldp, a.vocab);
+    const Row<BF16> Q(a.q, a.q != nullptr ? (size_t)r * a.ldq : 0, a.vocab);
+    bool minus = a.q != nullptr && rejected;           // weights P - Q
+    int drop = a.q == nullptr && rejected ? a.tokens[r + 1] : -1;  // (outside the vocabulary: none)
+    const bool together = Q.lead == P.lead;            // both rows' vectors hold the same indices
+    const int vectors = P.vectors();
+    const int per = (vectors + (int)ranks * kWarps - 1) / ((int)ranks * kWarps);  // vectors per warp
+    const int v0 = min(((int)rank * kWarps + warp) * per, vectors), v1 = min(v0 + per, vectors);
+
+    // the weights of vector v
+    auto weights = [&](int v, uint64_t (&w)[kVec]) {
+        float x[kVec], y[kVec];
+        P.load(v, 0.f, x);
+        if (minus) {
+            if (together) {
+                Q.load(v, 0.f, y);
+            } else {
+                const int i0 = P.first(v);
+#pragma unroll
+                for (int k = 0; k < kVec; k++) y[k] = i0 + k >= 0 && i0 + k < a.vocab ? Q.at(i0 + k) : 0.f;
+            }
+        }
+#pragma unroll
+        for (int k = 0; k < kVec; k++) {
+            w[k] = whole(x[k]);
+            if (minus) {
+                const uint64_t z = whole(y[k]);
+                w[k] = w[k] > z ? w[k] - z : 0;
+            }
+            if (P.first(v) + k == drop) w[k] = 0;
+        }
+    };
+
+    for (int round = 0; round < 2; round++) {
+        uint64_t sum = 0;
+#pragma unroll 2
+        for (int v = v0 + lane; v < v1; v += 32) {
+            uint64_t w[kVec];
+            weights(v, w);
+#pragma unroll
+            for (int k = 0; k < kVec; k++) sum += w[k];
+        }
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
+        if (lane == 0) s_warp[warp] = sum;
+        __syncthreads();
+        uint64_t cta = 0, before = 0;  // this CTA's sum; what its warps before this one hold
+#pragma unroll
+        for (int w = 0; w < kWarps; w++) {
+            if (w < warp) before += s_warp[w];
+            cta += s_warp[w];
+        }
+        if (round == 0) cluster_wait();
+        // every CTA writes its sum into all (nothing is read remotely, so none waits to exit)
+        if (tid < (int)ranks) store_cluster_u64(&s_cta[round][rank], (uint32_t)tid, cta);
+        cluster_sync();
+        uint64_t total = 0;
+        for (uint32_t k = 0; k < ranks; k++) {
+            if (k < rank) before += s_cta[round][k];
+            total += s_cta[round][k];
+        }
+        if (total == 0) {
+            if (round == 0 && (minus || drop >= 0)) {  // nothing is left: all of the target
+                minus = false;
+                drop = -1;
+                continue;
+            }
+            if (rank == 0 && tid == 0) a.next[b] = -1;
+            break;
         }
         const uint64_t m = whole_uniform(a.u_sample[b]);
         const uint64_t aim = (total >> kUniform) * m + (((total & ((1ull << kUniform) - 1)) * m) >> kUniform);
-        if (aim >= at && aim < at + mine) {
-            for (int i = i0; i < i1; i++) {
-                at += weight<BF16>(p, q, drop, i);
-                if (at > aim) {
-                    s_token = i;
-                    break;
+        if (aim >= before && aim < before + sum) {  // in this warp's part
+            uint64_t at = before;
+            for (int v = v0; v < v1; v += 32) {
+                uint64_t w[kVec], mine = 0;
+                if (v + lane < v1) {
+                    weights(v + lane, w);
+#pragma unroll
+                    for (int k = 0; k < kVec; k++) mine += w[k];
                 }
+                uint64_t upto = mine;  // inclusive over the lanes
+#pragma unroll
+                for (int d = 1; d < 32; d <<= 1) {
+                    const uint64_t o = __shfl_up_sync(0xffffffffu, upto, d);
+                    if (lane >= d) upto += o;
+                }
+                if (aim >= at + upto - mine && aim < at + upto) {
+                    uint64_t c = at + upto - mine;
+                    int found = -1;
+#pragma unroll
+                    for (int k = 0; k < kVec; k++) {
+                        c += w[k];
+                        if (found < 0 && c > aim) found = P.first(v + lane) + k;
+                    }
+                    a.next[b] = found;
+                }
+                at += __shfl_sync(0xffffffffu, upto, 31);
+                if (at > aim) break;
             }
         }
         break;
     }
-    __syncthreads();
-    if (tid == 0) {
-        a.accepted[b] = r - lo;
-        a.next[b] = s_token;
-    }
+    if (rank == 0 && tid == 0) a.accepted[b] = r - lo;
 }
 
-// A logit's place in the order (0: NaN, which is never the largest), then the lower index.
+// A value's place in the order (0: nothing), then the lower index.
 __device__ __forceinline__ uint64_t order_key(float x, int i) {
-    if (!(x == x)) return 0;
+    if (i < 0) return 0;
     const uint32_t u = __float_as_uint(x + 0.f);  // -0 equals +0
     const uint32_t o = (u & 0x80000000u) ? ~u : u | 0x80000000u;
     return (uint64_t)o << 32 | (0xffffffffu - (uint32_t)i);
 }
 
 template <bool BF16>
-__global__ void __launch_bounds__(kThreads) verify_greedy_kernel(const VerifyArgs a) {
-    __shared__ unsigned long long s_best;
-    const int b = blockIdx.x, tid = threadIdx.x;
+__global__ void __launch_bounds__(kThreads, 2) arg_max_kernel(const VerifyArgs a, int32_t *best) {
+    constexpr int kVec = Row<BF16>::kVec;
+    __shared__ uint64_t s_warp[kWarps];
+    __shared__ uint64_t s_cta[kMaxCluster];  // rank 0's: every CTA's best
+    const uint32_t rank = cluster_ctarank(), ranks = cluster_nctarank();
+    const int r = (int)(blockIdx.x / ranks), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    cluster_arrive();  // waited for before the remote store: by then every CTA has started
+    griddep_launch_dependents();
+    const Row<BF16> X(a.p, (size_t)r * a.ldp, a.vocab);
+    const int vectors = X.vectors();
+    float top = 0.f;
+    int at = -1;
+    // indices ascend in each thread, so only a larger value replaces (NaN never does)
+#pragma unroll 4
+    for (int v = (int)rank * kThreads + tid; v < vectors; v += (int)ranks * kThreads) {
+        float x[kVec];
+        X.load(v, __uint_as_float(0x7fc00000u), x);
+#pragma unroll
+        for (int k = 0; k < kVec; k++) {
+            if (x[k] > top || (at < 0 && x[k] == x[k])) {
+                top = x[k];
+                at = X.first(v) + k;
+            }
+        }
+    }
+    uint64_t key = order_key(top, at);
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, d));
+    if (lane == 0) s_warp[warp] = key;
+    __syncthreads();
+    cluster_wait();
+    if (warp == 0) {
+        key = lane < kWarps ? s_warp[lane] : 0;
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) key = max(key, __shfl_xor_sync(0xffffffffu, key, d));
+        if (lane == 0) store_cluster_u64(&s_cta[rank], 0, key);
+    }
+    cluster_sync();
+    if (rank == 0 && tid == 0) {
+        for (uint32_t k = 0; k < ranks; k++) key = max(key, s_cta[k]);
+        best[r] = key == 0 ? -1 : (int)(0xffffffffu - (uint32_t)key);
+    }
+}
+
+// A warp per sequence: the drafts that equal the rows' arg max.
+__global__ void __launch_bounds__(128) greedy_verdict_kernel(const VerifyArgs a, const int32_t *best) {
+    griddep_wait();
+    const int b = (int)(blockIdx.x * 4 + threadIdx.x / 32), lane = threadIdx.x & 31;
+    if (b >= a.seqs) return;
     int lo, hi;
     const bool ok = seq_rows(a.cu_rows, b, a.rows, lo, hi);
-    if (!ok || lo == hi) {
-        if (tid == 0) {
-            if (!ok) set_status(a.st, MOE_ERR_BAD_PAGE, 1);
-            a.accepted[b] = 0;
-            a.next[b] = -1;
+    if (!ok && lane == 0) set_status(a.st, MOE_ERR_BAD_PAGE, 1);
+    int r = hi - 1;
+    for (int r0 = lo; r0 < hi - 1; r0 += 32) {
+        const int k = r0 + lane;
+        const bool bad = k < hi - 1 && (best[k] < 0 || best[k] != a.tokens[k + 1]);
+        const uint32_t m = __ballot_sync(0xffffffffu, bad);
+        if (m != 0u) {
+            r = r0 + __ffs((int)m) - 1;
+            break;
         }
-        return;
     }
-    int r = lo, best = -1;
-    for (; r < hi; r++) {
-        if (tid == 0) s_best = 0;
-        __syncthreads();
-        uint64_t key = 0;
-        for (int i = tid; i < a.vocab; i += kThreads)
-            key = max(key, order_key(load_value<BF16>(a.p, (size_t)r * a.ldp + i), i));
-        atomicMax(&s_best, (unsigned long long)key);
-        __syncthreads();
-        best = s_best == 0 ? -1 : (int)(0xffffffffu - (uint32_t)s_best);
-        __syncthreads();
-        if (r == hi - 1 || a.tokens[r + 1] != best || best < 0) break;
+    if (lane == 0) {
+        a.accepted[b] = lo < hi ? r - lo : 0;
+        a.next[b] = lo < hi ? best[r] : -1;
     }
-    if (tid == 0) {
-        a.accepted[b] = r - lo;
-        a.next[b] = best;
-    }
+}
+
+PerDevice g_sms(0);
+
+// CTAs per cluster for `units` clusters: as many as fill the device at four CTAs of 512
+// threads per SM, 8 at most (the portable size).
+int cluster_size(int units, int sms) {
+    int c = kMaxCluster;
+    while (c > 1 && (int64_t)units * c > 4 * (int64_t)sms) c /= 2;
+    return c;
+}
+
+cudaLaunchConfig_t cluster_config(cudaLaunchAttribute *attr, int units, int c, cudaStream_t st) {
+    cudaLaunchConfig_t cfg = {};
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(units * c));
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = st;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cfg;
 }
 
 }  // namespace
 
-size_t verify_workspace_bytes(int, int) { return sizeof(StatusWord); }
+// The status word, then each row's arg max (greedy).
+size_t verify_workspace_bytes(int, int rows) { return sizeof(StatusWord) + align_up((size_t)rows * sizeof(int32_t), 256); }
 
 cudaError_t launch_verify_sampled(const VerifyArgs &a, void *, cudaStream_t st) {
     if (a.seqs == 0) return cudaSuccess;
+    int sms = 0;
+    const cudaError_t e = device_attr(cudaDevAttrMultiProcessorCount, g_sms, &sms);
+    if (e != cudaSuccess) return e;
+    cudaLaunchAttribute attr[1];
+    const cudaLaunchConfig_t cfg = cluster_config(attr, a.seqs, cluster_size(a.seqs, sms), st);
     TraceScope trace_scope("verify_sampled", st);
-    if (a.bf16)
-        verify_sampled_kernel<true><<<a.seqs, kThreads, 0, st>>>(a);
-    else
-        verify_sampled_kernel<false><<<a.seqs, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    return a.bf16 ? cudaLaunchKernelEx(&cfg, verify_sampled_kernel<true>, a)
+                  : cudaLaunchKernelEx(&cfg, verify_sampled_kernel<false>, a);
 }
 
-cudaError_t launch_verify_greedy(const VerifyArgs &a, void *, cudaStream_t st) {
+cudaError_t launch_verify_greedy(const VerifyArgs &a, void *ws, cudaStream_t st) {
     if (a.seqs == 0) return cudaSuccess;
+    int sms = 0;
+    cudaError_t e = device_attr(cudaDevAttrMultiProcessorCount, g_sms, &sms);
+    if (e != cudaSuccess) return e;
+    int32_t *best = reinterpret_cast<int32_t *>(static_cast<char *>(ws) + sizeof(StatusWord));
     TraceScope trace_scope("verify_greedy", st);
-    if (a.bf16)
-        verify_greedy_kernel<true><<<a.seqs, kThreads, 0, st>>>(a);
-    else
-        verify_greedy_kernel<false><<<a.seqs, kThreads, 0, st>>>(a);
-    return cudaGetLastError();
+    if (a.rows > 0) {
+        cudaLaunchAttribute attr[1];
+        const cudaLaunchConfig_t cfg = cluster_config(attr, a.rows, cluster_size(a.rows, sms), st);
+        e = a.bf16 ? cudaLaunchKernelEx(&cfg, arg_max_kernel<true>, a, best)
+                   : cudaLaunchKernelEx(&cfg, arg_max_kernel<false>, a, best);
+        if (e != cudaSuccess) return e;
+    }
+    return launch_pdl(greedy_verdict_kernel, dim3((unsigned)((a.seqs + 3) / 4)), dim3(128), 0, st, a,
+                      (const int32_t *)best);
 }
 
 }  // namespace moe
