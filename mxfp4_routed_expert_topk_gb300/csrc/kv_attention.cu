@@ -387,19 +387,20 @@ __global__ void __launch_bounds__(32 * kFirstSoft + 128 * groups_of(R), 1)
 #pragma unroll
             for (int w = 0; w < kGroups; w++) {
                 const float mw = mrow[w * R + row], *lw = lsum + 4 * w * R + row;
-                const float f = mw == -INFINITY ? 0.f : ex2(mw - m);
-                l += f * ((lw[0] + lw[R]) + (lw[2 * R] + lw[3 * R]));
+                const float lsum4 = (lw[0] + lw[R]) + (lw[2 * R] + lw[3 * R]);
+                const float f = lsum4 == 0.f ? 0.f : ex2(mw - m);  // (sum 0: it saw nothing; NaN stays)
+                l += lsum4 == 0.f ? 0.f : f * lsum4;
                 if (w == wg) ab[row].x = f;
             }
             float *part = sg->parts > 1 ? a.part + (size_t)(2 * (int)blockIdx.x + (tile0 == 0 ? 1 : 0)) * slot_floats
                                          : nullptr;
-            if (part == nullptr && wg == 0) ab[row].y = m == -INFINITY ? 0.f : 1.f / l;
+            if (part == nullptr && wg == 0) ab[row].y = l == 0.f ? 0.f : 1.f / l;
             if (sw == 0 && (lane * R & 31) < R && rows[row].row >= 0 && *(volatile int *)abort_flag == 0) {  // one lane per row
                 if (part != nullptr)
                     *reinterpret_cast<float2 *>(part + (size_t)R * D + 2 * row) = make_float2(m, l);
                 else if (a.k.lse != nullptr)
                     a.k.lse[(size_t)rows[row].row * a.k.heads_q + rows[row].head] =
-                        m == -INFINITY ? -INFINITY : kLn2 * (m + log2f(l));
+                        l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
             }
             __syncwarp();
 #pragma unroll

@@ -818,7 +818,7 @@ __device__ __forceinline__ void join_role(const AttnArgs &a, const Share &S, con
             for (int p = lane + 32; p < parts; p += 32) m = fmaxf(m, __ldcg(slot_of(p) + (size_t)a.rpt * D + 2 * r));
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-            const float mine = ml.x == -INFINITY ? 0.f : ex2(ml.x - m);
+            const float mine = ml.y == 0.f ? 0.f : ex2(ml.x - m);  // (sum 0: it saw nothing; NaN stays)
 #pragma unroll 1
             for (int p = 0; p < parts; p += U) {
 #pragma unroll
@@ -830,7 +830,7 @@ __device__ __forceinline__ void join_role(const AttnArgs &a, const Share &S, con
                         s = __shfl_sync(0xffffffffu, ml.y, p + i);
                     } else {
                         const float2 t = __ldcg(reinterpret_cast<const float2 *>(slot_of(p + i) + (size_t)a.rpt * D + 2 * r));
-                        f = t.x == -INFINITY ? 0.f : ex2(t.x - m);
+                        f = t.y == 0.f ? 0.f : ex2(t.x - m);
                         s = t.y;
                     }
                     l = fmaf(s, f, l);
@@ -843,12 +843,12 @@ __device__ __forceinline__ void join_role(const AttnArgs &a, const Share &S, con
             }
             const int R = g.rt * a.rpt + r, qi = R / a.group, row = g.row0 + qi;
             const int hq = g.head * a.group + R - qi * a.group;
-            const float inv = m == -INFINITY ? 0.f : 1.f / l;
+            const float inv = l == 0.f ? 0.f : 1.f / l;
             uint16_t *out = a.k.out + (size_t)row * a.k.ldo + (size_t)hq * D + lane * V;
 #pragma unroll
             for (int j = 0; j < V; j++) out[j] = __bfloat16_as_ushort(__float2bfloat16(acc[j] * inv));
             if (a.k.lse != nullptr && lane == 0)
-                a.k.lse[(size_t)row * a.k.heads_q + hq] = m == -INFINITY ? -INFINITY : kLn2 * (m + log2f(l));
+                a.k.lse[(size_t)row * a.k.heads_q + hq] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
         }
     }
     named_barrier(bar_id, NSOFT);

@@ -148,92 +148,92 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
 
     if (warp < kFirstSoft) {
         regs_dec<kRegsIssue>();
-    if (warp == 0) {
-        copy_role<D, 0>(a, &tm, smem, L, B, abort_flag);
-    } else if (warp == 2) {
-        copy_role<D, 1>(a, &tm, smem, L, B, abort_flag);
-    } else if (warp == 1) {
-        // ------------------------------------------------------ MMA issue
-        const uint32_t id_s = idesc_f8(kRows, kTokens, false, false), id_o = idesc_f8(kRows, D, false, true);
-        const uint64_t kd = smem_desc(smem_u32(smem + L.k), 16, kGroup8, kSwz);
-        const uint64_t vd = smem_desc(smem_u32(smem + L.v), kGroup8, kGroup8, kSwz);
-        const uint64_t qd = smem_desc(smem_u32(smem + L.q), 16, kGroup8, kSwz);
-        int ks = 0, vs = 0;  // stages
-        int ns = 0, np = 0, seg = 0, seg_end = 0, qb = 0;  // scores / outputs issued
-        int bs = 0, bp = 0;                                // and their buffers
-        bool last = false;                                 // seg_end is the share's end
-        const uint32_t elected = elect_one();
-        // Whichever is ready: the outputs of tile np, the scores of tile ns (over the weights of
-        // tile ns - 3, whose outputs have been issued; with the segment's queries).  Lanes 0 to 4
-        // look at one barrier each; a vote makes the outcome uniform, which keeps the descriptors
-        // in uniform registers.
-        Watch eye = lane == 0   ? Watch{B.p_ready(0), kSBufs, 0, 0u}
-                    : lane == 1 ? Watch{B.v_full(0), a.nv, 0, 0u}
-                    : lane == 2 ? Watch{B.o_empty(0), 1, 0, 1u}
-                    : lane == 3 ? Watch{B.k_full(0), a.nk, 0, 0u}
-                                : Watch{B.q_full(0), 2, 0, 0u};
-        uint64_t idle = 0;  // since when nothing has been ready
-        while (!(last && np == seg_end)) {
-            const uint32_t m = __ballot_sync(0xffffffffu, lane < 5 && eye.ready());
-            const bool out = np < ns && (m & 7u) == 7u;
-            if (ns == seg_end && !last && (m & 16u) != 0u) {  // the next segment's queries are there
-                const volatile Seg *sg = reinterpret_cast<const volatile Seg *>(smem + L.seg) + seg % kSegs;
-                const int count = __shfl_sync(0xffffffffu, sg->count, 0);
-                qb = seg & 1;
-                seg_end += count;
-                last = __any_sync(0xffffffffu, count == 0);
-                seg++;
-                if (lane == 4) eye.next();
+        if (warp == 0) {
+            copy_role<D, 0>(a, &tm, smem, L, B, abort_flag);
+        } else if (warp == 2) {
+            copy_role<D, 1>(a, &tm, smem, L, B, abort_flag);
+        } else if (warp == 1) {
+            // ------------------------------------------------------ MMA issue
+            const uint32_t id_s = idesc_f8(kRows, kTokens, false, false), id_o = idesc_f8(kRows, D, false, true);
+            const uint64_t kd = smem_desc(smem_u32(smem + L.k), 16, kGroup8, kSwz);
+            const uint64_t vd = smem_desc(smem_u32(smem + L.v), kGroup8, kGroup8, kSwz);
+            const uint64_t qd = smem_desc(smem_u32(smem + L.q), 16, kGroup8, kSwz);
+            int ks = 0, vs = 0;  // stages
+            int ns = 0, np = 0, seg = 0, seg_end = 0, qb = 0;  // scores / outputs issued
+            int bs = 0, bp = 0;                                // and their buffers
+            bool last = false;                                 // seg_end is the share's end
+            const uint32_t elected = elect_one();
+            // Whichever is ready: the outputs of tile np, the scores of tile ns (over the weights of
+            // tile ns - 3, whose outputs have been issued; with the segment's queries).  Lanes 0 to 4
+            // look at one barrier each; a vote makes the outcome uniform, which keeps the descriptors
+            // in uniform registers.
+            Watch eye = lane == 0   ? Watch{B.p_ready(0), kSBufs, 0, 0u}
+                        : lane == 1 ? Watch{B.v_full(0), a.nv, 0, 0u}
+                        : lane == 2 ? Watch{B.o_empty(0), 1, 0, 1u}
+                        : lane == 3 ? Watch{B.k_full(0), a.nk, 0, 0u}
+                                    : Watch{B.q_full(0), 2, 0, 0u};
+            uint64_t idle = 0;  // since when nothing has been ready
+            while (!(last && np == seg_end)) {
+                const uint32_t m = __ballot_sync(0xffffffffu, lane < 5 && eye.ready());
+                const bool out = np < ns && (m & 7u) == 7u;
+                if (ns == seg_end && !last && (m & 16u) != 0u) {  // the next segment's queries are there
+                    const volatile Seg *sg = reinterpret_cast<const volatile Seg *>(smem + L.seg) + seg % kSegs;
+                    const int count = __shfl_sync(0xffffffffu, sg->count, 0);
+                    qb = seg & 1;
+                    seg_end += count;
+                    last = __any_sync(0xffffffffu, count == 0);
+                    seg++;
+                    if (lane == 4) eye.next();
+                }
+                const bool scores = ns < seg_end && ns < np + (out ? 1 : 0) + kSBufs && (m & 8u) != 0u;
+                if (!out && !scores) {
+                    if (__any_sync(0xffffffffu, expired(idle, 0xb00u, abort_flag))) break;
+                    continue;
+                }
+                idle = 0;
+                tc_fence_after();
+                if (out) {
+                    const uint64_t va = vd + (uint64_t)((uint32_t)vs * kTile >> 4);
+                    const uint32_t p = tmem + (uint32_t)(bp * kTokens);
+                    // 32 tokens take 8 columns per part: the parts of each 32 lie side by side
+    #pragma unroll
+                    for (int part = 0; part < 2; part++)
+    #pragma unroll
+                        for (int k = 0; k < kTokens / 32; k++)
+                            tc_mma_f8_ts(tmem_o, p + (uint32_t)(16 * k + 8 * part),
+                                         va + (uint64_t)(k * (32 * D) >> 4), id_o, (part > 0 || k > 0) ? 1u : 0u, elected);
+                    tc_commit_elected(B.v_empty(vs), elected);
+                    tc_commit_elected(B.o_full(0), elected);
+                    if (++vs == a.nv) vs = 0;
+                    if (++bp == kSBufs) bp = 0;
+                    np++;
+                    if (lane < 3) eye.next();
+                }
+                if (scores) {
+                    const uint64_t ka = kd + (uint64_t)((uint32_t)ks * kTile >> 4);
+                    const uint64_t qa = qd + (uint64_t)((uint32_t)qb * (2u * kRows * D) >> 4);
+    #pragma unroll
+                    for (int part = 0; part < 2; part++)
+    #pragma unroll
+                        for (int k = 0; k < D / 32; k++)
+                            tc_mma_f8(tmem + (uint32_t)(bs * kTokens),
+                                      qa + (uint64_t)(part * (kRows * D) >> 4) + (uint64_t)(2 * k), ka + (uint64_t)(2 * k),
+                                      id_s, (part > 0 || k > 0) ? 1u : 0u, elected);
+                    tc_commit_elected(B.k_empty(ks), elected);
+                    tc_commit_elected(B.s_full(bs), elected);
+                    if (++ks == a.nk) ks = 0;
+                    if (++bs == kSBufs) bs = 0;
+                    ns++;
+                    if (lane == 3) eye.next();
+                }
             }
-            const bool scores = ns < seg_end && ns < np + (out ? 1 : 0) + kSBufs && (m & 8u) != 0u;
-            if (!out && !scores) {
-                if (__any_sync(0xffffffffu, expired(idle, 0xb00u, abort_flag))) break;
-                continue;
-            }
-            idle = 0;
-            tc_fence_after();
-            if (out) {
-                const uint64_t va = vd + (uint64_t)((uint32_t)vs * kTile >> 4);
-                const uint32_t p = tmem + (uint32_t)(bp * kTokens);
-                // 32 tokens take 8 columns per part: the parts of each 32 lie side by side
-#pragma unroll
-                for (int part = 0; part < 2; part++)
-#pragma unroll
-                    for (int k = 0; k < kTokens / 32; k++)
-                        tc_mma_f8_ts(tmem_o, p + (uint32_t)(16 * k + 8 * part),
-                                     va + (uint64_t)(k * (32 * D) >> 4), id_o, (part > 0 || k > 0) ? 1u : 0u, elected);
-                tc_commit_elected(B.v_empty(vs), elected);
-                tc_commit_elected(B.o_full(0), elected);
-                if (++vs == a.nv) vs = 0;
-                if (++bp == kSBufs) bp = 0;
-                np++;
-                if (lane < 3) eye.next();
-            }
-            if (scores) {
-                const uint64_t ka = kd + (uint64_t)((uint32_t)ks * kTile >> 4);
-                const uint64_t qa = qd + (uint64_t)((uint32_t)qb * (2u * kRows * D) >> 4);
-#pragma unroll
-                for (int part = 0; part < 2; part++)
-#pragma unroll
-                    for (int k = 0; k < D / 32; k++)
-                        tc_mma_f8(tmem + (uint32_t)(bs * kTokens),
-                                  qa + (uint64_t)(part * (kRows * D) >> 4) + (uint64_t)(2 * k), ka + (uint64_t)(2 * k),
-                                  id_s, (part > 0 || k > 0) ? 1u : 0u, elected);
-                tc_commit_elected(B.k_empty(ks), elected);
-                tc_commit_elected(B.s_full(bs), elected);
-                if (++ks == a.nk) ks = 0;
-                if (++bs == kSBufs) bs = 0;
-                ns++;
-                if (lane == 3) eye.next();
-            }
+            if (elect_one()) tc_commit(B.mma_done());
+            __syncwarp();
+            if (lane == 0) drain(B.mma_done(), 0u, abort_flag);
+            __syncwarp();
+        } else {
+            segment_role(a, smem, L, B, S, plan, abort_flag);
         }
-        if (elect_one()) tc_commit(B.mma_done());
-        __syncwarp();
-        if (lane == 0) drain(B.mma_done(), 0u, abort_flag);
-        __syncwarp();
-    } else {
-        segment_role(a, smem, L, B, S, plan, abort_flag);
-    }
     } else if (warp < kJoinWarp) {
         regs_dec<kRegsSoft>();
         // -------------------------------------------------------- softmax
@@ -464,7 +464,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                         *reinterpret_cast<float4 *>(d + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                     *reinterpret_cast<float2 *>(part + (size_t)a.rpt * D + 2 * row) = make_float2(m_run, l_run);
                 } else {
-                    const float inv = m_run == -INFINITY ? 0.f : 1.f / l_run;
+                    const float inv = l_run == 0.f ? 0.f : 1.f / l_run;  // (sum 0: it saw nothing; NaN stays)
                     uint16_t *d = a.k.out + (size_t)ri.row * a.k.ldo + (size_t)ri.head * D;
 #pragma unroll
                     for (int i = 0; i < D; i += 8) {
@@ -478,7 +478,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                     }
                     if (a.k.lse != nullptr)
                         a.k.lse[(size_t)ri.row * a.k.heads_q + ri.head] =
-                            m_run == -INFINITY ? -INFINITY : kLn2 * (m_run + log2f(l_run));
+                            l_run == 0.f ? -INFINITY : kLn2 * (m_run + log2f(l_run));
                 }
             }
             if (part != nullptr) {

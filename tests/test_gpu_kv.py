@@ -271,6 +271,17 @@ def test_attention_masked_tokens_do_not_reach(old, group, what):
         assert torch.isnan(seen).any()
 
 
+@pytest.mark.parametrize("n,old", [(1, 0), (1, 300), (9, 0), (9, 300)])
+def test_attention_shows_nan_that_a_row_sees(n, old):
+    """A NaN key is in every row that sees it, even where it is all the row sees."""
+    c = Case([n], [old], 1, 7, 128, 16, seed=old + n)
+    at = old                                              # the first row's own token
+    c.codes_np[c.table[0, at // 16], 0, 0, at % 16, 7] = 0x7F
+    c.upload()
+    out, lse = c.run()
+    assert torch.isnan(out).all() and torch.isnan(lse).all()
+
+
 def test_attention_wide_range_of_weights():
     """One token far above the rest, and a long tail of tiny weights that together matter."""
     c = Case([1], [3000], 1, 4, 128, 64, seed=11)
