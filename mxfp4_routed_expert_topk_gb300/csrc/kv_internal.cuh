@@ -63,8 +63,9 @@ struct KvAppendArgs {
     const int32_t *cu_rows, *start, *page_table;
     int table_width, seqs;
     StatusWord *st;
+    int units;  // (side, head) pairs a block takes (set by the launch)
 };
-cudaError_t launch_kv_append(const KvAppendArgs &a, cudaStream_t st);
+cudaError_t launch_kv_append(KvAppendArgs a, cudaStream_t st);
 
 struct KvAttentionArgs {
     KvView kv;
