@@ -27,13 +27,28 @@ constexpr int kMaxCluster = 8;
 constexpr int kGrid = 38;       // probabilities are whole multiples of 2^-38
 constexpr int kUniform = 24;    // uniforms are whole multiples of 2^-24
 
-// floor(2^38 min(max(p, 0), 1)), NaN: 0.
-__device__ __forceinline__ uint64_t whole(float p) {
-    return __float2ull_rz(fminf(fmaxf(p, 0.f), 1.f) * 274877906944.f);
+// floor(2^38 min(max(p, 0), 1)) + kRaw, NaN: as 0.  The whole part of 2^15 p and that of 2^23
+// times the rest appear in the mantissas of sums with 2^23 that are rounded towards zero: six
+// instructions at full rate, where a conversion to 64-bit integers alone takes twice their time.
+constexpr uint64_t kRaw = (0x4b000000ull << 23) + 0x4b000000ull;
+__device__ __forceinline__ uint64_t whole_raw(float p) {
+    const float x = __saturatef(p);
+    const float hi = __fmaf_rz(x, 32768.f, 8388608.f);
+    const float rest = fmaf(x, 32768.f, 8388608.f - hi);  // exact
+    const float lo = __fmaf_rz(rest, 8388608.f, 8388608.f);
+    return ((uint64_t)__float_as_uint(hi) << 23) + __float_as_uint(lo);
 }
+__device__ __forceinline__ uint64_t whole(float p) { return whole_raw(p) - kRaw; }
 
 __device__ __forceinline__ uint64_t whole_uniform(float u) {
     return (uint64_t)__float2uint_rz(fminf(fmaxf(u, 0.f), 0.99999994f) * 16777216.f);
+}
+
+// Larger of two pairs of bf16 values, each by itself; NaN only if both are.
+__device__ __forceinline__ uint32_t max2_bf16(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("max.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
 }
 
 // A row of n values, cut into vectors of 16 bytes on 16-byte boundaries: vector 0 is the
@@ -54,6 +69,23 @@ struct Row {
     __device__ __forceinline__ bool whole_vector(int v) const { return first(v) >= 0 && first(v) + kVec <= n; }
     __device__ __forceinline__ float at(int i) const {
         return BF16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t *>(p)[i]) : reinterpret_cast<const float *>(p)[i];
+    }
+    // largest value of vector v (NaN if it has none)
+    __device__ __forceinline__ float largest(int v) const {
+        if constexpr (BF16) {
+            const int i0 = first(v);
+            if (i0 >= 0 && i0 + kVec <= n) {
+                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p + (ptrdiff_t)i0 * kSize));
+                const uint32_t m = max2_bf16(max2_bf16(u.x, u.y), max2_bf16(u.z, u.w));
+                return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
+            }
+        }
+        float x[kVec], m;
+        load(v, __uint_as_float(0x7fc00000u), x);
+        m = x[0];
+#pragma unroll
+        for (int k = 1; k < kVec; k++) m = fmaxf(m, x[k]);
+        return m;
     }
     // the values of vector v (`none` outside the row)
     __device__ __forceinline__ void load(int v, float none, float (&x)[kVec]) const {
@@ -158,14 +190,21 @@ __global__ void __launch_bounds__(kThreads, 2) verify_sampled_kernel(const Verif
                 for (int k = 0; k < kVec; k++) y[k] = i0 + k >= 0 && i0 + k < a.vocab ? Q.at(i0 + k) : 0.f;
             }
         }
+        if (minus) {
 #pragma unroll
-        for (int k = 0; k < kVec; k++) {
-            w[k] = whole(x[k]);
-            if (minus) {
-                const uint64_t z = whole(y[k]);
-                w[k] = w[k] > z ? w[k] - z : 0;
+            for (int k = 0; k < kVec; k++) {
+                const int64_t d = (int64_t)(whole_raw(x[k]) - whole_raw(y[k]));
+                w[k] = d > 0 ? (uint64_t)d : 0;
             }
-            if (P.first(v) + k == drop) w[k] = 0;
+        } else {
+#pragma unroll
+            for (int k = 0; k < kVec; k++) w[k] = whole(x[k]);
+        }
+        const uint32_t at = (uint32_t)(drop - P.first(v));
+        if (drop >= 0 && at < (uint32_t)kVec) {
+#pragma unroll
+            for (int k = 0; k < kVec; k++)
+                if (at == (uint32_t)k) w[k] = 0;
         }
     };
 
@@ -261,20 +300,26 @@ __global__ void __launch_bounds__(kThreads, 2) arg_max_kernel(const VerifyArgs a
     griddep_launch_dependents();
     const Row<BF16> X(a.p, (size_t)r * a.ldp, a.vocab);
     const int vectors = X.vectors();
-    float top = 0.f;
-    int at = -1;
-    // indices ascend in each thread, so only a larger value replaces (NaN never does)
+    // The largest value of each vector (NaN is passed over) and the first vector that has it;
+    // vectors ascend in each thread, so only a larger one replaces.  Its place is looked up at the
+    // end: 1.5 instructions a value in place of 5.
+    float top = __uint_as_float(0x7fc00000u);  // none
+    int best_v = -1;
 #pragma unroll 4
     for (int v = (int)rank * kThreads + tid; v < vectors; v += (int)ranks * kThreads) {
-        float x[kVec];
-        X.load(v, __uint_as_float(0x7fc00000u), x);
-#pragma unroll
-        for (int k = 0; k < kVec; k++) {
-            if (x[k] > top || (at < 0 && x[k] == x[k])) {
-                top = x[k];
-                at = X.first(v) + k;
-            }
+        const float m = X.largest(v);
+        if (!(m <= top) && m == m) {
+            top = m;
+            best_v = v;
         }
+    }
+    int at = -1;
+    if (best_v >= 0) {
+        float x[kVec];
+        X.load(best_v, __uint_as_float(0x7fc00000u), x);
+#pragma unroll
+        for (int k = kVec - 1; k >= 0; k--)
+            if (x[k] == top) at = X.first(best_v) + k;
     }
     uint64_t key = order_key(top, at);
 #pragma unroll
