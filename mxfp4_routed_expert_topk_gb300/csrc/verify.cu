@@ -7,8 +7,8 @@
 // Sampled: a cluster of CTAs per sequence.  Every CTA finds the deciding row by itself (a lane
 // per draft: two gathers, a whole-number comparison, a vote), so nothing is exchanged for it;
 // then each warp sums the weights of its own consecutive part of that row, the CTAs' sums are
-// exchanged through distributed shared memory, and the one warp whose part holds the drawn
-// point scans it again (it is in L1 / L2).  Weights are whole numbers of 38 bits, so the sums
+// exchanged through distributed shared memory, and the CTA that has the drawn point divides the
+// part of the warp that holds it among all its warps and scans it again (it is in L1 / L2).  Weights are whole numbers of 38 bits, so the sums
 // are exact in any order and the result is the definition's, bit for bit.
 //
 // Greedy: a cluster per row finds its arg max (all rows at once: waiting for a row's verdict
@@ -146,7 +146,7 @@ template <bool BF16>
 __global__ void __launch_bounds__(kThreads, 2) verify_sampled_kernel(const VerifyArgs a) {
     constexpr int kVec = Row<BF16>::kVec;
     __shared__ int s_row;
-    __shared__ uint64_t s_warp[kWarps];
+    __shared__ uint64_t s_warp[2][kWarps];
     __shared__ uint64_t s_cta[2][kMaxCluster];  // [round][rank]: every CTA's sum
     const uint32_t rank = cluster_ctarank(), ranks = cluster_nctarank();
     const int b = (int)(blockIdx.x / ranks), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -208,10 +208,11 @@ __global__ void __launch_bounds__(kThreads, 2) verify_sampled_kernel(const Verif
         }
     };
 
-    for (int round = 0; round < 2; round++) {
+    // the weights of vectors [v, end), by one warp
+    auto sum_of = [&](int v, int end) {
         uint64_t sum = 0;
 #pragma unroll 2
-        for (int v = v0 + lane; v < v1; v += 32) {
+        for (v += lane; v < end; v += 32) {
             uint64_t w[kVec];
             weights(v, w);
 #pragma unroll
@@ -219,19 +220,21 @@ __global__ void __launch_bounds__(kThreads, 2) verify_sampled_kernel(const Verif
         }
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, d);
-        if (lane == 0) s_warp[warp] = sum;
+        return sum;
+    };
+
+    for (int round = 0; round < 2; round++) {
+        const uint64_t sum = sum_of(v0, v1);
+        if (lane == 0) s_warp[0][warp] = sum;
         __syncthreads();
-        uint64_t cta = 0, before = 0;  // this CTA's sum; what its warps before this one hold
+        uint64_t cta = 0;
 #pragma unroll
-        for (int w = 0; w < kWarps; w++) {
-            if (w < warp) before += s_warp[w];
-            cta += s_warp[w];
-        }
+        for (int w = 0; w < kWarps; w++) cta += s_warp[0][w];
         if (round == 0) cluster_wait();
         // every CTA writes its sum into all (nothing is read remotely, so none waits to exit)
         if (tid < (int)ranks) store_cluster_u64(&s_cta[round][rank], (uint32_t)tid, cta);
         cluster_sync();
-        uint64_t total = 0;
+        uint64_t total = 0, before = 0;  // all weights; what the CTAs before this one hold
         for (uint32_t k = 0; k < ranks; k++) {
             if (k < rank) before += s_cta[round][k];
             total += s_cta[round][k];
@@ -247,11 +250,21 @@ __global__ void __launch_bounds__(kThreads, 2) verify_sampled_kernel(const Verif
         }
         const uint64_t m = whole_uniform(a.u_sample[b]);
         const uint64_t aim = (total >> kUniform) * m + (((total & ((1ull << kUniform) - 1)) * m) >> kUniform);
-        if (aim >= before && aim < before + sum) {  // in this warp's part
+        if (aim < before || aim >= before + cta) break;  // in another CTA's part
+        // the warp whose part holds the point; the CTA's warps divide that part
+        int w = 0;
+        for (; w < kWarps - 1 && aim >= before + s_warp[0][w]; w++) before += s_warp[0][w];
+        const int a0 = min(((int)rank * kWarps + w) * per, vectors), a1 = min(a0 + per, vectors);
+        const int sub = (a1 - a0 + kWarps - 1) / kWarps, b0 = min(a0 + warp * sub, a1), b1 = min(b0 + sub, a1);
+        const uint64_t part = sum_of(b0, b1);
+        if (lane == 0) s_warp[1][warp] = part;
+        __syncthreads();
+        for (int k = 0; k < warp; k++) before += s_warp[1][k];
+        if (aim >= before && aim < before + part) {
             uint64_t at = before;
-            for (int v = v0; v < v1; v += 32) {
+            for (int v = b0; v < b1; v += 32) {
                 uint64_t w[kVec], mine = 0;
-                if (v + lane < v1) {
+                if (v + lane < b1) {
                     weights(v + lane, w);
 #pragma unroll
                     for (int k = 0; k < kVec; k++) mine += w[k];
@@ -366,11 +379,13 @@ __global__ void __launch_bounds__(128) greedy_verdict_kernel(const VerifyArgs a,
 
 PerDevice g_sms(0);
 
-// CTAs per cluster for `units` clusters: as many as fill the device at four CTAs of 512
-// threads per SM, 8 at most (the portable size).
+// CTAs per cluster for `units` clusters: as many as fit the device at once (two CTAs of 512
+// threads per SM), 8 at most (the portable size).  With cold caches, 1 / 2 / 4 / 8 CTAs: 64
+// sequences (131071 values) 64 / 39 / 31 / 33 us; 96 (65536 16-bit values) 23 / 19 / 23 / 27;
+// 136 rows' arg max (131072 16-bit values) 23 / 19 / 21 / 25; one sequence 23 / 17 / 15 / 13.
 int cluster_size(int units, int sms) {
     int c = kMaxCluster;
-    while (c > 1 && (int64_t)units * c > 4 * (int64_t)sms) c /= 2;
+    while (c > 1 && (int64_t)units * c > 2 * (int64_t)sms) c /= 2;
     return c;
 }
 
