@@ -22,14 +22,14 @@ namespace moe {
 namespace {
 
 constexpr int kBarAll = 7;  // named barrier of all softmax threads (warpgroup w: 1 + w)
-// Softmax warpgroups for R rows: as many as the registers allow (R running outputs a thread).
-__host__ __device__ constexpr int groups_of(int r) { return r <= 16 ? 4 : 3; }
+// Softmax warpgroups.  Four (for 16 rows; 32 take more registers than that leaves) were slower:
+// 96 sequences of 512 tokens 66 us in place of 62, one of 300 tokens 23 in place of 21 (cold).
+constexpr int kGroups = 3;
 
 struct FewSmem {
     CommonSmem c;
     uint32_t p, smax, ref, ab, lsum, mrow, nan, total;
     __host__ __device__ FewSmem(int dim, int r, int nk, int nv) : c(dim, r, nk, nv) {
-        const uint32_t kGroups = groups_of(r);
         uint32_t o = (c.total + 127u) & ~127u;
         p = o;     o += (uint32_t)kGroups * 2u * r * kTokens;       // [group][part][r / 16][128][16]
         smax = o;  o += (uint32_t)kGroups * 2u * 4u * r * 4u;       // [group][2][warp][r]
@@ -69,9 +69,9 @@ __device__ __forceinline__ float warp_max(float x) {
 }
 
 template <int D, int R>
-__global__ void __launch_bounds__(32 * kFirstSoft + 128 * groups_of(R), 1)
+__global__ void __launch_bounds__(32 * kFirstSoft + 128 * kGroups, 1)
     kv_attention_few_kernel(const __grid_constant__ CUtensorMap tm, const AttnArgs a) {
-    constexpr int kGroups = groups_of(R), kSoft = 128 * kGroups, kThreads = 32 * kFirstSoft + kSoft;
+    constexpr int kSoft = 128 * kGroups, kThreads = 32 * kFirstSoft + kSoft;
     constexpr uint32_t kTile = kTokens * D;  // bytes of a K or V tile
     constexpr uint32_t kSwz = D == 128 ? kSwizzle128B : kSwizzle64B;
     constexpr uint32_t kGroup8 = 8 * D;      // bytes of 8 rows
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(32 * kFirstSoft + 128 * groups_of(R), 1)
                 l += lsum4 == 0.f ? 0.f : f * lsum4;
                 if (w == wg) ab[row].x = f;
             }
-            float *part = sg->parts > 1 ? a.part + (size_t)(2 * (int)blockIdx.x + (tile0 == 0 ? 1 : 0)) * slot_floats
+            float *part = count < sg->nt ? a.part + (size_t)(2 * (int)blockIdx.x + (tile0 == 0 ? 1 : 0)) * slot_floats
                                          : nullptr;
             if (part == nullptr && wg == 0) ab[row].y = l == 0.f ? 0.f : 1.f / l;
             if (sw == 0 && (lane * R & 31) < R && rows[row].row >= 0 && *(volatile int *)abort_flag == 0) {  // one lane per row
@@ -466,13 +466,13 @@ int rows_per_tile(int max_rows, int group) {
 template <int D, int R>
 cudaError_t launch_few(const CUtensorMap &tm, AttnArgs a, int sms, int smem_max, cudaStream_t st) {
     static PerDevice smem_set(0);
-    a.over = 6;
+    a.over = 8;
     // as many stages as fit, values ahead of keys (a value stage is held for the whole softmax)
     a.nk = 2;
     a.nv = 3;
     while (true) {
         AttnArgs b = a;
-        if (b.nv < kMaxStages && b.nv < b.nk + groups_of(R))
+        if (b.nv < kMaxStages && b.nv < b.nk + kGroups)
             b.nv++;
         else if (b.nk < kMaxStages)
             b.nk++;
@@ -487,7 +487,7 @@ cudaError_t launch_few(const CUtensorMap &tm, AttnArgs a, int sms, int smem_max,
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)sms);
-    cfg.blockDim = dim3(32 * kFirstSoft + 128 * groups_of(R));
+    cfg.blockDim = dim3(32 * kFirstSoft + 128 * kGroups);
     cfg.dynamicSmemBytes = smem;
     cfg.stream = st;
     cudaLaunchAttribute attr[1];

@@ -62,7 +62,8 @@ struct Seg {
     int b, rt, n, len, row0, head, tile0;
     int count;             // tiles; 0: the share ends here
     int see_all, see_max;  // tokens that every row of the tile sees, and that any row sees
-    int c0, parts;         // the CTAs that share the unit: the first, and how many (1: this one has it all)
+    int nt;                // the unit's tiles: more than `count` if other CTAs have some of them
+    int64_t u0;            // position of its first tile on the line
 };
 constexpr int kSegs = 4;   // ring of segments
 
@@ -115,15 +116,16 @@ struct Share {
 };
 
 // The line of units: a unit is one (item, head), `over` positions that stand for its fixed
-// cost, then its tiles.  Cut it into equal shares (all threads; `mem`: 2 + NT / 32 words of
-// shared memory, the first two of which then hold the first position and number of the item
-// that lo lies in, after the caller's next barrier).
+// cost, then its tiles.  Cut it into equal shares (all threads; `mem`: kPlanWords + NT / 32 words
+// of shared memory, the first of which then hold the first position, number and description of
+// the item that lo lies in, after the caller's next barrier).
+constexpr int kPlanWords = 2 + (int)(sizeof(Item) + 7) / 8;
 __device__ __forceinline__ int unit_length(const AttnArgs &a, const Item &x) { return x.nt == 0 ? 0 : x.nt + a.over; }
 
 template <int NT>
 __device__ __forceinline__ Share cut_shares(const AttnArgs &a, int64_t *mem) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int64_t *sums = mem + 2;
+    int64_t *sums = mem + kPlanWords;
     const int items = a.k.seqs * a.nrt;
     const int per = (items + NT - 1) / NT;
     const int i0 = min(tid * per, items), i1 = min(i0 + per, items);
@@ -142,6 +144,7 @@ __device__ __forceinline__ Share cut_shares(const AttnArgs &a, int64_t *mem) {
             if (round == 1 && s.lo >= at && s.lo < at + u) {
                 mem[0] = at;
                 mem[1] = i;
+                *reinterpret_cast<Item *>(mem + 2) = x;
             }
             at += u;
         }
@@ -526,84 +529,109 @@ __device__ __forceinline__ void copy_role(const AttnArgs &a, const CUtensorMap *
 }
 
 // ------------------------------------------------------------------ queries
-// Rows r0 .. r1-1 of a segment's row tile (one warp): their data, and their queries as two E4M3
-// parts, after a power of two that puts a row's largest value into [128, 256).
-template <int D, int R>
+// Warp w's part (of nw) of the rows of a segment's row tile: their data, and their queries as
+// two E4M3 parts, after a power of two that puts a row's largest value into [128, 256).  A
+// lane takes 8 values, so a pass covers 2 rows of 128 or 4 of 64; kBatch passes' loads are in
+// flight while the batch before is converted.  The code is kept small: it runs once per segment,
+// and fetching unrolled code costs more than the latency it hides (kBatch = 4 in place of 2:
+// 96 sequences of 512 tokens 70 us in place of 66).
+template <int D, int R, int kBatch>
 __device__ __forceinline__ void load_queries(const AttnArgs &a, unsigned char *smem, const CommonSmem &L, const Seg *sg,
-                                             int buf, int r0, int r1) {
-    constexpr int V = D / 32;  // values per lane
-    constexpr int U = 8;       // rows whose loads are in flight together
-    const int lane = threadIdx.x & 31;
+                                             int buf, int w, int nw) {
+    constexpr int kLanes = D / 8, kPass = 32 / kLanes;
+    const int lane = threadIdx.x & 31, sub = lane / kLanes, col = lane % kLanes;
     RowInfo *rows = reinterpret_cast<RowInfo *>(smem + L.rows) + buf * R;
     unsigned char *q0 = smem + L.q + (uint32_t)buf * (2u * R * D);
-    const int rt = sg->rt, head = sg->head, row0 = sg->row0, before = sg->len - sg->n;
-    const int live = sg->count == 0 ? 0 : min(a.rpt, sg->n * a.group - rt * a.rpt);  // rows of the tile
+    const int first = sg->rt * a.rpt, head0 = sg->head * a.group, row0 = sg->row0, before = sg->len - sg->n;
+    const int live = sg->count == 0 ? 0 : min(a.rpt, sg->n * a.group - first);  // rows of the tile
     // rows past the tile see nothing (their queries are what was there: nobody reads their results)
-    for (int r = max(r0, live) + lane; r < r1; r += 32) {
+    for (int r = live + 32 * w + lane; r < R; r += 32 * nw) {
         RowInfo none = {-1, 0, 1.f, -1};
         rows[r] = none;
     }
-#pragma unroll 1
-    for (; r0 < min(r1, live); r0 += U) {
-        uint32_t u[U][V / 2];
-        int row[U], hq[U];
-        // (row, head) of the first of them; the others follow without a division
-        int qi = (rt * a.rpt + r0) / a.group, hd = rt * a.rpt + r0 - qi * a.group;
+    const int per = (live + nw * kPass - 1) / (nw * kPass) * kPass;  // (whole passes: any two warps write apart)
+    const int r0 = min(w * per, live), r1 = min(r0 + per, live);
+    // this lane's row of the next pass to load, as (row, head of the group); a pass moves it on
+    int qi = (first + r0 + sub) / a.group, hd = first + r0 + sub - qi * a.group;
+    const int step_q = kPass / a.group, step_h = kPass - step_q * a.group;
+    uint4 u[kBatch];
+    int row[kBatch], hq[kBatch];
+    auto load = [&](int r) {
 #pragma unroll
-        for (int i = 0; i < U; i++) {
-            row[i] = r0 + i < live ? row0 + qi : -1;
-            hq[i] = head * a.group + hd;
-            if (++hd == a.group) {
-                hd = 0;
+        for (int i = 0; i < kBatch; i++) {
+            const bool ok = r + i * kPass + sub < r1;
+            row[i] = ok ? row0 + qi : -1;
+            hq[i] = head0 + hd;
+            u[i] = make_uint4(0u, 0u, 0u, 0u);
+            if (ok) u[i] = *reinterpret_cast<const uint4 *>(a.k.q + (size_t)row[i] * a.k.ldq + (size_t)hq[i] * D + col * 8);
+            qi += step_q;
+            hd += step_h;
+            if (hd >= a.group) {
+                hd -= a.group;
                 qi++;
             }
-            const uint16_t *src = a.k.q + (size_t)max(row[i], 0) * a.k.ldq + (size_t)hq[i] * D + lane * V;
-            if constexpr (V == 4) {
-                const uint2 x2 = row[i] >= 0 ? *reinterpret_cast<const uint2 *>(src) : make_uint2(0u, 0u);
-                u[i][0] = x2.x;
-                u[i][1] = x2.y;
-            } else {
-                u[i][0] = row[i] >= 0 ? *reinterpret_cast<const uint32_t *>(src) : 0u;
-            }
         }
+    };
+    load(r0);
+#pragma unroll 1
+    for (int r = r0; r < r1; r += kBatch * kPass) {
+        uint4 x[kBatch];
+        int at[kBatch], hx[kBatch];
 #pragma unroll
-        for (int i = 0; i < U; i++) {
-            const int r = r0 + i;
-            float h[V], l[V];
-            uint32_t amax = 0;  // over finite values
+        for (int i = 0; i < kBatch; i++) {
+            x[i] = u[i];
+            at[i] = row[i];
+            hx[i] = hq[i];
+        }
+        if (r + kBatch * kPass < r1) load(r + kBatch * kPass);
 #pragma unroll
-            for (int j = 0; j < V / 2; j++) {
-                const uint32_t m = u[i][j] & 0x7fff7fffu;
-                amax = __vmaxu2(amax, m & ~__vcmpgeu2(m, 0x7f807f80u));
+        for (int i = 0; i < kBatch; i++) {
+            const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+            uint32_t top = 0;  // largest magnitude over finite values, two columns of them
+#pragma unroll
+            for (int j = 0; j < 4; j++) top = __vmaxu2(top, v[j] & 0x7fff7fffu);
+            if (__any_sync(0xffffffffu, __vcmpgeu2(top, 0x7f807f80u) != 0u)) {
+                top = 0;
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const uint32_t m = v[j] & 0x7fff7fffu;
+                    top = __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7f807f80u));
+                }
             }
-            amax = __reduce_max_sync(0xffffffffu, max(amax & 0xffffu, amax >> 16));
-            const int up = amax == 0 ? 0 : min(126, 7 - ((int)(amax >> 7) - 127));
+            top = max(top & 0xffffu, top >> 16);
+#pragma unroll
+            for (int d = kLanes / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+            const int up = top == 0 ? 0 : min(126, 7 - ((int)(top >> 7) - 127));
             const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+            uint32_t h4[2], l4[2];
 #pragma unroll
-            for (int j = 0; j < V; j++) {
-                const uint32_t v = u[i][j / 2];
-                const float y = __uint_as_float((j & 1) ? v & 0xffff0000u : v << 16) * f;
-                h[j] = part_hi(y);
-                l[j] = y - h[j];
+            for (int j = 0; j < 2; j++) {
+                float h[4], l[4];
+#pragma unroll
+                for (int k = 0; k < 4; k++) {
+                    const uint32_t e = v[2 * j + (k >> 1)];
+                    const float y = __uint_as_float((k & 1) ? e & 0xffff0000u : e << 16) * f;
+                    h[k] = part_hi(y);
+                    l[k] = y - h[k];
+                }
+                h4[j] = e4m3x4_rn(h[0], h[1], h[2], h[3]);
+                l4[j] = e4m3x4_rn(l[0], l[1], l[2], l[3]);
             }
-            // 16-byte chunks of a row are permuted as the tensor copies permute the keys'
-            const uint32_t byte = (uint32_t)(lane * V), chunk = byte >> 4;
-            const uint32_t swz = D == 128 ? (uint32_t)(r & 7) : (uint32_t)((r >> 1) & 3);
-            unsigned char *dst = q0 + (uint32_t)r * D + ((chunk ^ swz) << 4) + (byte & 15u);
-            if constexpr (V == 4) {
-                *reinterpret_cast<uint32_t *>(dst) = e4m3x4_rn(h[0], h[1], h[2], h[3]);
-                *reinterpret_cast<uint32_t *>(dst + R * D) = e4m3x4_rn(l[0], l[1], l[2], l[3]);
-            } else {
-                *reinterpret_cast<uint16_t *>(dst) = (uint16_t)e4m3x2_rn(h[0], h[1]);
-                *reinterpret_cast<uint16_t *>(dst + R * D) = (uint16_t)e4m3x2_rn(l[0], l[1]);
-            }
-            if (lane == 0 && row[i] >= 0) {
-                RowInfo ri;
-                ri.row = row[i];
-                ri.head = hq[i];
-                ri.qs = __uint_as_float((uint32_t)(127 - up) << 23);
-                ri.pos = before + (row[i] - row0);
-                rows[r] = ri;
+            if (at[i] >= 0) {
+                // 16-byte chunks of a row are permuted as the tensor copies permute the keys'
+                const int rr = r + i * kPass + sub;
+                const uint32_t swz = D == 128 ? (uint32_t)(rr & 7) : (uint32_t)((rr >> 1) & 3);
+                unsigned char *dst = q0 + (uint32_t)rr * D + (((uint32_t)(col >> 1) ^ swz) << 4) + (uint32_t)(col & 1) * 8u;
+                *reinterpret_cast<uint2 *>(dst) = make_uint2(h4[0], h4[1]);
+                *reinterpret_cast<uint2 *>(dst + R * D) = make_uint2(l4[0], l4[1]);
+                if (col == 0) {
+                    RowInfo ri;
+                    ri.row = at[i];
+                    ri.head = hx[i];
+                    ri.qs = __uint_as_float((uint32_t)(127 - up) << 23);
+                    ri.pos = before + (at[i] - row0);
+                    rows[rr] = ri;
+                }
             }
         }
     }
@@ -624,7 +652,7 @@ struct Walk {
 
     __device__ __forceinline__ Walk(const AttnArgs &a_, const Share &S_, const int64_t *plan)
         : a(a_), S(S_), w(S_.lo), first(plan[0]), it((int)plan[1]), published(0), ended(false) {
-        x = load_item(a, it);
+        x = *reinterpret_cast<const Item *>(plan + 2);
     }
 
     __device__ __forceinline__ void publish(Seg *ring, const Bars &B) {
@@ -660,13 +688,8 @@ struct Walk {
             const int q0 = x.rt * a.rpt / a.group, q1 = min(x.n - 1, ((x.rt + 1) * a.rpt - 1) / a.group);
             g.see_all = min(x.len, max(0, x.len - x.n + q0 + 1));
             g.see_max = min(x.len, max(0, x.len - x.n + q1 + 1));
-            g.c0 = (int)blockIdx.x;
-            g.parts = 1;
-            if (g.count < x.nt) {
-                const int64_t u0 = first + (int64_t)g.head * unit_length(a, x) + a.over;  // the unit's first tile
-                g.c0 = cta_of(u0, S.total, S.ctas);
-                g.parts = cta_of(u0 + x.nt - 1, S.total, S.ctas) - g.c0 + 1;
-            }
+            g.nt = x.nt;
+            g.u0 = first + (int64_t)g.head * unit_length(a, x) + a.over;
         }
         if ((threadIdx.x & 31) == 0) {
             ring[ss] = g;
@@ -685,9 +708,15 @@ __device__ __forceinline__ void segment_query_role(const AttnArgs &a, unsigned c
     Walk W(a, S, plan);
 #pragma unroll 1
     for (int seg = 0;; seg++) {
-        // this segment and the next, and more if there is room
+        if (W.published == seg) W.publish(ring, B);  // (the first; its place is free)
+        const int buf = seg & 1;
+        if (!warp_wait(B.q_empty(buf), ((uint32_t)(seg >> 1) & 1u) ^ 1u, 0xe00u + buf, abort_flag)) return;
+        load_queries<D, R, 2>(a, smem, L, ring + seg % kSegs, buf, 0, 1);
+        if ((threadIdx.x & 31) == 0) mbar_arrive(B.q_full(buf));
+        if (ring[seg % kSegs].count == 0) return;
+        // the next segment, and more if there is room
 #pragma unroll 1
-        while (!W.ended && W.published < seg + kSegs) {
+        while (!W.ended && W.published < seg + 1 + kSegs) {
             uint64_t *bar = B.seg_empty(W.published % kSegs);
             const uint32_t parity = ((uint32_t)(W.published / kSegs) & 1u) ^ 1u;
             if (W.published > seg + 1) {
@@ -697,11 +726,20 @@ __device__ __forceinline__ void segment_query_role(const AttnArgs &a, unsigned c
             }
             W.publish(ring, B);
         }
-        const int buf = seg & 1;
-        if (!warp_wait(B.q_empty(buf), ((uint32_t)(seg >> 1) & 1u) ^ 1u, 0xe00u + buf, abort_flag)) return;
-        load_queries<D, R>(a, smem, L, ring + seg % kSegs, buf, 0, R);
-        if ((threadIdx.x & 31) == 0) mbar_arrive(B.q_full(buf));
-        if (ring[seg % kSegs].count == 0) return;
+    }
+}
+
+// Asks for a published segment's queries ahead of their use (into L2).
+__device__ __forceinline__ void prefetch_queries(const AttnArgs &a, const Seg *sg) {
+    if (sg->count == 0) return;
+    const int first = sg->rt * a.rpt, live = min(a.rpt, sg->n * a.group - first);
+    const int q0 = first / a.group, q1 = (first + live - 1) / a.group;
+    const int lines = (a.group * a.k.kv.dim * 2 + 127) / 128;  // a row's heads of the group lie side by side
+#pragma unroll 1
+    for (int i = threadIdx.x & 31; i < (q1 - q0 + 1) * lines; i += 32) {
+        const int r = i / lines;
+        const uint16_t *at = a.k.q + (size_t)(sg->row0 + q0 + r) * a.k.ldq + (size_t)sg->head * a.group * a.k.kv.dim;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(at + (i - r * lines) * 64));
     }
 }
 
@@ -715,6 +753,7 @@ __device__ __forceinline__ void segment_role(const AttnArgs &a, unsigned char *s
         if (!warp_wait(B.seg_empty(W.published % kSegs), ((uint32_t)(W.published / kSegs) & 1u) ^ 1u, 0xe10u, abort_flag))
             return;
         W.publish(ring, B);
+        prefetch_queries(a, ring + (W.published - 1) % kSegs);
     }
 }
 
@@ -768,6 +807,19 @@ __device__ __forceinline__ void join_role(const AttnArgs &a, const Share &S, con
     __threadfence();
     named_barrier(bar_id, NSOFT);
     if (tid == 0) red_release_gpu_add(arrive, 1u);
+    // the (at most two) units: the CTAs that share each, and this CTA's rows of it
+    int c0[2], parts[2], mine[2];
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        c0[i] = parts[i] = mine[i] = 0;
+        if (i < shared) {
+            const Seg &g = list[i];
+            c0[i] = cta_of(g.u0, S.total, S.ctas);
+            parts[i] = cta_of(g.u0 + g.nt - 1, S.total, S.ctas) - c0[i] + 1;
+            const int nrows = min(a.rpt, g.n * a.group - g.rt * a.rpt);
+            mine[i] = max(0, (nrows - (cta - c0[i]) + parts[i] - 1) / parts[i]);  // rows cta - c0, + parts, ...
+        }
+    }
     if (shared > 0) {
         if (tid == 0 && *(volatile int *)abort_flag == 0) {
             const uint64_t t0 = global_timer_ns(), lim = g_wait_limit_ns;
@@ -779,18 +831,16 @@ __device__ __forceinline__ void join_role(const AttnArgs &a, const Share &S, con
             }
         }
         named_barrier(bar_id, NSOFT);
-    }
+        // a warp per row, lanes over the head's values
 #pragma unroll 1
-    for (int i = 0; i < shared; i++) {
-        if (*(volatile int *)abort_flag) break;
-        const Seg &g = list[i];
-        const int c0 = g.c0, parts = g.parts;
-        const int nrows = min(a.rpt, g.n * a.group - g.rt * a.rpt);
-        // rows cta - c0, + parts, ...: a warp per row, lanes over the head's values
-#pragma unroll 1
-        for (int r = (cta - c0) + parts * sw; r < nrows; r += parts * (NSOFT / 32)) {
+        for (int j = sw; j < mine[0] + mine[1]; j += NSOFT / 32) {
+            if (*(volatile int *)abort_flag) break;
+            const bool second = j >= mine[0];
+            const Seg &g = list[second ? 1 : 0];
+            const int c0_ = second ? c0[1] : c0[0], parts_ = second ? parts[1] : parts[0];
+            const int r = cta - c0_ + parts_ * (second ? j - mine[0] : j);
             constexpr int V = D / 32, U = 4;  // values per lane; parts whose loads are in flight together
-            auto slot_of = [&](int p) { return a.part + (size_t)(2 * (c0 + p) + (p == 0 ? 1 : 0)) * slot_floats; };
+            auto slot_of = [&](int p) { return a.part + (size_t)(2 * (c0_ + p) + (p == 0 ? 1 : 0)) * slot_floats; };
             auto load = [&](int p, float (&x)[V]) {
                 const float *v = slot_of(p) + (size_t)r * D + lane * V;
                 if constexpr (V == 4) {
@@ -810,20 +860,20 @@ __device__ __forceinline__ void join_role(const AttnArgs &a, const Share &S, con
             for (int j = 0; j < V; j++) acc[j] = 0.f;
 #pragma unroll
             for (int i = 0; i < U; i++)
-                if (i < parts) load(i, x[i]);
+                if (i < parts_) load(i, x[i]);
             // references and sums, a lane per part (the first 32, and what more there is one by one)
             float2 ml = make_float2(-INFINITY, 0.f);
-            if (lane < parts) ml = __ldcg(reinterpret_cast<const float2 *>(slot_of(lane) + (size_t)a.rpt * D + 2 * r));
+            if (lane < parts_) ml = __ldcg(reinterpret_cast<const float2 *>(slot_of(lane) + (size_t)a.rpt * D + 2 * r));
             m = ml.x;
-            for (int p = lane + 32; p < parts; p += 32) m = fmaxf(m, __ldcg(slot_of(p) + (size_t)a.rpt * D + 2 * r));
+            for (int p = lane + 32; p < parts_; p += 32) m = fmaxf(m, __ldcg(slot_of(p) + (size_t)a.rpt * D + 2 * r));
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
             const float mine = ml.y == 0.f ? 0.f : ex2(ml.x - m);  // (sum 0: it saw nothing; NaN stays)
 #pragma unroll 1
-            for (int p = 0; p < parts; p += U) {
+            for (int p = 0; p < parts_; p += U) {
 #pragma unroll
                 for (int i = 0; i < U; i++) {
-                    if (p + i >= parts) continue;
+                    if (p + i >= parts_) continue;
                     float f, s;
                     if (p + i < 32) {
                         f = __shfl_sync(0xffffffffu, mine, p + i);
@@ -839,7 +889,7 @@ __device__ __forceinline__ void join_role(const AttnArgs &a, const Share &S, con
                 }
 #pragma unroll
                 for (int i = 0; i < U; i++)
-                    if (p + U + i < parts) load(p + U + i, x[i]);
+                    if (p + U + i < parts_) load(p + U + i, x[i]);
             }
             const int R = g.rt * a.rpt + r, qi = R / a.group, row = g.row0 + qi;
             const int hq = g.head * a.group + R - qi * a.group;

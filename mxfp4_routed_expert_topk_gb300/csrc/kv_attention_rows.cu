@@ -389,8 +389,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             if (!warp_wait(B.seg_full(s % kSegs), (uint32_t)(s / kSegs) & 1u, 0xe20u, abort_flag) ||
                 !warp_wait(B.q_empty(s & 1), ((uint32_t)(s >> 1) & 1u) ^ 1u, 0xe00u, abort_flag))
                 return;
-            load_queries<D, kRows>(a, smem, L, reinterpret_cast<const Seg *>(smem + L.seg) + s % kSegs, s & 1, 32 * ew,
-                                   32 * ew + 32);
+            load_queries<D, kRows, 1>(a, smem, L, reinterpret_cast<const Seg *>(smem + L.seg) + s % kSegs, s & 1, ew, 4);
             if (lane == 0) mbar_arrive(B.q_full(s & 1));
         };
         queries(0);
@@ -454,7 +453,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                 }
             }
 
-            float *part = sg->parts > 1 ? a.part + (size_t)(2 * (int)blockIdx.x + (tile0 == 0 ? 1 : 0)) * slot_floats
+            float *part = count < sg->nt ? a.part + (size_t)(2 * (int)blockIdx.x + (tile0 == 0 ? 1 : 0)) * slot_floats
                                         : nullptr;
             if (ri.row >= 0 && !*(volatile int *)abort_flag) {
                 if (part != nullptr) {
@@ -508,7 +507,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
 template <int D>
 cudaError_t launch(const CUtensorMap &tm, AttnArgs a, int sms, int smem_max, cudaStream_t st) {
     static PerDevice smem_set(0);
-    a.over = 4;
+    a.over = 3;
     a.nk = a.nv = 2;
     while (true) {  // as many stages as fit, values first
         AttnArgs b = a;
