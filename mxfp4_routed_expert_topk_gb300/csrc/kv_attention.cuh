@@ -33,7 +33,6 @@ namespace moe {
 namespace {
 
 constexpr int kTokens = 128;             // tokens per tile
-constexpr int kMaxStages = 8;            // per ring
 constexpr int kMaxSlots = kTokens / 16;  // pages per tile
 constexpr int kMaxLen = 1 << 30;         // tokens of a sequence
 constexpr uint32_t kSwizzle64B = 4;
@@ -52,7 +51,7 @@ struct AttnArgs {
     int nk, nv;     // stages of the key and value rings
     int over;       // what starting a unit costs, in tiles
     float scale2;   // scale * log2(e)
-    float *part;    // partial results: 2 slots per CTA of [rpt][dim] + [rpt][2]
+    float *part;    // partial results: 2 slots per worker of [rpt][dim] + [rpt][2]
 };
 
 namespace {
@@ -65,7 +64,6 @@ struct Seg {
     int nt;                // the unit's tiles: more than `count` if other CTAs have some of them
     int64_t u0;            // position of its first tile on the line
 };
-constexpr int kSegs = 4;   // ring of segments
 
 // One row of a row tile.
 struct RowInfo {
@@ -104,34 +102,40 @@ __device__ __forceinline__ Item load_item(const AttnArgs &a, int it) {
     return x;
 }
 
-// The CTA whose share of `total` positions over `ctas` CTAs holds position w.
-__device__ __forceinline__ int cta_of(int64_t w, int64_t total, int ctas) {
-    return (int)(((w + 1) * ctas - 1) / total);
+// The worker whose share of `total` positions over `workers` holds position w.
+__device__ __forceinline__ int worker_of(int64_t w, int64_t total, int workers) {
+    return (int)(((w + 1) * workers - 1) / total);
 }
 
-// A CTA's share [lo, hi) and where it starts.
-struct Share {
-    int64_t total, lo, hi;
-    int ctas;
+// The line of units: a unit is one (item, head), `over` positions that stand for its fixed
+// cost, then its tiles.  It is cut into equal shares, one per worker; a CTA has NW workers
+// (numbers blockIdx.x, + gridDim.x, ...), which walk their shares independently.
+struct Line {
+    int64_t total;
+    int workers;  // with a share; the first ones
+    __device__ __forceinline__ int64_t cut(int w) const { return w < workers ? total * w / workers : total; }
 };
 
-// The line of units: a unit is one (item, head), `over` positions that stand for its fixed
-// cost, then its tiles.  Cut it into equal shares (all threads; `mem`: kPlanWords + NT / 32 words
-// of shared memory, the first of which then hold the first position, number and description of
-// the item that lo lies in, after the caller's next barrier).
-constexpr int kPlanWords = 2 + (int)(sizeof(Item) + 7) / 8;
 __device__ __forceinline__ int unit_length(const AttnArgs &a, const Item &x) { return x.nt == 0 ? 0 : x.nt + a.over; }
 
-template <int NT>
-__device__ __forceinline__ Share cut_shares(const AttnArgs &a, int64_t *mem) {
+// Where a worker starts: the first position, number and description of the item it starts in.
+struct Start {
+    int64_t first;
+    int item;
+    Item x;
+};
+
+// Cut the line (all NT threads; `sums`: NT / 32 words of shared memory); the CTA's workers'
+// starts are in start[] after the caller's next barrier.
+template <int NT, int NW>
+__device__ __forceinline__ Line cut_line(const AttnArgs &a, int64_t *sums, Start *start) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    int64_t *sums = mem + kPlanWords;
     const int items = a.k.seqs * a.nrt;
     const int per = (items + NT - 1) / NT;
     const int i0 = min(tid * per, items), i1 = min(i0 + per, items);
-    // two rounds over the thread's items: their sum, then the item that holds lo
-    Share s;
-    int64_t mine = 0, pre = 0;
+    // two rounds over the thread's items: their sum, then those that hold the workers' starts
+    Line l;
+    int64_t mine = 0, pre = 0, lo[NW];
 #pragma unroll 1
     for (int round = 0; round < 2; round++) {
         int64_t at = pre;
@@ -141,10 +145,15 @@ __device__ __forceinline__ Share cut_shares(const AttnArgs &a, int64_t *mem) {
             const Item x = load_item(a, i);
             good &= x.ok;
             const int64_t u = (int64_t)unit_length(a, x) * a.k.kv.heads;
-            if (round == 1 && s.lo >= at && s.lo < at + u) {
-                mem[0] = at;
-                mem[1] = i;
-                *reinterpret_cast<Item *>(mem + 2) = x;
+            if (round == 1) {
+#pragma unroll
+                for (int w = 0; w < NW; w++) {
+                    if (lo[w] >= at && lo[w] < at + u) {
+                        start[w].first = at;
+                        start[w].item = i;
+                        start[w].x = x;
+                    }
+                }
             }
             at += u;
         }
@@ -159,22 +168,23 @@ __device__ __forceinline__ Share cut_shares(const AttnArgs &a, int64_t *mem) {
         }
         if (lane == 31) sums[warp] = pre;
         __syncthreads();
-        s.total = 0;
+        l.total = 0;
 #pragma unroll 1
         for (int w = 0; w < NT / 32; w++) {
             if (w < warp) pre += sums[w];
-            s.total += sums[w];
+            l.total += sums[w];
         }
         pre -= mine;
-        s.ctas = (int)min((int64_t)gridDim.x, s.total);
-        s.lo = s.hi = 0;
-        const int cta = (int)blockIdx.x;
-        if (cta >= s.ctas) break;
-        s.lo = s.total * cta / s.ctas;
-        s.hi = s.total * (cta + 1) / s.ctas;
-        if (s.lo < pre || s.lo >= pre + mine) break;
+        l.workers = (int)min((int64_t)gridDim.x * NW, l.total);
+        bool holds = false;
+#pragma unroll
+        for (int w = 0; w < NW; w++) {
+            lo[w] = l.cut((int)(blockIdx.x + w * gridDim.x));  // (without a share: past every item)
+            holds |= lo[w] >= pre && lo[w] < pre + mine;
+        }
+        if (!holds) break;
     }
-    return s;
+    return l;
 }
 
 // ------------------------------------------------------------ PTX
@@ -379,42 +389,6 @@ struct Watch {
     }
 };
 
-// Shared memory that both forms have, in bytes.
-struct CommonSmem {
-    uint32_t k, v, q, scales, seg, split, rows, bars, misc, total;
-    __host__ __device__ CommonSmem(int dim, int rows_, int nk, int nv) {
-        uint32_t o = 0;
-        k = o;      o += (uint32_t)nk * kTokens * dim;
-        v = o;      o += (uint32_t)nv * kTokens * dim;
-        q = o;      o += 4u * (uint32_t)rows_ * dim;                     // [2 buffers][2 parts][rows][dim]
-        scales = o; o += (uint32_t)kMaxStages * 2u * kMaxSlots * 4u;     // per value stage: keys', values'
-        seg = o;    o += (uint32_t)kSegs * (uint32_t)sizeof(Seg);
-        split = o;  o += 2u * (uint32_t)sizeof(Seg);                       // units shared with other CTAs
-        rows = o;   o += 2u * (uint32_t)rows_ * (uint32_t)sizeof(RowInfo);
-        bars = o;   o += 64u * 8u;
-        misc = o;   o += 512u;
-        total = o;
-    }
-};
-
-// Barriers, by index.
-struct Bars {
-    uint64_t *b;
-    __device__ uint64_t *k_full(int s) const { return b + s; }
-    __device__ uint64_t *k_empty(int s) const { return b + kMaxStages + s; }
-    __device__ uint64_t *v_full(int s) const { return b + 2 * kMaxStages + s; }
-    __device__ uint64_t *v_empty(int s) const { return b + 3 * kMaxStages + s; }
-    __device__ uint64_t *q_full(int s) const { return b + 4 * kMaxStages + s; }
-    __device__ uint64_t *q_empty(int s) const { return b + 4 * kMaxStages + 2 + s; }
-    __device__ uint64_t *s_full(int s) const { return b + 4 * kMaxStages + 4 + s; }   // scores in TMEM
-    __device__ uint64_t *p_ready(int s) const { return b + 4 * kMaxStages + 8 + s; }  // weights written, scores read
-    __device__ uint64_t *o_full(int s) const { return b + 4 * kMaxStages + 12 + s; }  // outputs in TMEM
-    __device__ uint64_t *o_empty(int s) const { return b + 4 * kMaxStages + 16 + s; }
-    __device__ uint64_t *mma_done() const { return b + 4 * kMaxStages + 20; }
-    __device__ uint64_t *seg_full(int s) const { return b + 4 * kMaxStages + 21 + s; }
-    __device__ uint64_t *seg_empty(int s) const { return b + 4 * kMaxStages + 25 + s; }
-};
-
 // ------------------------------------------- copies (warp 0: keys, warp 2: values, scales)
 // As with the MMAs, the predicate stands on the copy itself and the warp stays converged.
 __device__ __forceinline__ void tma_load_3d_elected(void *dst, const CUtensorMap *map, int c0, int c1, int c2,
@@ -428,105 +402,78 @@ __device__ __forceinline__ void tma_load_3d_elected(void *dst, const CUtensorMap
         : "memory");
 }
 
-// SIDE 0: keys, 1: values; P: page size (a constant, as the warp's time per tile counts).
-template <int D, int SIDE, int P>
-__device__ __forceinline__ void copy_pages(const AttnArgs &a, const CUtensorMap *tm, unsigned char *smem,
-                                           const CommonSmem &L, const Bars &B, int *abort_flag) {
-    constexpr uint32_t kTile = kTokens * D;
-    constexpr int kSlots = kTokens / P;
-    const int lane = threadIdx.x & 31;
-    const KvView &kv = a.k.kv;
-    StatusWord *st = a.k.st;
-    const int n = SIDE ? a.nv : a.nk;
-    unsigned char *ring = smem + (SIDE ? L.v : L.k);
-    const uint32_t elected = elect_one();
-    Ring R;
-    int issued = 0;
-    bool run = true;
-#pragma unroll 1
-    for (int seg = 0; run; seg++) {
-        const int ss = seg % kSegs;
-        if (!warp_wait(B.seg_full(ss), (uint32_t)(seg / kSegs) & 1u, 0xa60u + SIDE, abort_flag)) break;
-        const Seg *sg = reinterpret_cast<const Seg *>(smem + L.seg) + ss;
-        const int count = sg->count;
-        if (count == 0) break;
-        const int32_t *row = a.k.page_table + (size_t)sg->b * a.k.table_width;
-        const int c0 = sg->tile0 * kSlots, c1 = min((sg->see_max + P - 1) / P, (sg->tile0 + count) * kSlots);
-        const int y = (SIDE * kv.heads + sg->head) * P;
-        const uint8_t *scale = reinterpret_cast<const uint8_t *>(kv.scale(0, a.k.layer, 0, sg->head));
-        __syncwarp();
-        if (elected) mbar_arrive(B.seg_empty(ss));
-        // page numbers, 32 columns at a time: lane l holds column base + l, and the next 32.  One
-        // past the last stands for a page outside the cache (it lies outside the tensor: zeros
-        // arrive) and for columns past the sequence's end.
-        auto number = [&](int col) {
-            if (col >= c1) return kv.n_pages;
-            const int page = row[col];
-            if (page >= 0 && page < kv.n_pages) return page;
-            set_status(st, MOE_ERR_BAD_PAGE, 3);
-            return kv.n_pages;
-        };
-        int at = 0, left = c1 - c0;  // column of the tile in the 32; columns from the tile on
-        int id = number(c0 + lane), id2 = number(c0 + 32 + lane), ahead = c0 + 64;
-#pragma unroll 1
-        for (int t = 0; t < count; t++) {
-            uint64_t *full = SIDE ? B.v_full(R.s) : B.k_full(R.s);
-            if (!(run = warp_wait(SIDE ? B.v_empty(R.s) : B.k_empty(R.s), R.ph ^ 1u, 0xa00u + 16 * SIDE + R.s, abort_flag)))
-                break;
-            unsigned char *dst = ring + (uint32_t)R.s * kTile;
-            if (left >= kSlots) {
-                if (elected) mbar_arrive_expect_tx(full, kTile);
-                __syncwarp();
-#pragma unroll
-                for (int j = 0; j < kSlots; j++)
-                    tma_load_3d_elected(dst + j * (P * D), tm, 0, y, __shfl_sync(0xffffffffu, id, at + j), full, elected);
-            } else {  // the sequence ends in this tile
-                if (elected) mbar_arrive_expect_tx(full, (uint32_t)max(left, 0) * (uint32_t)(P * D));
-                __syncwarp();
-                for (int j = 0; j < left; j++)
-                    tma_load_3d_elected(dst + j * (P * D), tm, 0, y, __shfl_sync(0xffffffffu, id, at + j), full, elected);
-            }
-            if constexpr (SIDE == 1) {
-                const int page = __shfl_sync(0xffffffffu, id, (at + lane) & 31);
-                if (lane < kSlots) {
-                    const bool ok = lane < left && page < kv.n_pages;
-                    const uint32_t sc = smem_u32(smem + L.scales) + (uint32_t)(R.s * 2 * kMaxSlots + lane) * 4u;
-                    const uint8_t *src = scale + (uint64_t)(ok ? page : 0) * kv.page_rec;
-                    cp_async4(sc, src, ok);
-                    cp_async4(sc + kMaxSlots * 4u, src + 4 * kv.heads, ok);
-                    cp_async_arrive(full);
-                }
-            }
-            at += kSlots;
-            left -= kSlots;
-            if (at == 32) {
-                at = 0;
-                id = id2;
-                id2 = number(ahead + lane);
-                ahead += 32;
-            }
-            issued++;
-            R.next(n);
+// The page numbers of a segment, 32 columns of the table at a time: lane l holds column
+// base + l, and the next 32.  One past the last page stands for a page outside the cache (it
+// lies outside the tensor: zeros arrive) and for columns past the sequence's end.
+template <int P>
+struct Pages {
+    static constexpr int kSlots = kTokens / P;
+    const int32_t *row;
+    StatusWord *st;
+    int n_pages, c1, at, left, id, id2, ahead;  // column of the tile in the 32; columns from the tile on
+
+    __device__ __forceinline__ int number(int col) const {
+        if (col >= c1) return n_pages;
+        const int page = row[col];
+        if (page >= 0 && page < n_pages) return page;
+        set_status(st, MOE_ERR_BAD_PAGE, 3);
+        return n_pages;
+    }
+    __device__ __forceinline__ void start(const AttnArgs &a, const Seg &g) {
+        const int lane = threadIdx.x & 31, c0 = g.tile0 * kSlots;
+        row = a.k.page_table + (size_t)g.b * a.k.table_width;
+        st = a.k.st;
+        n_pages = a.k.kv.n_pages;
+        c1 = min((g.see_max + P - 1) / P, (g.tile0 + g.count) * kSlots);
+        at = 0;
+        left = c1 - c0;
+        id = number(c0 + lane);
+        id2 = number(c0 + 32 + lane);
+        ahead = c0 + 64;
+    }
+    __device__ __forceinline__ void next_tile() {
+        at += kSlots;
+        left -= kSlots;
+        if (at == 32) {
+            at = 0;
+            id = id2;
+            id2 = number(ahead + (int)(threadIdx.x & 31));
+            ahead += 32;
         }
     }
-    // nothing may be in flight when the CTA exits
-    if (lane == 0) {
-        for (int i = max(0, issued - n); i < issued; i++)
-            drain(SIDE ? B.v_full(i % n) : B.k_full(i % n), (uint32_t)(i / n) & 1u, abort_flag);
+    // One side (rows from y on of each page) of the tile's pages -> dst.
+    template <int D>
+    __device__ __forceinline__ void copy(const CUtensorMap *tm, unsigned char *dst, int y, uint64_t *full,
+                                         uint32_t elected) const {
+        if (left >= kSlots) {
+            if (elected) mbar_arrive_expect_tx(full, kTokens * D);
+            __syncwarp();
+#pragma unroll
+            for (int j = 0; j < kSlots; j++)
+                tma_load_3d_elected(dst + j * (P * D), tm, 0, y, __shfl_sync(0xffffffffu, id, at + j), full, elected);
+        } else {  // the sequence ends in this tile
+            if (elected) mbar_arrive_expect_tx(full, (uint32_t)max(left, 0) * (uint32_t)(P * D));
+            __syncwarp();
+#pragma unroll 1
+            for (int j = 0; j < left; j++)
+                tma_load_3d_elected(dst + j * (P * D), tm, 0, y, __shfl_sync(0xffffffffu, id, at + j), full, elected);
+        }
     }
-    __syncwarp();
-}
-
-template <int D, int SIDE>
-__device__ __forceinline__ void copy_role(const AttnArgs &a, const CUtensorMap *tm, unsigned char *smem,
-                                          const CommonSmem &L, const Bars &B, int *abort_flag) {
-    switch (a.k.kv.page) {
-        case 16: return copy_pages<D, SIDE, 16>(a, tm, smem, L, B, abort_flag);
-        case 32: return copy_pages<D, SIDE, 32>(a, tm, smem, L, B, abort_flag);
-        case 64: return copy_pages<D, SIDE, 64>(a, tm, smem, L, B, abort_flag);
-        case 128: return copy_pages<D, SIDE, 128>(a, tm, smem, L, B, abort_flag);
+    // The tile's scales of both sides -> [keys', values'][kMaxSlots] (kSlots arrivals on `full`).
+    __device__ __forceinline__ void copy_scales(const AttnArgs &a, int head, float *dst, uint64_t *full) const {
+        const int lane = threadIdx.x & 31, page = __shfl_sync(0xffffffffu, id, (at + lane) & 31);
+        if (lane < kSlots) {
+            const KvView &kv = a.k.kv;
+            const bool ok = lane < left && page < n_pages;
+            const uint32_t sc = smem_u32(dst + lane);
+            const uint8_t *src = reinterpret_cast<const uint8_t *>(kv.scale(0, a.k.layer, 0, head)) +
+                                 (uint64_t)(ok ? page : 0) * kv.page_rec;
+            cp_async4(sc, src, ok);
+            cp_async4(sc + kMaxSlots * 4u, src + 4 * kv.heads, ok);
+            cp_async_arrive(full);
+        }
     }
-}
+};
 
 // ------------------------------------------------------------------ queries
 // Warp w's part (of nw) of the rows of a segment's row tile: their data, and their queries as
@@ -536,14 +483,11 @@ __device__ __forceinline__ void copy_role(const AttnArgs &a, const CUtensorMap *
 // and fetching unrolled code costs more than the latency it hides (kBatch = 4 in place of 2:
 // 96 sequences of 512 tokens 70 us in place of 66).
 template <int D, int R, int kBatch>
-__device__ __forceinline__ void load_queries(const AttnArgs &a, unsigned char *smem, const CommonSmem &L, const Seg *sg,
-                                             int buf, int w, int nw) {
+__device__ __forceinline__ void load_queries(const AttnArgs &a, RowInfo *rows, unsigned char *q0, const Seg &g, int w, int nw) {
     constexpr int kLanes = D / 8, kPass = 32 / kLanes;
     const int lane = threadIdx.x & 31, sub = lane / kLanes, col = lane % kLanes;
-    RowInfo *rows = reinterpret_cast<RowInfo *>(smem + L.rows) + buf * R;
-    unsigned char *q0 = smem + L.q + (uint32_t)buf * (2u * R * D);
-    const int first = sg->rt * a.rpt, head0 = sg->head * a.group, row0 = sg->row0, before = sg->len - sg->n;
-    const int live = sg->count == 0 ? 0 : min(a.rpt, sg->n * a.group - first);  // rows of the tile
+    const int first = g.rt * a.rpt, head0 = g.head * a.group, row0 = g.row0, before = g.len - g.n;
+    const int live = g.count == 0 ? 0 : min(a.rpt, g.n * a.group - first);  // rows of the tile
     // rows past the tile see nothing (their queries are what was there: nobody reads their results)
     for (int r = live + 32 * w + lane; r < R; r += 32 * nw) {
         RowInfo none = {-1, 0, 1.f, -1};
@@ -639,28 +583,25 @@ __device__ __forceinline__ void load_queries(const AttnArgs &a, unsigned char *s
     __syncwarp();
 }
 
-// ------------------------------------------------------------- segments (warp 3)
-// Walks the CTA's share and publishes its segments, then one with count 0.
+// ------------------------------------------------------------------- segments
+// Walks a worker's share.
 struct Walk {
     const AttnArgs &a;
-    const Share &S;
-    int64_t w, first;  // next position; first position of the item
+    int64_t w, hi, first;  // next position, end of the share; first position of the item
     int it;
     Item x;
-    int published;
-    bool ended;  // the end has been published
 
-    __device__ __forceinline__ Walk(const AttnArgs &a_, const Share &S_, const int64_t *plan)
-        : a(a_), S(S_), w(S_.lo), first(plan[0]), it((int)plan[1]), published(0), ended(false) {
-        x = *reinterpret_cast<const Item *>(plan + 2);
+    __device__ __forceinline__ Walk(const AttnArgs &a_, const Line &l, int worker, const Start &st)
+        : a(a_), w(l.cut(worker)), hi(l.cut(worker + 1)), first(st.first), it(st.item), x(st.x) {
+        if (worker >= l.workers) hi = w;
     }
 
-    __device__ __forceinline__ void publish(Seg *ring, const Bars &B) {
-        const int ss = published % kSegs;
+    // The next segment; count 0 at the end of the share.
+    __device__ __forceinline__ Seg next() {
         Seg g;
         g.count = 0;
 #pragma unroll 1
-        while (w < S.hi) {  // the next positions with tiles
+        while (w < hi) {  // the next positions with tiles
             const int len = unit_length(a, x);
             const int64_t units = (int64_t)len * a.k.kv.heads, local = w - first;
             if (local >= units) {
@@ -671,15 +612,14 @@ struct Walk {
             // (a division of 32 bits wherever the numbers allow)
             g.head = (local >> 31) == 0 ? (int)((uint32_t)local / (uint32_t)len) : (int)(local / len);
             const int pos = (int)(local - (int64_t)g.head * len);
-            const int end = (int)min((int64_t)len, pos + (S.hi - w));
+            const int end = (int)min((int64_t)len, pos + (hi - w));
             w += end - pos;
             g.tile0 = max(0, pos - a.over);
             g.count = max(0, end - a.over) - g.tile0;
             if (g.count > 0) break;
         }
         g.count = max(g.count, 0);
-        ended = g.count == 0;
-        if (!ended) {
+        if (g.count != 0) {
             g.b = x.b;
             g.rt = x.rt;
             g.n = x.n;
@@ -691,71 +631,9 @@ struct Walk {
             g.nt = x.nt;
             g.u0 = first + (int64_t)g.head * unit_length(a, x) + a.over;
         }
-        if ((threadIdx.x & 31) == 0) {
-            ring[ss] = g;
-            mbar_arrive(B.seg_full(ss));
-        }
-        __syncwarp();
-        published++;
+        return g;
     }
 };
-
-// Publishes segments a few ahead and loads each one's queries, one segment ahead of the softmax.
-template <int D, int R>
-__device__ __forceinline__ void segment_query_role(const AttnArgs &a, unsigned char *smem, const CommonSmem &L,
-                                                   const Bars &B, const Share &S, const int64_t *plan, int *abort_flag) {
-    Seg *ring = reinterpret_cast<Seg *>(smem + L.seg);
-    Walk W(a, S, plan);
-#pragma unroll 1
-    for (int seg = 0;; seg++) {
-        if (W.published == seg) W.publish(ring, B);  // (the first; its place is free)
-        const int buf = seg & 1;
-        if (!warp_wait(B.q_empty(buf), ((uint32_t)(seg >> 1) & 1u) ^ 1u, 0xe00u + buf, abort_flag)) return;
-        load_queries<D, R, 2>(a, smem, L, ring + seg % kSegs, buf, 0, 1);
-        if ((threadIdx.x & 31) == 0) mbar_arrive(B.q_full(buf));
-        if (ring[seg % kSegs].count == 0) return;
-        // the next segment, and more if there is room
-#pragma unroll 1
-        while (!W.ended && W.published < seg + 1 + kSegs) {
-            uint64_t *bar = B.seg_empty(W.published % kSegs);
-            const uint32_t parity = ((uint32_t)(W.published / kSegs) & 1u) ^ 1u;
-            if (W.published > seg + 1) {
-                if (!__all_sync(0xffffffffu, mbar_test(bar, parity))) break;
-            } else if (!warp_wait(bar, parity, 0xe10u, abort_flag)) {
-                return;
-            }
-            W.publish(ring, B);
-        }
-    }
-}
-
-// Asks for a published segment's queries ahead of their use (into L2).
-__device__ __forceinline__ void prefetch_queries(const AttnArgs &a, const Seg *sg) {
-    if (sg->count == 0) return;
-    const int first = sg->rt * a.rpt, live = min(a.rpt, sg->n * a.group - first);
-    const int q0 = first / a.group, q1 = (first + live - 1) / a.group;
-    const int lines = (a.group * a.k.kv.dim * 2 + 127) / 128;  // a row's heads of the group lie side by side
-#pragma unroll 1
-    for (int i = threadIdx.x & 31; i < (q1 - q0 + 1) * lines; i += 32) {
-        const int r = i / lines;
-        const uint16_t *at = a.k.q + (size_t)(sg->row0 + q0 + r) * a.k.ldq + (size_t)sg->head * a.group * a.k.kv.dim;
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(at + (i - r * lines) * 64));
-    }
-}
-
-// Publishes segments only.
-__device__ __forceinline__ void segment_role(const AttnArgs &a, unsigned char *smem, const CommonSmem &L, const Bars &B,
-                                             const Share &S, const int64_t *plan, int *abort_flag) {
-    Seg *ring = reinterpret_cast<Seg *>(smem + L.seg);
-    Walk W(a, S, plan);
-#pragma unroll 1
-    while (!W.ended) {
-        if (!warp_wait(B.seg_empty(W.published % kSegs), ((uint32_t)(W.published / kSegs) & 1u) ^ 1u, 0xe10u, abort_flag))
-            return;
-        W.publish(ring, B);
-        prefetch_queries(a, ring + (W.published - 1) % kSegs);
-    }
-}
 
 // Value rows of the tile's tokens in shared memory, for one tile that not every row sees
 // whole (thread = token `tok` of the tile, which is token t of the sequence): rows that no
@@ -793,52 +671,52 @@ __device__ __forceinline__ const uint8_t *value_codes(const AttnArgs &a, int b, 
     return a.k.kv.codes(page, a.k.layer, 1, head) + (size_t)(t % P) * a.k.kv.dim;
 }
 
-// ---------------------------------------- sequences shared with other CTAs
-// All NSOFT softmax threads, after the CTA's last segment: partial results are published,
-// and once every CTA has done so the CTA joins its rows of the (at most two) units it shares,
-// `shared` of which stand in `list`.
-template <int D, int NSOFT>
-__device__ __forceinline__ void join_role(const AttnArgs &a, const Share &S, const Seg *list, int shared, int bar_id,
-                                          int *abort_flag) {
+// ---------------------------------------- units shared with other workers
+// All NT threads of a worker (tid: 0 .. NT-1), after its last segment: partial results are
+// published, and once every worker has done so this one joins its rows of the (at most two)
+// units it shares, `shared` of which stand in `list`.
+template <int D, int NT>
+__device__ __forceinline__ void join_role(const AttnArgs &a, const Line &line, int worker, const Seg *list, int shared,
+                                          int tid, int bar_id, int *abort_flag) {
     StatusWord *st = a.k.st;
-    const int tid = (int)threadIdx.x - 32 * kFirstSoft, lane = tid & 31, sw = tid >> 5, cta = (int)blockIdx.x;
+    const int lane = tid & 31, sw = tid >> 5;
     const size_t slot_floats = (size_t)a.rpt * D + 2 * a.rpt;
     unsigned int *arrive = &st->pad[kStKvArrive], *leave = &st->pad[kStKvExit];
     __threadfence();
-    named_barrier(bar_id, NSOFT);
+    named_barrier(bar_id, NT);
     if (tid == 0) red_release_gpu_add(arrive, 1u);
-    // the (at most two) units: the CTAs that share each, and this CTA's rows of it
+    // the (at most two) units: the workers that share each, and this one's rows of it
     int c0[2], parts[2], mine[2];
 #pragma unroll
     for (int i = 0; i < 2; i++) {
         c0[i] = parts[i] = mine[i] = 0;
         if (i < shared) {
             const Seg &g = list[i];
-            c0[i] = cta_of(g.u0, S.total, S.ctas);
-            parts[i] = cta_of(g.u0 + g.nt - 1, S.total, S.ctas) - c0[i] + 1;
+            c0[i] = worker_of(g.u0, line.total, line.workers);
+            parts[i] = worker_of(g.u0 + g.nt - 1, line.total, line.workers) - c0[i] + 1;
             const int nrows = min(a.rpt, g.n * a.group - g.rt * a.rpt);
-            mine[i] = max(0, (nrows - (cta - c0[i]) + parts[i] - 1) / parts[i]);  // rows cta - c0, + parts, ...
+            mine[i] = max(0, (nrows - (worker - c0[i]) + parts[i] - 1) / parts[i]);  // rows worker - c0, + parts, ...
         }
     }
     if (shared > 0) {
         if (tid == 0 && *(volatile int *)abort_flag == 0) {
             const uint64_t t0 = global_timer_ns(), lim = g_wait_limit_ns;
-            while (ld_acquire_gpu(arrive) < (unsigned)S.ctas) {
+            while (ld_acquire_gpu(arrive) < (unsigned)line.workers) {
                 if (global_timer_ns() - t0 > lim) {
                     *(volatile int *)abort_flag = 0xd00;
                     break;
                 }
             }
         }
-        named_barrier(bar_id, NSOFT);
+        named_barrier(bar_id, NT);
         // a warp per row, lanes over the head's values
 #pragma unroll 1
-        for (int j = sw; j < mine[0] + mine[1]; j += NSOFT / 32) {
+        for (int j = sw; j < mine[0] + mine[1]; j += NT / 32) {
             if (*(volatile int *)abort_flag) break;
             const bool second = j >= mine[0];
             const Seg &g = list[second ? 1 : 0];
             const int c0_ = second ? c0[1] : c0[0], parts_ = second ? parts[1] : parts[0];
-            const int r = cta - c0_ + parts_ * (second ? j - mine[0] : j);
+            const int r = worker - c0_ + parts_ * (second ? j - mine[0] : j);
             constexpr int V = D / 32, U = 4;  // values per lane; parts whose loads are in flight together
             auto slot_of = [&](int p) { return a.part + (size_t)(2 * (c0_ + p) + (p == 0 ? 1 : 0)) * slot_floats; };
             auto load = [&](int p, float (&x)[V]) {
@@ -901,9 +779,9 @@ __device__ __forceinline__ void join_role(const AttnArgs &a, const Share &S, con
                 a.k.lse[(size_t)row * a.k.heads_q + hq] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
         }
     }
-    named_barrier(bar_id, NSOFT);
-    if (tid == 0 && atomicAdd(leave, 1u) == (unsigned)S.ctas - 1u) {
-        // every CTA has arrived and has stopped polling
+    named_barrier(bar_id, NT);
+    if (tid == 0 && atomicAdd(leave, 1u) == (unsigned)line.workers - 1u) {
+        // every worker has arrived and has stopped polling
         *(volatile unsigned int *)arrive = 0u;
         *(volatile unsigned int *)leave = 0u;
     }

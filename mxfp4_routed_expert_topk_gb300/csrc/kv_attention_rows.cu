@@ -34,6 +34,134 @@ constexpr int kRegsIssue = 96, kRegsSoft = 112, kRegsJoin = 192;
 static_assert(kRegsIssue + kGroups * kRegsSoft + kRegsJoin <= 4 * 128 && kThreads == 512, "register split");
 constexpr int kBarAll = 7;
 
+constexpr int kMaxStages = 8;  // per ring
+constexpr int kSegs = 4;       // ring of segments
+
+// Shared memory, in bytes.
+struct CommonSmem {
+    uint32_t k, v, q, scales, seg, split, rows, bars, misc, total;
+    __host__ __device__ CommonSmem(int dim, int rows_, int nk, int nv) {
+        uint32_t o = 0;
+        k = o;      o += (uint32_t)nk * kTokens * dim;
+        v = o;      o += (uint32_t)nv * kTokens * dim;
+        q = o;      o += 4u * (uint32_t)rows_ * dim;                     // [2 buffers][2 parts][rows][dim]
+        scales = o; o += (uint32_t)kMaxStages * 2u * kMaxSlots * 4u;     // per value stage: keys', values'
+        seg = o;    o += (uint32_t)kSegs * (uint32_t)sizeof(Seg);
+        split = o;  o += 2u * (uint32_t)sizeof(Seg);                       // units shared with other CTAs
+        rows = o;   o += 2u * (uint32_t)rows_ * (uint32_t)sizeof(RowInfo);
+        bars = o;   o += 64u * 8u;
+        misc = o;   o += 512u;
+        total = o;
+    }
+};
+
+// Barriers, by index.
+struct Bars {
+    uint64_t *b;
+    __device__ uint64_t *k_full(int s) const { return b + s; }
+    __device__ uint64_t *k_empty(int s) const { return b + kMaxStages + s; }
+    __device__ uint64_t *v_full(int s) const { return b + 2 * kMaxStages + s; }
+    __device__ uint64_t *v_empty(int s) const { return b + 3 * kMaxStages + s; }
+    __device__ uint64_t *q_full(int s) const { return b + 4 * kMaxStages + s; }
+    __device__ uint64_t *q_empty(int s) const { return b + 4 * kMaxStages + 2 + s; }
+    __device__ uint64_t *s_full(int s) const { return b + 4 * kMaxStages + 4 + s; }   // scores in TMEM
+    __device__ uint64_t *p_ready(int s) const { return b + 4 * kMaxStages + 8 + s; }  // weights written, scores read
+    __device__ uint64_t *o_full(int s) const { return b + 4 * kMaxStages + 12 + s; }  // outputs in TMEM
+    __device__ uint64_t *o_empty(int s) const { return b + 4 * kMaxStages + 16 + s; }
+    __device__ uint64_t *mma_done() const { return b + 4 * kMaxStages + 20; }
+    __device__ uint64_t *seg_full(int s) const { return b + 4 * kMaxStages + 21 + s; }
+    __device__ uint64_t *seg_empty(int s) const { return b + 4 * kMaxStages + 25 + s; }
+};
+
+// One side's copies (SIDE 0: keys, 1: values and scales); P: page size (a constant, as the
+// warp's time per tile counts).
+template <int D, int SIDE, int P>
+__device__ __forceinline__ void copy_pages(const AttnArgs &a, const CUtensorMap *tm, unsigned char *smem,
+                                           const CommonSmem &L, const Bars &B, int *abort_flag) {
+    constexpr uint32_t kTile = kTokens * D;
+    const int n = SIDE ? a.nv : a.nk;
+    unsigned char *ring = smem + (SIDE ? L.v : L.k);
+    const uint32_t elected = elect_one();
+    Ring R;
+    Pages<P> pg;
+    int issued = 0;
+    bool run = true;
+#pragma unroll 1
+    for (int seg = 0; run; seg++) {
+        const int ss = seg % kSegs;
+        if (!warp_wait(B.seg_full(ss), (uint32_t)(seg / kSegs) & 1u, 0xa60u + SIDE, abort_flag)) break;
+        const Seg *sg = reinterpret_cast<const Seg *>(smem + L.seg) + ss;
+        const int count = sg->count, head = sg->head;
+        if (count == 0) break;
+        const int y = (SIDE * a.k.kv.heads + head) * P;
+        pg.start(a, *sg);
+        __syncwarp();
+        if (elected) mbar_arrive(B.seg_empty(ss));
+#pragma unroll 1
+        for (int t = 0; t < count; t++) {
+            uint64_t *full = SIDE ? B.v_full(R.s) : B.k_full(R.s);
+            if (!(run = warp_wait(SIDE ? B.v_empty(R.s) : B.k_empty(R.s), R.ph ^ 1u, 0xa00u + 16 * SIDE + R.s, abort_flag)))
+                break;
+            pg.template copy<D>(tm, ring + (uint32_t)R.s * kTile, y, full, elected);
+            if constexpr (SIDE == 1)
+                pg.copy_scales(a, head, reinterpret_cast<float *>(smem + L.scales) + R.s * 2 * kMaxSlots, full);
+            pg.next_tile();
+            issued++;
+            R.next(n);
+        }
+    }
+    // nothing may be in flight when the CTA exits
+    if ((threadIdx.x & 31) == 0) {
+        for (int i = max(0, issued - n); i < issued; i++)
+            drain(SIDE ? B.v_full(i % n) : B.k_full(i % n), (uint32_t)(i / n) & 1u, abort_flag);
+    }
+    __syncwarp();
+}
+
+template <int D, int SIDE>
+__device__ __forceinline__ void copy_role(const AttnArgs &a, const CUtensorMap *tm, unsigned char *smem,
+                                          const CommonSmem &L, const Bars &B, int *abort_flag) {
+    switch (a.k.kv.page) {
+        case 16: return copy_pages<D, SIDE, 16>(a, tm, smem, L, B, abort_flag);
+        case 32: return copy_pages<D, SIDE, 32>(a, tm, smem, L, B, abort_flag);
+        case 64: return copy_pages<D, SIDE, 64>(a, tm, smem, L, B, abort_flag);
+        case 128: return copy_pages<D, SIDE, 128>(a, tm, smem, L, B, abort_flag);
+    }
+}
+
+// Asks for a segment's queries ahead of their use (into L2).
+__device__ __forceinline__ void prefetch_queries(const AttnArgs &a, const Seg &g) {
+    const int first = g.rt * a.rpt, live = min(a.rpt, g.n * a.group - first);
+    const int q0 = first / a.group, q1 = (first + live - 1) / a.group;
+    const int lines = (a.group * a.k.kv.dim * 2 + 127) / 128;  // a row's heads of the group lie side by side
+#pragma unroll 1
+    for (int i = threadIdx.x & 31; i < (q1 - q0 + 1) * lines; i += 32) {
+        const int r = i / lines;
+        const uint16_t *at = a.k.q + (size_t)(g.row0 + q0 + r) * a.k.ldq + (size_t)g.head * a.group * a.k.kv.dim;
+        asm volatile("prefetch.global.L2 [%0];" ::"l"(at + (i - r * lines) * 64));
+    }
+}
+
+// Publishes the worker's segments, then one with count 0.
+__device__ __forceinline__ void segment_role(const AttnArgs &a, unsigned char *smem, const CommonSmem &L, const Bars &B,
+                                             const Line &line, const Start &start, int *abort_flag) {
+    Seg *ring = reinterpret_cast<Seg *>(smem + L.seg);
+    Walk W(a, line, (int)blockIdx.x, start);
+#pragma unroll 1
+    for (int i = 0;; i++) {
+        const int ss = i % kSegs;
+        if (!warp_wait(B.seg_empty(ss), ((uint32_t)(i / kSegs) & 1u) ^ 1u, 0xe10u, abort_flag)) return;
+        const Seg g = W.next();
+        if ((threadIdx.x & 31) == 0) {
+            ring[ss] = g;
+            mbar_arrive(B.seg_full(ss));
+        }
+        __syncwarp();
+        if (g.count == 0) return;
+        prefetch_queries(a, g);
+    }
+}
+
 struct RowsSmem {
     CommonSmem c;
     uint32_t ml, fac, chunk, nan, total;
@@ -105,12 +233,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
     uint32_t *tmem_slot = misc;
     int *abort_flag = reinterpret_cast<int *>(misc + 1);
     int *n_shared = reinterpret_cast<int *>(misc + 2);
-    int64_t *plan = reinterpret_cast<int64_t *>(misc + 8);
+    int64_t *sums = reinterpret_cast<int64_t *>(misc + 8);
+    Start *start = reinterpret_cast<Start *>(misc + 64);
     StatusWord *st = a.k.st;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 
-    const Share S = cut_shares<kThreads>(a, plan);
-    if ((int)blockIdx.x >= S.ctas) return;  // the whole CTA: nothing set up yet
+    const Line line = cut_line<kThreads, 1>(a, sums, start);
+    if ((int)blockIdx.x >= line.workers) return;  // the whole CTA: nothing set up yet
     if (tid == 0) {
         for (int s = 0; s < a.nk; s++) {
             mbar_init(B.k_full(s), 1);
@@ -232,7 +361,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             if (lane == 0) drain(B.mma_done(), 0u, abort_flag);
             __syncwarp();
         } else {
-            segment_role(a, smem, L, B, S, plan, abort_flag);
+            segment_role(a, smem, L, B, line, *start, abort_flag);
         }
     } else if (warp < kJoinWarp) {
         regs_dec<kRegsSoft>();
@@ -264,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                 const int u = done + t, sb = u % kSBufs, vb = u % a.nv;
                 soft_wait(B.v_full(vb), (uint32_t)(u / a.nv) & 1u, 0xc10u + vb, abort_flag);
                 // constants of the tile's pages: lane j has page j
+                float unit;  // value of a weight unit
                 {
                     const float *sc = scales + vb * 2 * kMaxSlots;
                     const float ks = sc[lane & 7] * a.scale2, vs = lane < slots ? sc[kMaxSlots + lane] : 0.f;
@@ -275,7 +405,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                     const float c = fmaxf(256.f * __fdividef(vs, vone), 8.67361738e-19f);  // at least 2^-60
                     if (lane < kMaxSlots)
                         chunk[lane] = make_float4(ks, fin ? lg2(c) : kNan, fin ? __fdividef(1.f, c) : 1.f, 0.f);
-                    if (lane == 0) fac[u & 3] = vone * (1.f / 256.f);
+                    unit = vone * (1.f / 256.f);
                 }
                 const bool special = (tile0 + t + 1) * kTokens > see_all;
                 const int lim = min(max(ri.pos + 1 - (tile0 + t) * kTokens, 0), kTokens);  // tokens the row sees
@@ -286,8 +416,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                     word = __ballot_sync(0xffffffffu, bad);
                     fence_proxy_async_smem();
                 }
-                if (lane == 0) nan[(u & 3) * 4 + ew] = word;
                 soft_wait(B.s_full(sb), (uint32_t)(u / kSBufs) & 1u, 0xc00u + sb, abort_flag);
+                // (from here on: these scores are there, so the outputs of tile u - 3 have been issued,
+                // so those of tile u - 4, whose places these are, have been joined)
+                if (lane == 0) {
+                    fac[u & 3] = unit;
+                    nan[(u & 3) * 4 + ew] = word;
+                }
                 tc_fence_after();
                 const uint32_t ts = tmem + (uint32_t)(sb * kTokens) + lanes;
                 // loops over 32 tokens are not unrolled: the body must stay in the instruction cache
@@ -389,7 +524,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             if (!warp_wait(B.seg_full(s % kSegs), (uint32_t)(s / kSegs) & 1u, 0xe20u, abort_flag) ||
                 !warp_wait(B.q_empty(s & 1), ((uint32_t)(s >> 1) & 1u) ^ 1u, 0xe00u, abort_flag))
                 return;
-            load_queries<D, kRows, 1>(a, smem, L, reinterpret_cast<const Seg *>(smem + L.seg) + s % kSegs, s & 1, ew, 4);
+            load_queries<D, kRows, 1>(a, reinterpret_cast<RowInfo *>(smem + L.rows) + (s & 1) * kRows,
+                                      smem + L.q + (uint32_t)(s & 1) * (2u * kRows * D),
+                                      reinterpret_cast<const Seg *>(smem + L.seg)[s % kSegs], ew, 4);
             if (lane == 0) mbar_arrive(B.q_full(s & 1));
         };
         queries(0);
@@ -496,7 +633,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
     }
     if (warp >= kFirstSoft) {
         named_barrier(kBarAll, kSoft);  // the list of shared units is complete
-        join_role<D, kSoft>(a, S, reinterpret_cast<const Seg *>(smem + L.split), *n_shared, kBarAll, abort_flag);
+        join_role<D, kSoft>(a, line, (int)blockIdx.x, reinterpret_cast<const Seg *>(smem + L.split), *n_shared,
+                            tid - 32 * kFirstSoft, kBarAll, abort_flag);
     }
     __syncthreads();
     tc_fence_after();

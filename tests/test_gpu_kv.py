@@ -232,6 +232,14 @@ def test_attention_pages_and_groups(dim, page, group):
     Case([4, 1, 3], [page - 2, 3 * page, 257], 2, group, dim, page, layers=3, layer=1, seed=page + group).check()
 
 
+@pytest.mark.parametrize("rows,dim,group", [(1, 128, 3), (2, 64, 8), (5, 128, 7)])
+def test_attention_many_short_sequences(rows, dim, group):
+    """Thousands of units of one to three tiles: every part of the device walks through several."""
+    r = np.random.default_rng(rows)
+    n = [int(x) for x in r.integers(0, rows + 1, 700)]
+    Case(n, [int(x) for x in r.integers(0, 300, 700)], 4, group, dim, 32, seed=dim).check()
+
+
 def test_attention_rows_that_see_nothing():
     """Fewer tokens than rows: the first rows stand before token 0; no tokens at all."""
     c = Case([5, 3, 2], [-3, -3, -1], 2, 7, 128, 16)
