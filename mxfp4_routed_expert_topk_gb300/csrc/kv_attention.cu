@@ -70,14 +70,14 @@ struct FewBars {
 // Feeds one worker (a warp): walks its share, copies tiles, loads queries, whichever is possible.
 template <int D, int P>
 __device__ __forceinline__ void feed(const AttnArgs &a, const CUtensorMap *tm, unsigned char *smem, const FewSmem &F,
-                                     int w, const FewBars &B, const Line &line, const Start &start, int *abort_flag) {
+                                     int w, const FewBars &B, const Start &start, int *abort_flag) {
     constexpr uint32_t kTile = kTokens * D;
     const int lane = threadIdx.x & 31;
     const uint32_t elected = elect_one();
     unsigned char *kv = smem + F.kv + (uint32_t)w * (kStages * 2u * kTile);
     float *scales = reinterpret_cast<float *>(smem + F.scales) + w * kStages * 2 * kMaxSlots;
     Seg *ring = reinterpret_cast<Seg *>(smem + F.seg) + 2 * w;
-    Walk W(a, line, (int)(blockIdx.x + w * gridDim.x), start);
+    Walk W(a, start);
     Pages<P> pg;
     Watch eye = lane == 0 ? Watch{B.empty(0), kStages, 0, 1u}
                 : lane == 1 ? Watch{B.q_free(), 1, 0, 1u}
@@ -88,7 +88,10 @@ __device__ __forceinline__ void feed(const AttnArgs &a, const CUtensorMap *tm, u
 #pragma unroll 1
     for (int seg = 0; run; seg++) {
         const Seg g = W.next();
-        if (g.count > 0) pg.start(a, g);
+        if (g.count > 0) {
+            prefetch_queries(a, g);
+            pg.start(a, g);
+        }
         bool told = false;  // description and queries are out
         int t = 0;
 #pragma unroll 1
@@ -214,10 +217,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_few_kernel(const __g
         const int w = warp == 0 ? 0 : warp - 1;
         const FewBars B{bars + 16 * w};
         switch (a.k.kv.page) {
-            case 16: feed<D, 16>(a, &tm, smem, F, w, B, line, start[w], abort_flag); break;
-            case 32: feed<D, 32>(a, &tm, smem, F, w, B, line, start[w], abort_flag); break;
-            case 64: feed<D, 64>(a, &tm, smem, F, w, B, line, start[w], abort_flag); break;
-            case 128: feed<D, 128>(a, &tm, smem, F, w, B, line, start[w], abort_flag); break;
+            case 16: feed<D, 16>(a, &tm, smem, F, w, B, start[w], abort_flag); break;
+            case 32: feed<D, 32>(a, &tm, smem, F, w, B, start[w], abort_flag); break;
+            case 64: feed<D, 64>(a, &tm, smem, F, w, B, start[w], abort_flag); break;
+            case 128: feed<D, 128>(a, &tm, smem, F, w, B, start[w], abort_flag); break;
         }
     } else if (warp == 1) {
         // ------------------------------------------------------ MMA issue

@@ -59,6 +59,7 @@ namespace {
 // A segment: consecutive tiles of one (sequence, row tile, head) in a CTA's share.
 struct Seg {
     int b, rt, n, len, row0, head, tile0;
+    int q0, q1, h0;        // rows of the tile: the first, the last, and the first's head of the group
     int count;             // tiles; 0: the share ends here
     int see_all, see_max;  // tokens that every row of the tile sees, and that any row sees
     int nt;                // the unit's tiles: more than `count` if other CTAs have some of them
@@ -80,7 +81,7 @@ struct Item {
 
 __device__ __forceinline__ Item load_item(const AttnArgs &a, int it) {
     Item x;
-    x.b = it / a.nrt;
+    x.b = a.nrt == 1 ? it : it / a.nrt;
     x.rt = it - x.b * a.nrt;
     int hi;
     x.ok = seq_rows(a.k.cu_rows, x.b, a.k.rows, x.row0, hi);
@@ -95,32 +96,45 @@ __device__ __forceinline__ Item load_item(const AttnArgs &a, int it) {
     x.len = (int)min((int64_t)len, room);
     x.nt = 0;
     if (x.rt * a.rpt < x.n * a.group) {
-        const int last = min(x.n - 1, ((x.rt + 1) * a.rpt - 1) / a.group);  // last row of the tile
+        const int last = a.nrt == 1 ? x.n - 1 : min(x.n - 1, ((x.rt + 1) * a.rpt - 1) / a.group);  // row of the tile
         const int see = min(x.len, max(0, x.len - x.n + last + 1));
         x.nt = max(1, (see + kTokens - 1) / kTokens);
     }
     return x;
 }
 
-// The worker whose share of `total` positions over `workers` holds position w.
-__device__ __forceinline__ int worker_of(int64_t w, int64_t total, int workers) {
-    return (int)(((w + 1) * workers - 1) / total);
-}
-
 // The line of units: a unit is one (item, head), `over` positions that stand for its fixed
 // cost, then its tiles.  It is cut into equal shares, one per worker; a CTA has NW workers
 // (numbers blockIdx.x, + gridDim.x, ...), which walk their shares independently.
 struct Line {
-    int64_t total;
-    int workers;  // with a share; the first ones
-    __device__ __forceinline__ int64_t cut(int w) const { return w < workers ? total * w / workers : total; }
+    int64_t total, share;  // positions; of a worker, the first `more` of them one more
+    int workers, more;     // workers with a share: the first ones
+    // (divisions of 32 bits wherever the numbers allow: all of this is code that runs once, and
+    // fetching it is what it costs)
+    static __device__ __forceinline__ int64_t ratio(int64_t x, int64_t y) {
+        return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
+    }
+    __device__ __forceinline__ void set(int64_t total_, int max_workers) {
+        total = total_;
+        workers = (int)min((int64_t)max_workers, total);
+        share = workers > 0 ? ratio(total, workers) : 0;
+        more = (int)(total - share * workers);
+    }
+    // Where worker w's share begins (past the last worker: the end).
+    __device__ __forceinline__ int64_t cut(int w) const { return w < workers ? w * share + min(w, more) : total; }
+    // The worker that has position x.
+    __device__ __forceinline__ int worker_of(int64_t x) const {
+        const int64_t longer = (share + 1) * more;
+        const bool in = x < longer;
+        return (in ? 0 : more) + (int)ratio(in ? x : x - longer, in ? share + 1 : share);
+    }
 };
 
 __device__ __forceinline__ int unit_length(const AttnArgs &a, const Item &x) { return x.nt == 0 ? 0 : x.nt + a.over; }
 
-// Where a worker starts: the first position, number and description of the item it starts in.
+// A worker's share, and the item it starts in: its first position, number and description.
 struct Start {
-    int64_t first;
+    int64_t lo, hi, first;
     int item;
     Item x;
 };
@@ -168,18 +182,23 @@ __device__ __forceinline__ Line cut_line(const AttnArgs &a, int64_t *sums, Start
         }
         if (lane == 31) sums[warp] = pre;
         __syncthreads();
-        l.total = 0;
+        int64_t total = 0;
 #pragma unroll 1
         for (int w = 0; w < NT / 32; w++) {
             if (w < warp) pre += sums[w];
-            l.total += sums[w];
+            total += sums[w];
         }
         pre -= mine;
-        l.workers = (int)min((int64_t)gridDim.x * NW, l.total);
+        l.set(total, (int)gridDim.x * NW);
         bool holds = false;
 #pragma unroll
         for (int w = 0; w < NW; w++) {
-            lo[w] = l.cut((int)(blockIdx.x + w * gridDim.x));  // (without a share: past every item)
+            const int worker = (int)(blockIdx.x + w * gridDim.x);
+            lo[w] = l.cut(worker);  // (without a share: past every item)
+            if (tid == 0) {
+                start[w].lo = lo[w];
+                start[w].hi = l.cut(worker + 1);
+            }
             holds |= lo[w] >= pre && lo[w] < pre + mine;
         }
         if (!holds) break;
@@ -478,16 +497,15 @@ struct Pages {
 // ------------------------------------------------------------------ queries
 // Warp w's part (of nw) of the rows of a segment's row tile: their data, and their queries as
 // two E4M3 parts, after a power of two that puts a row's largest value into [128, 256).  A
-// lane takes 8 values, so a pass covers 2 rows of 128 or 4 of 64; kBatch passes' loads are in
-// flight while the batch before is converted.  The code is kept small: it runs once per segment,
-// and fetching unrolled code costs more than the latency it hides (kBatch = 4 in place of 2:
-// 96 sequences of 512 tokens 70 us in place of 66).
-template <int D, int R, int kBatch>
+// lane takes 8 values, so a pass covers 2 rows of 128 or 4 of 64; the next pass's loads are in
+// flight while one is converted.  One pass per turn: this code runs once per segment, and
+// fetching an unrolled loop costs more than the latency that it hides (four passes in flight:
+// one sequence of 300 tokens 31 us in place of 27).  kUnroll: words converted at once.
+template <int D, int R, int kUnroll>
 __device__ __forceinline__ void load_queries(const AttnArgs &a, RowInfo *rows, unsigned char *q0, const Seg &g, int w, int nw) {
     constexpr int kLanes = D / 8, kPass = 32 / kLanes;
     const int lane = threadIdx.x & 31, sub = lane / kLanes, col = lane % kLanes;
-    const int first = g.rt * a.rpt, head0 = g.head * a.group, row0 = g.row0, before = g.len - g.n;
-    const int live = g.count == 0 ? 0 : min(a.rpt, g.n * a.group - first);  // rows of the tile
+    const int live = min(a.rpt, g.n * a.group - g.rt * a.rpt);  // rows of the tile
     // rows past the tile see nothing (their queries are what was there: nobody reads their results)
     for (int r = live + 32 * w + lane; r < R; r += 32 * nw) {
         RowInfo none = {-1, 0, 1.f, -1};
@@ -495,89 +513,67 @@ __device__ __forceinline__ void load_queries(const AttnArgs &a, RowInfo *rows, u
     }
     const int per = (live + nw * kPass - 1) / (nw * kPass) * kPass;  // (whole passes: any two warps write apart)
     const int r0 = min(w * per, live), r1 = min(r0 + per, live);
-    // this lane's row of the next pass to load, as (row, head of the group); a pass moves it on
-    int qi = (first + r0 + sub) / a.group, hd = first + r0 + sub - qi * a.group;
-    const int step_q = kPass / a.group, step_h = kPass - step_q * a.group;
-    uint4 u[kBatch];
-    int row[kBatch], hq[kBatch];
+    // this lane's row of the next pass, as (row, head of the group); a pass moves it on
+    int qi = g.q0, hd = g.h0 + r0 + sub;
+    if (r0 > 0) {
+        qi += hd / a.group;
+        hd %= a.group;
+    }
+    uint4 u;
     auto load = [&](int r) {
-#pragma unroll
-        for (int i = 0; i < kBatch; i++) {
-            const bool ok = r + i * kPass + sub < r1;
-            row[i] = ok ? row0 + qi : -1;
-            hq[i] = head0 + hd;
-            u[i] = make_uint4(0u, 0u, 0u, 0u);
-            if (ok) u[i] = *reinterpret_cast<const uint4 *>(a.k.q + (size_t)row[i] * a.k.ldq + (size_t)hq[i] * D + col * 8);
-            qi += step_q;
-            hd += step_h;
-            if (hd >= a.group) {
-                hd -= a.group;
-                qi++;
-            }
+        while (hd >= a.group) {
+            hd -= a.group;
+            qi++;
         }
+        u = make_uint4(0u, 0u, 0u, 0u);
+        if (r + sub < r1)
+            u = *reinterpret_cast<const uint4 *>(a.k.q + (size_t)(g.row0 + qi) * a.k.ldq +
+                                                 (size_t)(g.head * a.group + hd) * D + col * 8);
     };
     load(r0);
 #pragma unroll 1
-    for (int r = r0; r < r1; r += kBatch * kPass) {
-        uint4 x[kBatch];
-        int at[kBatch], hx[kBatch];
+    for (int r = r0; r < r1; r += kPass) {
+        uint32_t v[4] = {u.x, u.y, u.z, u.w};
+        RowInfo ri;
+        ri.row = g.row0 + qi;
+        ri.head = g.head * a.group + hd;
+        ri.pos = g.len - g.n + qi;
+        hd += kPass;
+        load(r + kPass);
+        // largest magnitude over finite values, two columns of them
+        constexpr uint32_t kMag = 0x7fff7fffu;
+        uint32_t top = __vmaxu2(__vmaxu2(v[0] & kMag, v[1] & kMag), __vmaxu2(v[2] & kMag, v[3] & kMag));
+        if (__any_sync(0xffffffffu, max(top & 0xffffu, top >> 16) >= 0x7f80u)) {
+            top = 0;
 #pragma unroll
-        for (int i = 0; i < kBatch; i++) {
-            x[i] = u[i];
-            at[i] = row[i];
-            hx[i] = hq[i];
-        }
-        if (r + kBatch * kPass < r1) load(r + kBatch * kPass);
-#pragma unroll
-        for (int i = 0; i < kBatch; i++) {
-            const uint32_t v[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-            uint32_t top = 0;  // largest magnitude over finite values, two columns of them
-#pragma unroll
-            for (int j = 0; j < 4; j++) top = __vmaxu2(top, v[j] & 0x7fff7fffu);
-            if (__any_sync(0xffffffffu, __vcmpgeu2(top, 0x7f807f80u) != 0u)) {
-                top = 0;
-#pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const uint32_t m = v[j] & 0x7fff7fffu;
-                    top = __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7f807f80u));
-                }
-            }
-            top = max(top & 0xffffu, top >> 16);
-#pragma unroll
-            for (int d = kLanes / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
-            const int up = top == 0 ? 0 : min(126, 7 - ((int)(top >> 7) - 127));
-            const float f = __uint_as_float((uint32_t)(127 + up) << 23);
-            uint32_t h4[2], l4[2];
-#pragma unroll
-            for (int j = 0; j < 2; j++) {
-                float h[4], l[4];
-#pragma unroll
-                for (int k = 0; k < 4; k++) {
-                    const uint32_t e = v[2 * j + (k >> 1)];
-                    const float y = __uint_as_float((k & 1) ? e & 0xffff0000u : e << 16) * f;
-                    h[k] = part_hi(y);
-                    l[k] = y - h[k];
-                }
-                h4[j] = e4m3x4_rn(h[0], h[1], h[2], h[3]);
-                l4[j] = e4m3x4_rn(l[0], l[1], l[2], l[3]);
-            }
-            if (at[i] >= 0) {
-                // 16-byte chunks of a row are permuted as the tensor copies permute the keys'
-                const int rr = r + i * kPass + sub;
-                const uint32_t swz = D == 128 ? (uint32_t)(rr & 7) : (uint32_t)((rr >> 1) & 3);
-                unsigned char *dst = q0 + (uint32_t)rr * D + (((uint32_t)(col >> 1) ^ swz) << 4) + (uint32_t)(col & 1) * 8u;
-                *reinterpret_cast<uint2 *>(dst) = make_uint2(h4[0], h4[1]);
-                *reinterpret_cast<uint2 *>(dst + R * D) = make_uint2(l4[0], l4[1]);
-                if (col == 0) {
-                    RowInfo ri;
-                    ri.row = at[i];
-                    ri.head = hx[i];
-                    ri.qs = __uint_as_float((uint32_t)(127 - up) << 23);
-                    ri.pos = before + (at[i] - row0);
-                    rows[rr] = ri;
-                }
+            for (int j = 0; j < 4; j++) {
+                const uint32_t m = v[j] & kMag;
+                top = __vmaxu2(top, m & ~__vcmpgeu2(m, 0x7f807f80u));
             }
         }
+        top = max(top & 0xffffu, top >> 16);
+#pragma unroll kUnroll
+        for (int d = kLanes / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
+        const int up = top == 0 ? 0 : min(126, 7 - ((int)(top >> 7) - 127));
+        const float f = __uint_as_float((uint32_t)(127 + up) << 23);
+        ri.qs = __uint_as_float((uint32_t)(127 - up) << 23);
+        // 16-byte chunks of a row are permuted as the tensor copies permute the keys'
+        const int rr = r + sub;
+        const uint32_t swz = D == 128 ? (uint32_t)(rr & 7) : (uint32_t)((rr >> 1) & 3);
+        unsigned char *dst = q0 + (uint32_t)rr * D + (((uint32_t)(col >> 1) ^ swz) << 4) + (uint32_t)(col & 1) * 8u;
+#pragma unroll kUnroll
+        for (int j = 0; j < 4; j++) {
+            const float y0 = __uint_as_float(v[0] << 16) * f, y1 = __uint_as_float(v[0] & 0xffff0000u) * f;
+            const float h0 = part_hi(y0), h1 = part_hi(y1);
+            if (rr < r1) {
+                *reinterpret_cast<uint16_t *>(dst + 2 * j) = (uint16_t)e4m3x2_rn(h0, h1);
+                *reinterpret_cast<uint16_t *>(dst + R * D + 2 * j) = (uint16_t)e4m3x2_rn(y0 - h0, y1 - h1);
+            }
+            v[0] = v[1];
+            v[1] = v[2];
+            v[2] = v[3];
+        }
+        if (rr < r1 && col == 0) rows[rr] = ri;
     }
     fence_proxy_async_smem();
     __syncwarp();
@@ -591,10 +587,8 @@ struct Walk {
     int it;
     Item x;
 
-    __device__ __forceinline__ Walk(const AttnArgs &a_, const Line &l, int worker, const Start &st)
-        : a(a_), w(l.cut(worker)), hi(l.cut(worker + 1)), first(st.first), it(st.item), x(st.x) {
-        if (worker >= l.workers) hi = w;
-    }
+    __device__ __forceinline__ Walk(const AttnArgs &a_, const Start &st)
+        : a(a_), w(st.lo), hi(st.hi), first(st.first), it(st.item), x(st.x) {}
 
     // The next segment; count 0 at the end of the share.
     __device__ __forceinline__ Seg next() {
@@ -625,7 +619,15 @@ struct Walk {
             g.n = x.n;
             g.len = x.len;
             g.row0 = x.row0;
-            const int q0 = x.rt * a.rpt / a.group, q1 = min(x.n - 1, ((x.rt + 1) * a.rpt - 1) / a.group);
+            // the tile's first and last row, and the first's head of the group
+            int q0 = 0, q1 = x.n - 1;
+            if (a.nrt > 1) {
+                q0 = x.rt * a.rpt / a.group;
+                q1 = min(q1, ((x.rt + 1) * a.rpt - 1) / a.group);
+            }
+            g.q0 = q0;
+            g.q1 = q1;
+            g.h0 = x.rt * a.rpt - q0 * a.group;
             g.see_all = min(x.len, max(0, x.len - x.n + q0 + 1));
             g.see_max = min(x.len, max(0, x.len - x.n + q1 + 1));
             g.nt = x.nt;
@@ -634,6 +636,18 @@ struct Walk {
         return g;
     }
 };
+
+// Asks for a segment's queries ahead of their use (into L2): rows' heads of the group lie side
+// by side.
+__device__ __forceinline__ void prefetch_queries(const AttnArgs &a, const Seg &g) {
+    const int bytes = a.group * a.k.kv.dim * 2;
+    const char *at = reinterpret_cast<const char *>(a.k.q + (size_t)(g.row0 + g.q0) * a.k.ldq) + (size_t)g.head * bytes;
+#pragma unroll 1
+    for (int r = g.q0; r <= g.q1; r++, at += a.k.ldq * 2)
+#pragma unroll 1
+        for (int i = (threadIdx.x & 31) * 128; i < bytes; i += 32 * 128)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(at + i));
+}
 
 // Value rows of the tile's tokens in shared memory, for one tile that not every row sees
 // whole (thread = token `tok` of the tile, which is token t of the sequence): rows that no
@@ -692,8 +706,8 @@ __device__ __forceinline__ void join_role(const AttnArgs &a, const Line &line, i
         c0[i] = parts[i] = mine[i] = 0;
         if (i < shared) {
             const Seg &g = list[i];
-            c0[i] = worker_of(g.u0, line.total, line.workers);
-            parts[i] = worker_of(g.u0 + g.nt - 1, line.total, line.workers) - c0[i] + 1;
+            c0[i] = line.worker_of(g.u0);
+            parts[i] = line.worker_of(g.u0 + g.nt - 1) - c0[i] + 1;
             const int nrows = min(a.rpt, g.n * a.group - g.rt * a.rpt);
             mine[i] = max(0, (nrows - (worker - c0[i]) + parts[i] - 1) / parts[i]);  // rows worker - c0, + parts, ...
         }

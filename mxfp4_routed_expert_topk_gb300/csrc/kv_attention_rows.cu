@@ -129,24 +129,11 @@ __device__ __forceinline__ void copy_role(const AttnArgs &a, const CUtensorMap *
     }
 }
 
-// Asks for a segment's queries ahead of their use (into L2).
-__device__ __forceinline__ void prefetch_queries(const AttnArgs &a, const Seg &g) {
-    const int first = g.rt * a.rpt, live = min(a.rpt, g.n * a.group - first);
-    const int q0 = first / a.group, q1 = (first + live - 1) / a.group;
-    const int lines = (a.group * a.k.kv.dim * 2 + 127) / 128;  // a row's heads of the group lie side by side
-#pragma unroll 1
-    for (int i = threadIdx.x & 31; i < (q1 - q0 + 1) * lines; i += 32) {
-        const int r = i / lines;
-        const uint16_t *at = a.k.q + (size_t)(g.row0 + q0 + r) * a.k.ldq + (size_t)g.head * a.group * a.k.kv.dim;
-        asm volatile("prefetch.global.L2 [%0];" ::"l"(at + (i - r * lines) * 64));
-    }
-}
-
 // Publishes the worker's segments, then one with count 0.
 __device__ __forceinline__ void segment_role(const AttnArgs &a, unsigned char *smem, const CommonSmem &L, const Bars &B,
-                                             const Line &line, const Start &start, int *abort_flag) {
+                                             const Start &start, int *abort_flag) {
     Seg *ring = reinterpret_cast<Seg *>(smem + L.seg);
-    Walk W(a, line, (int)blockIdx.x, start);
+    Walk W(a, start);
 #pragma unroll 1
     for (int i = 0;; i++) {
         const int ss = i % kSegs;
@@ -361,7 +348,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             if (lane == 0) drain(B.mma_done(), 0u, abort_flag);
             __syncwarp();
         } else {
-            segment_role(a, smem, L, B, line, *start, abort_flag);
+            segment_role(a, smem, L, B, *start, abort_flag);
         }
     } else if (warp < kJoinWarp) {
         regs_dec<kRegsSoft>();
@@ -524,9 +511,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             if (!warp_wait(B.seg_full(s % kSegs), (uint32_t)(s / kSegs) & 1u, 0xe20u, abort_flag) ||
                 !warp_wait(B.q_empty(s & 1), ((uint32_t)(s >> 1) & 1u) ^ 1u, 0xe00u, abort_flag))
                 return;
-            load_queries<D, kRows, 1>(a, reinterpret_cast<RowInfo *>(smem + L.rows) + (s & 1) * kRows,
-                                      smem + L.q + (uint32_t)(s & 1) * (2u * kRows * D),
-                                      reinterpret_cast<const Seg *>(smem + L.seg)[s % kSegs], ew, 4);
+            const Seg &g = reinterpret_cast<const Seg *>(smem + L.seg)[s % kSegs];
+            if (g.count > 0)
+                load_queries<D, kRows, 4>(a, reinterpret_cast<RowInfo *>(smem + L.rows) + (s & 1) * kRows,
+                                          smem + L.q + (uint32_t)(s & 1) * (2u * kRows * D), g, ew, 4);
             if (lane == 0) mbar_arrive(B.q_full(s & 1));
         };
         queries(0);
