@@ -383,11 +383,12 @@ __device__ __forceinline__ bool lane_wait(uint64_t *bar, uint32_t parity, unsign
     return true;
 }
 
-// Wait for copies or MMAs in flight, before the CTA exits, even after an abort (within the limit).
+// Wait for copies or MMAs in flight, before the CTA exits, even after an abort: within the
+// limit, but never less than 0.1 s, as what is in flight writes to this CTA's memory.
 __device__ __forceinline__ void drain(uint64_t *bar, uint32_t parity, int *abort_flag) {
-    const uint64_t t0 = global_timer_ns();
+    const uint64_t t0 = global_timer_ns(), lim = max(g_wait_limit_ns, (uint64_t)100000000);
     while (!mbar_try_wait(bar, parity)) {
-        if (global_timer_ns() - t0 > g_wait_limit_ns) {
+        if (global_timer_ns() - t0 > lim) {
             *(volatile int *)abort_flag = 0xfff;
             break;
         }

@@ -290,6 +290,28 @@ def test_attention_shows_nan_that_a_row_sees(n, old):
     assert torch.isnan(out).all() and torch.isnan(lse).all()
 
 
+@pytest.mark.parametrize("n", [1, 9])
+def test_attention_wait_that_runs_out_is_reported(n):
+    """With a wait limit far below a kernel's start, every role gives up, drains what it has in
+    flight and reports; the same workspace then serves the next call."""
+    c = Case([n] * 40, [400 * i for i in range(40)], 2, 7, 128, 64, seed=n)
+    ws = moe.workspace(moe.moe_kv_attention_workspace_size(c.cache, n, 14))
+    call = lambda: moe.moe_kv_attention(c.cache, 0, c.q, c.dev(c.cu), c.dev(c.lens), c.dev(c.table),  # noqa: E731
+                                        max_rows=n, ws=ws)
+    want = call()
+    assert moe.moe_check_status(ws) == moe.MOE_OK
+    moe.moe_debug_set_wait_limit(200)  # ns
+    try:
+        call()
+        got = moe.moe_check_status(ws)
+    finally:
+        moe.moe_debug_set_wait_limit(0)
+    assert got == moe.MOE_ERR_TIMEOUT
+    moe.moe_clear_status(ws)
+    assert torch.equal(call().view(torch.int16), want.view(torch.int16))
+    assert moe.moe_check_status(ws) == moe.MOE_OK
+
+
 def test_attention_wide_range_of_weights():
     """One token far above the rest, and a long tail of tiny weights that together matter."""
     c = Case([1], [3000], 1, 4, 128, 64, seed=11)
