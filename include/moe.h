@@ -365,8 +365,8 @@ moe_status moe_kv_append(const moe_kv *kv, int layer, const uint16_t *k, size_t 
  * multiple of 8, 16-byte aligned); heads_q a multiple of heads, query heads
  * g * (heads_q / heads) .. share key/value head g.  Sequence b has the rows cu_rows[b] ..
  * cu_rows[b+1]-1, n of them, at most max_rows (more rows take more tiles; max_rows * heads_q /
- * heads <= 2^24), and kv_len[b] tokens (at most 2^30).  Row i of it stands at token kv_len[b] - n + i and sees tokens 0 up to
- * and with that one: causal among the new rows.  Out: out (like q, ldo) =
+ * heads <= 2^24), and kv_len[b] tokens (at most 2^30).  Row i of it stands at token
+ * kv_len[b] - n + i and sees tokens 0 up to and with that one: causal among the new rows.  Out: out (like q, ldo) =
  * sum_t softmax_t(scale * q . k_t) v_t in bf16; lse [rows][heads_q] fp32 (or NULL) = the
  * natural logarithm of sum_t exp(scale * q . k_t).  A row that sees no token gives out = 0
  * and lse = -infinity.  Keys and values a row does not see do not reach it, whatever they
@@ -377,7 +377,8 @@ moe_status moe_kv_append(const moe_kv *kv, int layer, const uint16_t *k, size_t 
  * the cache; scores, maxima, sums and outputs are fp32.  The result does not depend on
  * timing, and a token whose page is outside the cache or past the table is reported as
  * MOE_ERR_BAD_PAGE (the sequence's rows are then not valid), as are more rows than
- * max_rows.  ws: moe_kv_attention_workspace_size() bytes for the current device. */
+ * max_rows.  ws: moe_kv_attention_workspace_size() bytes for the current device (what serves
+ * max_rows serves fewer, too). */
 moe_status moe_kv_attention_workspace_size(const moe_kv *kv, int max_rows, int heads_q, size_t *bytes);
 moe_status moe_kv_attention(const moe_kv *kv, int layer, const uint16_t *q, size_t ldq, int rows, int heads_q,
                             const int32_t *cu_rows, const int32_t *kv_len, const int32_t *page_table,

@@ -1,19 +1,23 @@
-// Cache attention, the form for few rows (up to 32 per row tile: all query heads of a
-// key/value head of one token, or of a few drafted ones), and the choice between the forms.
+// Cache attention, the form for few rows (up to 16 per row tile: all query heads of a
+// key/value head of one token, or of two or three drafted ones), and the choice between the forms.
 //
 // Tokens, not rows, lie along M: S^T = K Q^T (M = 128 tokens, N = rows) and O^T = V^T P^T
 // (M = head_dim, N = rows, K = 128 tokens).  However few the rows, every MMA is full along M,
 // and K and V are its A operand (V^T is V's tile read M-major).  The TMEM lane of a score is
 // its token, so a thread has one token's scores and writes the rows' weights as one vector of
-// its token (P^T is N-major); the maximum and sum of a row run across lanes, by halving
-// exchanges that leave each lane one row.
+// its token (P^T is N-major); the maximum and sum of a row run across lanes.
 //
-// What bounds it is the time one tile takes from its scores to its output (about 2800 clocks:
-// TMEM read, two cross-lane reductions, a warpgroup barrier, the exponentials, the fences and
-// the two MMA groups), twice what the tile's 32 KB take from HBM.  So three warpgroups take
-// tiles in turn, each with its own running maximum, sum and output, joined in shared memory at
-// the segment's end; keys and values have rings of their own, as a key stage is free as soon
-// as the scores are there, while a value stage waits for the weights.
+// What bounds it is HBM for long sequences: one token for each of 64 sequences of up to 16384
+// (8 heads of 128, 7 query heads each) takes 197 us at 1119 MB, 5.7 TB/s (84 % of a copy's rate).
+// A tile takes about 2800 clocks from its scores to its output (TMEM read, two cross-lane
+// reductions, a warpgroup barrier, the exponentials, the fences and the two MMA groups), twice
+// what its 32 KB take from HBM.  So a CTA has three workers, each a softmax warpgroup with a
+// warp that feeds it, and each worker has a share of its own: nothing is exchanged between
+// them, and one's end of a unit overlaps with the others' tiles.  (Three warpgroups on one
+// share, joined at each unit's end: 256 sequences of 128 tokens 84 us, so 44, both from cold
+// caches.  Four such: 66 us in place of 62 for 96 sequences of 512.)  Short calls are bound by
+// the start (8 us: launch, shares, the first loads) and by code that runs once: fetching it from
+// cold caches takes 300 clocks per 8 instructions.
 #include <algorithm>
 
 #include "kv_attention.cuh"
@@ -21,7 +25,10 @@
 namespace moe {
 namespace {
 
-constexpr int kRows = 16;     // rows of a row tile
+// Rows of a row tile.  (A form of 32 with two outputs' worth of registers took 165 us for 4 rows
+// in each of 24 sequences of 8192, where the rows form takes 144; with 16 or fewer the rows form
+// takes 138 us where this one takes 98.)
+constexpr int kRows = 16;
 // Workers of a CTA, a softmax warpgroup each.
 constexpr int kWorkers = 3;
 constexpr int kThreads = 32 * kFirstSoft + 128 * kWorkers;
@@ -39,9 +46,9 @@ struct FewSmem {
         rows = o;   o += (uint32_t)kWorkers * 2u * kRows * (uint32_t)sizeof(RowInfo);  // [worker][buffer]
         smax = o;   o += (uint32_t)kWorkers * 2u * 4u * kRows * 4u;                 // [worker][2][warp][row]
         ref = o;    o += (uint32_t)kWorkers * 4u * kRows * 8u;                      // [warp][row] (query scale, reference)
-        ab = o;     o += (uint32_t)kWorkers * 4u * kRows * 8u;                      // [warp][row] (factor of the old output, of the new)
+        ab = o;     o += (uint32_t)kWorkers * 4u * kRows * 8u;                      // [warp][row] (factors of the outputs)
         lsum = o;   o += (uint32_t)kWorkers * 4u * kRows * 4u;                      // [warp][row]
-        nan = o;    o += (uint32_t)kWorkers * 2u * 4u * 4u;                         // [worker][2][warp] tokens whose values hold partial NaN
+        nan = o;    o += (uint32_t)kWorkers * 2u * 4u * 4u;                         // [worker][2][warp] tokens with NaN values
         seg = o;    o += (uint32_t)kWorkers * 2u * (uint32_t)sizeof(Seg);           // [worker][buffer]
         split = o;  o += (uint32_t)kWorkers * 2u * (uint32_t)sizeof(Seg);           // units shared with other workers
         bars = o;   o += ((uint32_t)kWorkers * 16u + 1u) * 8u;
@@ -516,7 +523,7 @@ int rows_per_tile(int max_rows, int group) {
 template <int D>
 cudaError_t launch_few(const CUtensorMap &tm, AttnArgs a, int sms, int smem_max, cudaStream_t st) {
     static PerDevice smem_set(0);
-    a.over = 2;
+    a.over = 2;  // (1 to 4 measure alike)
     const size_t smem = FewSmem(D).total + 1024;
     if (smem > (size_t)smem_max) return cudaErrorNotSupported;
     cudaError_t e = ensure_dynamic_smem(kv_attention_few_kernel<D>, smem, smem_set);

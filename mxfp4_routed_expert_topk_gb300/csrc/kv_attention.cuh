@@ -1,5 +1,5 @@
-// What the two forms of the cache attention share: the division of work, the copy and
-// query-loading roles, and the joining of results that several CTAs hold parts of.
+// What the two forms of the cache attention share: the division of work, copies, query loading,
+// and the joining of results that several workers hold parts of.
 //
 //   s[t][r] = ks_t * (k_t . q_r),  m_r = max_t s,  o_r = sum_t 2^(s - m) vs_t v_t / sum_t 2^(s - m)
 //
@@ -17,13 +17,14 @@
 //     stands above the tile.  The pages' value scales, relative to the tile's largest,
 //     multiply the weights before they are split.
 //   - Work: the (sequence, row tile, head, 128-token tile) units of the call in one line, cut
-//     into equal shares, one per SM.  A share may begin and end inside a sequence: such
-//     partial results go to the workspace and, after a grid barrier (cooperative launch), the
-//     CTAs that worked on the sequence join it, each some rows.  Shares are cut by the lengths
-//     on the device, so a captured graph serves any lengths.
+//     into equal shares, one per worker (one or three of an SM).  A share may begin and end
+//     inside a sequence: such partial results go to the workspace and, after a grid barrier
+//     (cooperative launch), the workers that share the sequence join it, each some rows.  Shares
+//     are cut by the lengths on the device, so a captured graph serves any lengths.
 //
-// Roles of a CTA: warp 0 copies keys, warp 2 values and scales; warp 1 issues MMAs; warp 3
-// loads the next segment's queries; the rest are softmax warpgroups.
+// Roles of a CTA: warp 1 issues MMAs; the other three of the first four warps walk the share,
+// copy tiles and load queries (one for each worker in the few-rows form; keys, values and the
+// walk in the rows form); the rest are softmax warpgroups.
 #pragma once
 
 #include "kv_internal.cuh"
@@ -48,7 +49,7 @@ struct AttnArgs {
     int group;      // query heads per key/value head
     int rpt;        // rows per row tile
     int nrt;        // row tiles of max_rows rows
-    int nk, nv;     // stages of the key and value rings
+    int nk, nv;     // stages of the key and value rings (rows form)
     int over;       // what starting a unit costs, in tiles
     float scale2;   // scale * log2(e)
     float *part;    // partial results: 2 slots per worker of [rpt][dim] + [rpt][2]
@@ -503,7 +504,8 @@ struct Pages {
 // fetching an unrolled loop costs more than the latency that it hides (four passes in flight:
 // one sequence of 300 tokens 31 us in place of 27).  kUnroll: words converted at once.
 template <int D, int R, int kUnroll>
-__device__ __forceinline__ void load_queries(const AttnArgs &a, RowInfo *rows, unsigned char *q0, const Seg &g, int w, int nw) {
+__device__ __forceinline__ void load_queries(const AttnArgs &a, RowInfo *rows, unsigned char *q0, const Seg &g, int w,
+                                             int nw) {
     constexpr int kLanes = D / 8, kPass = 32 / kLanes;
     const int lane = threadIdx.x & 31, sub = lane / kLanes, col = lane % kLanes;
     const int live = min(a.rpt, g.n * a.group - g.rt * a.rpt);  // rows of the tile
@@ -805,7 +807,7 @@ __device__ __forceinline__ void join_role(const AttnArgs &a, const Line &line, i
 }  // namespace
 
 // The two forms, by the number of rows of a row tile: tokens along the tensor cores' M for
-// up to 32 rows (kv_attention.cu), rows along M for up to 128 (kv_attention_rows.cu).
+// up to 16 rows (kv_attention.cu), rows along M for up to 128 (kv_attention_rows.cu).
 cudaError_t launch_attention_rows(const CUtensorMap &tm, AttnArgs a, int sms, int smem_max, cudaStream_t st);
 cudaError_t set_wait_limit_kv_attention_rows(uint64_t ns);
 

@@ -1,4 +1,4 @@
-// Cache attention, the form for row tiles of more than 32 rows (a verification batch's rows
+// Cache attention, the form for row tiles of more than 16 rows (a verification batch's rows
 // times the query heads of a key/value head, or a prompt's).
 //
 // Rows lie along M: S = Q K^T (M = 128 rows, N = 128 tokens, both operands K-major) and
@@ -10,11 +10,17 @@
 //
 // What bounds it is instruction issue and latency: 128 x 128 scores a tile at 7 to 8
 // instructions each are about 1000 clocks of all four schedulers, next to 1400 that the tile's
-// 32 KB take from HBM and 1024 of the tensor pipe.  So the work is split by role: softmax
-// warpgroups take tiles in turn (a thread per row) over three score buffers, so that the next
-// scores are ready when a warpgroup comes for them, and one more warpgroup joins each tile's
-// output with the running one as soon as it is there, which frees the single output buffer.
-// Registers go to the warpgroups by need (setmaxnreg).
+// 32 KB take from HBM and 1024 of the tensor pipe; a tile takes 2700.  So the work is split by
+// role: softmax warpgroups take tiles in turn (a thread per row) over three score buffers, so
+// that the next scores are ready when a warpgroup comes for them, and one more warpgroup joins
+// each tile's output with the running one as soon as it is there, which frees the single output
+// buffer.  Registers go to the warpgroups by need (setmaxnreg).  17 rows in each of 4 sequences
+// of 131072 tokens (7 query heads of 8 x 128) take 329 us: 0.48 of the HBM and 0.41 of the bf16
+// rate; without the joining warpgroup and the third buffer 438.  Not better: weights as one
+// fp16 part with V's tile converted to fp16 (346 us with two softmax warpgroups, 352 with three),
+// and, for up to 64 rows, the rows twice or four times in the tile with the tokens divided among
+// the copies (4 rows in 24 sequences of 8192 144 -> 138 us, heads of 64 80 -> 62, but each unit
+// 2.5 us longer: 24 ragged ones of 5 rows 107 -> 121).
 #include <algorithm>
 
 #include "kv_attention.cuh"
@@ -633,7 +639,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
 template <int D>
 cudaError_t launch(const CUtensorMap &tm, AttnArgs a, int sms, int smem_max, cudaStream_t st) {
     static PerDevice smem_set(0);
-    a.over = 3;
+    a.over = 3;  // (2 to 5 measure alike)
     a.nk = a.nv = 2;
     while (true) {  // as many stages as fit, values first
         AttnArgs b = a;

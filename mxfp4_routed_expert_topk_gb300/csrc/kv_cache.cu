@@ -232,20 +232,14 @@ cudaError_t launch_kv_append(KvAppendArgs a, cudaStream_t st) {
     if (blocks > 0x7fffffff) return cudaErrorNotSupported;
     const dim3 grid((unsigned)blocks);
     TraceScope trace_scope("kv_append", st);
-    const bool wide = a.kv.dim == 128;
+    auto launch = [&](auto wide, auto narrow) {
+        a.kv.dim == 128 ? wide<<<grid, kThreads, 0, st>>>(a) : narrow<<<grid, kThreads, 0, st>>>(a);
+    };
     switch (a.kv.page) {
-        case 16:
-            wide ? kv_append_kernel<2, 128><<<grid, kThreads, 0, st>>>(a) : kv_append_kernel<1, 64><<<grid, kThreads, 0, st>>>(a);
-            break;
-        case 32:
-            wide ? kv_append_kernel<4, 128><<<grid, kThreads, 0, st>>>(a) : kv_append_kernel<2, 64><<<grid, kThreads, 0, st>>>(a);
-            break;
-        case 64:
-            wide ? kv_append_kernel<8, 128><<<grid, kThreads, 0, st>>>(a) : kv_append_kernel<4, 64><<<grid, kThreads, 0, st>>>(a);
-            break;
-        case 128:
-            wide ? kv_append_kernel<16, 128><<<grid, kThreads, 0, st>>>(a) : kv_append_kernel<8, 64><<<grid, kThreads, 0, st>>>(a);
-            break;
+        case 16: launch(kv_append_kernel<2, 128>, kv_append_kernel<1, 64>); break;
+        case 32: launch(kv_append_kernel<4, 128>, kv_append_kernel<2, 64>); break;
+        case 64: launch(kv_append_kernel<8, 128>, kv_append_kernel<4, 64>); break;
+        case 128: launch(kv_append_kernel<16, 128>, kv_append_kernel<8, 64>); break;
         default: return cudaErrorNotSupported;
     }
     return cudaGetLastError();
