@@ -36,7 +36,7 @@ constexpr int kThreads = 32 * kFirstSoft + kSoft;
 constexpr int kRows = 128;
 // Registers of a thread: at launch, then by role; the sum over the warpgroups is no more than
 // what the launch allocated (512 x 128).
-constexpr int kRegsIssue = 96, kRegsSoft = 112, kRegsJoin = 192;
+constexpr int kRegsIssue = 80, kRegsSoft = 120, kRegsJoin = 192;
 static_assert(kRegsIssue + kGroups * kRegsSoft + kRegsJoin <= 4 * 128 && kThreads == 512, "register split");
 constexpr int kBarAll = 7;
 
@@ -55,7 +55,8 @@ struct CommonSmem {
         seg = o;    o += (uint32_t)kSegs * (uint32_t)sizeof(Seg);
         split = o;  o += 2u * (uint32_t)sizeof(Seg);                       // units shared with other CTAs
         rows = o;   o += 2u * (uint32_t)rows_ * (uint32_t)sizeof(RowInfo);
-        bars = o;   o += 64u * 8u;
+        bars = o;   o += (4u * kMaxStages + 29u + kMaxStages) * 8u;
+        o = (o + 15u) & ~15u;
         misc = o;   o += 512u;
         total = o;
     }
@@ -77,6 +78,7 @@ struct Bars {
     __device__ uint64_t *mma_done() const { return b + 4 * kMaxStages + 20; }
     __device__ uint64_t *seg_full(int s) const { return b + 4 * kMaxStages + 21 + s; }
     __device__ uint64_t *seg_empty(int s) const { return b + 4 * kMaxStages + 25 + s; }
+    __device__ uint64_t *c_full(int s) const { return b + 4 * kMaxStages + 29 + s; }  // a value stage's constants
 };
 
 // One side's copies (SIDE 0: keys, 1: values and scales); P: page size (a constant, as the
@@ -135,26 +137,6 @@ __device__ __forceinline__ void copy_role(const AttnArgs &a, const CUtensorMap *
     }
 }
 
-// Publishes the worker's segments, then one with count 0.
-__device__ __forceinline__ void segment_role(const AttnArgs &a, unsigned char *smem, const CommonSmem &L, const Bars &B,
-                                             const Start &start, int *abort_flag) {
-    Seg *ring = reinterpret_cast<Seg *>(smem + L.seg);
-    Walk W(a, start);
-#pragma unroll 1
-    for (int i = 0;; i++) {
-        const int ss = i % kSegs;
-        if (!warp_wait(B.seg_empty(ss), ((uint32_t)(i / kSegs) & 1u) ^ 1u, 0xe10u, abort_flag)) return;
-        const Seg g = W.next();
-        if ((threadIdx.x & 31) == 0) {
-            ring[ss] = g;
-            mbar_arrive(B.seg_full(ss));
-        }
-        __syncwarp();
-        if (g.count == 0) return;
-        prefetch_queries(a, g);
-    }
-}
-
 struct RowsSmem {
     CommonSmem c;
     uint32_t ml, fac, chunk, nan, total;
@@ -164,7 +146,8 @@ struct RowsSmem {
         fac = o;   o += 4u * 4u;                 // [4 tiles] value of a weight unit
         nan = o;   o += 4u * 4u * 4u;            // [4 tiles][warp] tokens whose values hold partial NaN
         o = (o + 15u) & ~15u;
-        chunk = o; o += 4u * kGroups * kMaxSlots * 16u;    // [warp][page] (key scale, log2 weight scale, 1 / weight scale)
+        // [value stage][page] (key scale, log2 weight scale, 1 / weight scale, value of a weight unit)
+        chunk = o; o += (uint32_t)nv * kMaxSlots * 16u;
         total = o;
     }
 };
@@ -211,6 +194,63 @@ __device__ __forceinline__ void regs_dec() {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
 }
 
+// Publishes the worker's segments, then one with count 0, and the constants of each tile's
+// pages (lane j has page j), which are then no part of the softmax warps' time (400 clocks of
+// 5400 a tile).  A tile's constants stand beside its value stage: nothing more says that their
+// place is free.
+__device__ __forceinline__ void segment_role(const AttnArgs &a, unsigned char *smem, const RowsSmem &F, const Bars &B,
+                                             const Start &start, int *abort_flag) {
+    const int lane = threadIdx.x & 31, slots = kTokens / a.k.kv.page;
+    Seg *ring = reinterpret_cast<Seg *>(smem + F.c.seg);
+    const float *scales = reinterpret_cast<const float *>(smem + F.c.scales);
+    float4 *chunk = reinterpret_cast<float4 *>(smem + F.chunk);
+    Walk W(a, start);
+    Watch eye = lane == 0 ? Watch{B.seg_empty(0), kSegs, 0, 1u} : Watch{B.v_full(0), a.nv, 0, 0u};
+    int published = 0, known = 0, u = 0;  // segments, their tiles; tiles whose constants are there
+    bool ended = false;
+    uint64_t idle = 0;
+#pragma unroll 1
+    while (!ended || u < known) {
+        const uint32_t m = __ballot_sync(0xffffffffu, lane < 2 && eye.ready());
+        const bool publish = !ended && (m & 1u) != 0u, constants = u < known && (m & 2u) != 0u;
+        if (constants && !publish) {
+            const int vb = u % a.nv;
+            const float *sc = scales + vb * 2 * kMaxSlots;
+            __syncwarp();  // (lane 1 has seen the copies land)
+            const float ks = sc[lane & 7] * a.scale2, vs = lane < slots ? sc[kMaxSlots + lane] : 0.f;
+            const bool fin = vs < INFINITY;
+            float vone = fin ? vs : 0.f;
+#pragma unroll
+            for (int d = 4; d > 0; d >>= 1) vone = fmaxf(vone, __shfl_xor_sync(0xffffffffu, vone, d));
+            vone = vone > 0.f ? vone : 1.f;
+            const float c = fmaxf(256.f * __fdividef(vs, vone), 8.67361738e-19f);  // at least 2^-60
+            if (lane < kMaxSlots)
+                chunk[vb * kMaxSlots + lane] =
+                    make_float4(ks, fin ? lg2(c) : kNan, fin ? __fdividef(1.f, c) : 1.f, vone * (1.f / 256.f));
+            __syncwarp();
+            if (lane == 0) mbar_arrive(B.c_full(vb));
+            u++;
+            if (lane == 1) eye.next();
+        } else if (publish) {
+            const Seg g = W.next();
+            if (lane == 0) {
+                ring[published % kSegs] = g;
+                mbar_arrive(B.seg_full(published % kSegs));
+                eye.next();
+            }
+            __syncwarp();
+            published++;
+            known += g.count;
+            ended = g.count == 0;
+            if (!ended) prefetch_queries(a, g);
+        } else {
+            if (__any_sync(0xffffffffu, expired(idle, 0xe10u, abort_flag))) return;
+            continue;
+        }
+        idle = 0;
+    }
+}
+
 template <int D>
 __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __grid_constant__ CUtensorMap tm,
                                                                          const AttnArgs a) {
@@ -241,6 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         for (int s = 0; s < a.nv; s++) {
             mbar_init(B.v_full(s), 1 + kTokens / a.k.kv.page);
             mbar_init(B.v_empty(s), 1);
+            mbar_init(B.c_full(s), 1);
         }
         for (int b = 0; b < 2; b++) {
             mbar_init(B.q_full(b), 4);
@@ -354,7 +395,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             if (lane == 0) drain(B.mma_done(), 0u, abort_flag);
             __syncwarp();
         } else {
-            segment_role(a, smem, L, B, *start, abort_flag);
+            segment_role(a, smem, F, B, *start, abort_flag);
         }
     } else if (warp < kJoinWarp) {
         regs_dec<kRegsSoft>();
@@ -365,9 +406,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         float2 *ml = reinterpret_cast<float2 *>(smem + F.ml);
         float *fac = reinterpret_cast<float *>(smem + F.fac);
         uint32_t *nan = reinterpret_cast<uint32_t *>(smem + F.nan);
-        float4 *chunk = reinterpret_cast<float4 *>(smem + F.chunk) + sw * kMaxSlots;
-        const float *scales = reinterpret_cast<const float *>(smem + L.scales);
-        const int page_shift = 31 - __clz(a.k.kv.page), slots = kTokens >> page_shift;
+        const int page_shift = 31 - __clz(a.k.kv.page);
         int done = 0;  // tiles of earlier segments
 
 #pragma unroll 1
@@ -384,27 +423,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
 #pragma unroll 1
             for (int t = (wg + kGroups - done % kGroups) % kGroups; t < count; t += kGroups) {
                 const int u = done + t, sb = u % kSBufs, vb = u % a.nv;
-                soft_wait(B.v_full(vb), (uint32_t)(u / a.nv) & 1u, 0xc10u + vb, abort_flag);
-                // constants of the tile's pages: lane j has page j
-                float unit;  // value of a weight unit
-                {
-                    const float *sc = scales + vb * 2 * kMaxSlots;
-                    const float ks = sc[lane & 7] * a.scale2, vs = lane < slots ? sc[kMaxSlots + lane] : 0.f;
-                    const bool fin = vs < INFINITY;
-                    float vone = fin ? vs : 0.f;
-#pragma unroll
-                    for (int d = 4; d > 0; d >>= 1) vone = fmaxf(vone, __shfl_xor_sync(0xffffffffu, vone, d));
-                    vone = vone > 0.f ? vone : 1.f;
-                    const float c = fmaxf(256.f * __fdividef(vs, vone), 8.67361738e-19f);  // at least 2^-60
-                    if (lane < kMaxSlots)
-                        chunk[lane] = make_float4(ks, fin ? lg2(c) : kNan, fin ? __fdividef(1.f, c) : 1.f, 0.f);
-                    unit = vone * (1.f / 256.f);
-                }
+                const float4 *chunk = reinterpret_cast<const float4 *>(smem + F.chunk) + vb * kMaxSlots;
+                soft_wait(B.c_full(vb), (uint32_t)(u / a.nv) & 1u, 0xc11u, abort_flag);
                 const bool special = (tile0 + t + 1) * kTokens > see_all;
                 const int lim = min(max(ri.pos + 1 - (tile0 + t) * kTokens, 0), kTokens);  // tokens the row sees
                 uint32_t word = 0;
                 if (special) {
                     const int tk = (tile0 + t) * kTokens + row;
+                    soft_wait(B.v_full(vb), (uint32_t)(u / a.nv) & 1u, 0xc10u + vb, abort_flag);
                     const bool bad = clean_values<D>(smem + L.v + (uint32_t)vb * kTile, row, tk, see_all, see_max);
                     word = __ballot_sync(0xffffffffu, bad);
                     fence_proxy_async_smem();
@@ -413,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                 // (from here on: these scores are there, so the outputs of tile u - 3 have been issued,
                 // so those of tile u - 4, whose places these are, have been joined)
                 if (lane == 0) {
-                    fac[u & 3] = unit;
+                    fac[u & 3] = chunk[0].w;
                     nan[(u & 3) * 4 + ew] = word;
                 }
                 tc_fence_after();
@@ -421,21 +447,24 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                 // loops over 32 tokens are not unrolled: the body must stay in the instruction cache
                 float mx = -INFINITY;
 #pragma unroll 1
-                for (int h = 0; h < kTokens; h += 32) {
-                    float x[32];
+                for (int h = 0; h < kTokens; h += 64) {
+                    float x[64];
                     tmem_ld32(ts + h, x);
+                    tmem_ld32(ts + h + 32, x + 32);
                     tmem_ld_wait(x);
                     if (special) {
 #pragma unroll
-                        for (int i = 0; i < 32; i++) x[i] = h + i < lim ? x[i] : -INFINITY;
+                        for (int i = 0; i < 64; i++) x[i] = h + i < lim ? x[i] : -INFINITY;
                     }
 #pragma unroll
-                    for (int q = 0; q < 2; q++) {
+                    for (int q = 0; q < 4; q++) {
                         float m4[4];
 #pragma unroll
                         for (int i = 0; i < 4; i++)
-                            m4[i] = fmaxf(fmaxf(x[16 * q + i], x[16 * q + 4 + i]), fmaxf(x[16 * q + 8 + i], x[16 * q + 12 + i]));
-                        mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * chunk[(h + 16 * q) >> page_shift].x);
+                            m4[i] = fmaxf(fmaxf(x[16 * q + i], x[16 * q + 4 + i]),
+                                          fmaxf(x[16 * q + 8 + i], x[16 * q + 12 + i]));
+                        mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) *
+                                           chunk[(h + 16 * q) >> page_shift].x);
                     }
                 }
                 const float mt = mx * ri.qs, base = mt == -INFINITY ? 0.f : mt;
