@@ -502,17 +502,20 @@ struct Pages {
 // lane takes 8 values, so a pass covers 2 rows of 128 or 4 of 64; the next pass's loads are in
 // flight while one is converted.  One pass per turn: this code runs once per segment, and
 // fetching an unrolled loop costs more than the latency that it hides (four passes in flight:
-// one sequence of 300 tokens 31 us in place of 27).  kUnroll: words converted at once.
-template <int D, int R, int kUnroll>
+// one sequence of 300 tokens 31 us in place of 27).  kUnroll: words converted at once;
+// kCopies: how often the rows stand in the tile.
+template <int D, int R, int kUnroll, int kCopies = 1>
 __device__ __forceinline__ void load_queries(const AttnArgs &a, RowInfo *rows, unsigned char *q0, const Seg &g, int w,
                                              int nw) {
     constexpr int kLanes = D / 8, kPass = 32 / kLanes;
     const int lane = threadIdx.x & 31, sub = lane / kLanes, col = lane % kLanes;
+    constexpr int kSpan = R / kCopies;                          // places of a copy
     const int live = min(a.rpt, g.n * a.group - g.rt * a.rpt);  // rows of the tile
     // rows past the tile see nothing (their queries are what was there: nobody reads their results)
-    for (int r = live + 32 * w + lane; r < R; r += 32 * nw) {
+    for (int r = live + 32 * w + lane; r < kSpan; r += 32 * nw) {
         RowInfo none = {-1, 0, 1.f, -1};
-        rows[r] = none;
+#pragma unroll
+        for (int i = 0; i < kCopies; i++) rows[r + i * kSpan] = none;
     }
     const int per = (live + nw * kPass - 1) / (nw * kPass) * kPass;  // (whole passes: any two warps write apart)
     const int r0 = min(w * per, live), r1 = min(r0 + per, live);
@@ -564,19 +567,25 @@ __device__ __forceinline__ void load_queries(const AttnArgs &a, RowInfo *rows, u
         const int rr = r + sub;
         const uint32_t swz = D == 128 ? (uint32_t)(rr & 7) : (uint32_t)((rr >> 1) & 3);
         unsigned char *dst = q0 + (uint32_t)rr * D + (((uint32_t)(col >> 1) ^ swz) << 4) + (uint32_t)(col & 1) * 8u;
+        uint64_t hi = 0, lo = 0;  // codes of the 8 values
 #pragma unroll kUnroll
         for (int j = 0; j < 4; j++) {
             const float y0 = __uint_as_float(v[0] << 16) * f, y1 = __uint_as_float(v[0] & 0xffff0000u) * f;
             const float h0 = part_hi(y0), h1 = part_hi(y1);
-            if (rr < r1) {
-                *reinterpret_cast<uint16_t *>(dst + 2 * j) = (uint16_t)e4m3x2_rn(h0, h1);
-                *reinterpret_cast<uint16_t *>(dst + R * D + 2 * j) = (uint16_t)e4m3x2_rn(y0 - h0, y1 - h1);
-            }
+            hi = hi >> 16 | (uint64_t)e4m3x2_rn(h0, h1) << 48;
+            lo = lo >> 16 | (uint64_t)e4m3x2_rn(y0 - h0, y1 - h1) << 48;
             v[0] = v[1];
             v[1] = v[2];
             v[2] = v[3];
         }
-        if (rr < r1 && col == 0) rows[rr] = ri;
+        if (rr < r1) {
+#pragma unroll
+            for (int i = 0; i < kCopies; i++) {  // (a copy lies whole swizzle periods further on)
+                *reinterpret_cast<uint64_t *>(dst + i * (kSpan * D)) = hi;
+                *reinterpret_cast<uint64_t *>(dst + (R + i * kSpan) * D) = lo;
+                if (col == 0) rows[rr + i * kSpan] = ri;
+            }
+        }
     }
     fence_proxy_async_smem();
     __syncwarp();

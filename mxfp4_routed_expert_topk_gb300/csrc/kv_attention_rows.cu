@@ -10,17 +10,25 @@
 //
 // What bounds it is instruction issue and latency: 128 x 128 scores a tile at 7 to 8
 // instructions each are about 1000 clocks of all four schedulers, next to 1400 that the tile's
-// 32 KB take from HBM and 1024 of the tensor pipe; a tile takes 2700.  So the work is split by
-// role: softmax warpgroups take tiles in turn (a thread per row) over three score buffers, so
-// that the next scores are ready when a warpgroup comes for them, and one more warpgroup joins
-// each tile's output with the running one as soon as it is there, which frees the single output
-// buffer.  Registers go to the warpgroups by need (setmaxnreg).  17 rows in each of 4 sequences
-// of 131072 tokens (7 query heads of 8 x 128) take 329 us: 0.48 of the HBM and 0.41 of the bf16
-// rate; without the joining warpgroup and the third buffer 438.  Not better: weights as one
-// fp16 part with V's tile converted to fp16 (346 us with two softmax warpgroups, 352 with three),
-// and, for up to 64 rows, the rows twice or four times in the tile with the tokens divided among
-// the copies (4 rows in 24 sequences of 8192 144 -> 138 us, heads of 64 80 -> 62, but each unit
-// 2.5 us longer: 24 ragged ones of 5 rows 107 -> 121).
+// 32 KB take from HBM and 1024 of the tensor pipe; a tile takes 2500.  So the work is split by
+// role: softmax warpgroups take tiles in turn (a thread per row) over two or three score buffers,
+// so that the next scores are ready when a warpgroup comes for them, one more warpgroup joins
+// each tile's output with the running one as soon as it is there, and a warp of its own prepares
+// the tiles' constants.  Registers go to the warpgroups by need (setmaxnreg).  17 rows in each of
+// 4 sequences of up to 131072 tokens (7 query heads of 8 x 128) take 313 us: 0.50 of the HBM and
+// 0.43 of the bf16 rate; with the constants in the softmax warps 331, and without the joining
+// warpgroup and the third score buffer 438.
+//
+// Row tiles of up to 64 (32) rows stand two (four) times in the 128 places, and each copy takes a
+// half (quarter) of every tile's tokens: its weights for the others are zero, and the copies'
+// outputs are added up at the end of the unit.  That halves (quarters) the softmax warps' work;
+// the joining warpgroup is then the slowest (1700 clocks a tile), so the softmax warps load the
+// queries.  24 sequences of 8192: 3 rows 136 -> 116 us, 9 rows 148 -> 136; heads of 64, 4 rows
+// 76 -> 55, 8 rows 79 -> 65; only units of one tile get slower (256 sequences of 128 tokens, 5
+// rows: 105 -> 115).
+//
+// Not better: weights as one fp16 part with V's tile converted to fp16 in shared memory (4 x 17:
+// 346 us with two softmax warpgroups, 352 with three, where two parts took 338).
 #include <algorithm>
 
 #include "kv_attention.cuh"
@@ -29,7 +37,7 @@ namespace moe {
 namespace {
 
 constexpr int kGroups = 2;                     // softmax warpgroups
-constexpr int kSBufs = 3;                      // score buffers
+constexpr int kRing = 8;                       // tiles whose references and sums are kept
 constexpr int kJoinWarp = kFirstSoft + 4 * kGroups;
 constexpr int kSoft = 128 * kGroups + 128;     // with the joining warpgroup
 constexpr int kThreads = 32 * kFirstSoft + kSoft;
@@ -38,7 +46,7 @@ constexpr int kRows = 128;
 // what the launch allocated (512 x 128).
 constexpr int kRegsIssue = 80, kRegsSoft = 120, kRegsJoin = 192;
 static_assert(kRegsIssue + kGroups * kRegsSoft + kRegsJoin <= 4 * 128 && kThreads == 512, "register split");
-constexpr int kBarAll = 7;
+constexpr int kBarAll = 7, kBarJoin = 1;
 
 constexpr int kMaxStages = 8;  // per ring
 constexpr int kSegs = 4;       // ring of segments
@@ -139,12 +147,16 @@ __device__ __forceinline__ void copy_role(const AttnArgs &a, const CUtensorMap *
 
 struct RowsSmem {
     CommonSmem c;
-    uint32_t ml, fac, chunk, nan, total;
-    __host__ __device__ RowsSmem(int dim, int nk, int nv) : c(dim, kRows, nk, nv) {
+    uint32_t ml, fac, chunk, nan, merge = 0, mlc = 0, total;
+    __host__ __device__ RowsSmem(int dim, int nk, int nv, int copies) : c(dim, kRows, nk, nv) {
         uint32_t o = (c.total + 127u) & ~127u;
-        ml = o;    o += 4u * kRows * 8u;         // [4 tiles][row] (reference, sum)
-        fac = o;   o += 4u * 4u;                 // [4 tiles] value of a weight unit
-        nan = o;   o += 4u * 4u * 4u;            // [4 tiles][warp] tokens whose values hold partial NaN
+        ml = o;    o += (uint32_t)kRing * kRows * 8u;  // [tile][row] (reference, sum)
+        fac = o;   o += (uint32_t)kRing * 4u;    // [tile] value of a weight unit
+        nan = o;   o += (uint32_t)kRing * 4u * 4u;  // [tile][warp] tokens whose values hold partial NaN
+        if (copies > 1) {
+            merge = o; o += 3u * 32u * 36u * 4u; // [warp of the copies but the first][lane][32 + 4] values of the head
+            mlc = o;   o += kRows * 8u;          // [place] (reference, sum)
+        }
         o = (o + 15u) & ~15u;
         // [value stage][page] (key scale, log2 weight scale, 1 / weight scale, value of a weight unit)
         chunk = o; o += (uint32_t)nv * kMaxSlots * 16u;
@@ -251,21 +263,44 @@ __device__ __forceinline__ void segment_role(const AttnArgs &a, unsigned char *s
     }
 }
 
-template <int D>
+// Warp w's part (of nw) of segment s's queries, once the segment is there and its buffers are
+// free (`must`: waits for that).  False if they are not.
+template <int D, int COPIES>
+__device__ __forceinline__ bool segment_queries(const AttnArgs &a, unsigned char *smem, const CommonSmem &L, const Bars &B,
+                                                int s, int w, int nw, bool must, int *abort_flag) {
+    uint64_t *full = B.seg_full(s % kSegs), *empty = B.q_empty(s & 1);
+    const uint32_t pf = (uint32_t)(s / kSegs) & 1u, pe = ((uint32_t)(s >> 1) & 1u) ^ 1u;
+    if (must) {
+        if (!warp_wait(full, pf, 0xe20u, abort_flag) || !warp_wait(empty, pe, 0xe00u, abort_flag)) return false;
+    } else if (!__all_sync(0xffffffffu, mbar_test(full, pf) && mbar_test(empty, pe))) {
+        return false;
+    }
+    const Seg &g = reinterpret_cast<const Seg *>(smem + L.seg)[s % kSegs];
+    if (g.count > 0)
+        load_queries<D, kRows, 4, COPIES>(a, reinterpret_cast<RowInfo *>(smem + L.rows) + (s & 1) * kRows,
+                                          smem + L.q + (uint32_t)(s & 1) * (2u * kRows * D), g, w, nw);
+    if ((threadIdx.x & 31) == 0) mbar_arrive(B.q_full(s & 1));
+    return true;
+}
+
+template <int D, int COPIES>
 __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __grid_constant__ CUtensorMap tm,
                                                                          const AttnArgs a) {
     constexpr uint32_t kTile = kTokens * D;
     constexpr uint32_t kSwz = D == 128 ? kSwizzle128B : kSwizzle64B;
     constexpr uint32_t kGroup8 = 8 * D;
+    // score and output buffers: what TMEM's 512 columns hold
+    constexpr int kSBufs = D == 128 && COPIES > 1 ? 2 : 3, kOBufs = D == 128 && COPIES == 1 ? 1 : 2;
+    static_assert(kSBufs * kTokens + kOBufs * D <= 512 && kSBufs + kOBufs <= kRing, "buffers");
     extern __shared__ __align__(1024) unsigned char smem_raw[];
     unsigned char *smem = (unsigned char *)(((uintptr_t)smem_raw + 1023) & ~(uintptr_t)1023);
-    const RowsSmem F(D, a.nk, a.nv);
+    const RowsSmem F(D, a.nk, a.nv, COPIES);
     const CommonSmem &L = F.c;
     const Bars B{reinterpret_cast<uint64_t *>(smem + L.bars)};
     uint32_t *misc = reinterpret_cast<uint32_t *>(smem + L.misc);
     uint32_t *tmem_slot = misc;
     int *abort_flag = reinterpret_cast<int *>(misc + 1);
-    int *n_shared = reinterpret_cast<int *>(misc + 2);
+    int *n_shared = reinterpret_cast<int *>(misc + 2), *go = reinterpret_cast<int *>(misc + 3);
     int64_t *sums = reinterpret_cast<int64_t *>(misc + 8);
     Start *start = reinterpret_cast<Start *>(misc + 64);
     StatusWord *st = a.k.st;
@@ -284,15 +319,17 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             mbar_init(B.c_full(s), 1);
         }
         for (int b = 0; b < 2; b++) {
-            mbar_init(B.q_full(b), 4);
+            mbar_init(B.q_full(b), COPIES == 1 ? 4 : 4 * kGroups);  // the warps that load queries
             mbar_init(B.q_empty(b), kSoft / 32);
         }
         for (int b = 0; b < kSBufs; b++) {
             mbar_init(B.s_full(b), 1);
             mbar_init(B.p_ready(b), 4);
         }
-        mbar_init(B.o_full(0), 1);
-        mbar_init(B.o_empty(0), 4);
+        for (int b = 0; b < kOBufs; b++) {
+            mbar_init(B.o_full(b), 1);
+            mbar_init(B.o_empty(b), 4);
+        }
         for (int b = 0; b < kSegs; b++) {
             mbar_init(B.seg_full(b), 1);
             mbar_init(B.seg_empty(b), 2 + kSoft / 32);  // the copying warps, and the softmax
@@ -323,16 +360,16 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
             const uint64_t qd = smem_desc(smem_u32(smem + L.q), 16, kGroup8, kSwz);
             int ks = 0, vs = 0;  // stages
             int ns = 0, np = 0, seg = 0, seg_end = 0, qb = 0;  // scores / outputs issued
-            int bs = 0, bp = 0;                                // and their buffers
+            int bs = 0, bp = 0, bo = 0;                        // and their buffers
             bool last = false;                                 // seg_end is the share's end
             const uint32_t elected = elect_one();
             // Whichever is ready: the outputs of tile np, the scores of tile ns (over the weights of
-            // tile ns - 3, whose outputs have been issued; with the segment's queries).  Lanes 0 to 4
+            // tile ns - kSBufs, whose outputs have been issued; with the segment's queries).  Lanes 0 to 4
             // look at one barrier each; a vote makes the outcome uniform, which keeps the descriptors
             // in uniform registers.
             Watch eye = lane == 0   ? Watch{B.p_ready(0), kSBufs, 0, 0u}
                         : lane == 1 ? Watch{B.v_full(0), a.nv, 0, 0u}
-                        : lane == 2 ? Watch{B.o_empty(0), 1, 0, 1u}
+                        : lane == 2 ? Watch{B.o_empty(0), kOBufs, 0, 1u}
                         : lane == 3 ? Watch{B.k_full(0), a.nk, 0, 0u}
                                     : Watch{B.q_full(0), 2, 0, 0u};
             uint64_t idle = 0;  // since when nothing has been ready
@@ -363,12 +400,13 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                     for (int part = 0; part < 2; part++)
     #pragma unroll
                         for (int k = 0; k < kTokens / 32; k++)
-                            tc_mma_f8_ts(tmem_o, p + (uint32_t)(16 * k + 8 * part),
+                            tc_mma_f8_ts(tmem_o + (uint32_t)(bo * D), p + (uint32_t)(16 * k + 8 * part),
                                          va + (uint64_t)(k * (32 * D) >> 4), id_o, (part > 0 || k > 0) ? 1u : 0u, elected);
                     tc_commit_elected(B.v_empty(vs), elected);
-                    tc_commit_elected(B.o_full(0), elected);
+                    tc_commit_elected(B.o_full(bo), elected);
                     if (++vs == a.nv) vs = 0;
                     if (++bp == kSBufs) bp = 0;
+                    if (++bo == kOBufs) bo = 0;
                     np++;
                     if (lane < 3) eye.next();
                 }
@@ -407,21 +445,29 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         float *fac = reinterpret_cast<float *>(smem + F.fac);
         uint32_t *nan = reinterpret_cast<uint32_t *>(smem + F.nan);
         const int page_shift = 31 - __clz(a.k.kv.page);
+        // the tokens of a tile that this warp's copy of the rows takes
+        constexpr int kTake = kTokens / COPIES, kWide = kTake < 64 ? kTake : 64;
+        const int h0 = ew * COPIES / 4 * kTake;
         int done = 0;  // tiles of earlier segments
 
 #pragma unroll 1
-        for (int seg = 0;; seg++) {
+        for (int seg = COPIES == 1 ? 0 : -1;; seg++) {  // (-1: only the first segment's queries)
             const int buf = seg & 1;
             // (no barrier stands between these warps: after an abort each leaves by itself)
-            if (!warp_wait(B.q_full(buf), (uint32_t)(seg >> 1) & 1u, 0xc31u, abort_flag)) break;
-            const Seg *sg = reinterpret_cast<const Seg *>(smem + L.seg) + seg % kSegs;
+            if (seg >= 0 && !warp_wait(B.q_full(buf), (uint32_t)(seg >> 1) & 1u, 0xc31u, abort_flag)) break;
+            const Seg *sg = reinterpret_cast<const Seg *>(smem + L.seg) + (seg & (kSegs - 1));
             const RowInfo ri = reinterpret_cast<const RowInfo *>(smem + L.rows)[buf * kRows + row];
-            const int count = sg->count, tile0 = sg->tile0, see_all = sg->see_all, see_max = sg->see_max;
-            if (count == 0) break;
+            const int count = seg < 0 ? 0 : sg->count, tile0 = sg->tile0, see_all = sg->see_all, see_max = sg->see_max;
+            if (seg >= 0 && count == 0) break;
+            bool asked = COPIES == 1;  // the next segment's queries are loaded
 
             // scores of tile t of the segment -> weights; its reference and sum
 #pragma unroll 1
-            for (int t = (wg + kGroups - done % kGroups) % kGroups; t < count; t += kGroups) {
+            for (int t = (wg + kGroups - done % kGroups) % kGroups;; t += kGroups) {
+                // (with several copies these warps have the time, the joining ones do not)
+                if (!asked)
+                    asked = segment_queries<D, COPIES>(a, smem, L, B, seg + 1, sw, 4 * kGroups, t >= count, abort_flag);
+                if (t >= count) break;
                 const int u = done + t, sb = u % kSBufs, vb = u % a.nv;
                 const float4 *chunk = reinterpret_cast<const float4 *>(smem + F.chunk) + vb * kMaxSlots;
                 soft_wait(B.c_full(vb), (uint32_t)(u / a.nv) & 1u, 0xc11u, abort_flag);
@@ -436,28 +482,28 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                     fence_proxy_async_smem();
                 }
                 soft_wait(B.s_full(sb), (uint32_t)(u / kSBufs) & 1u, 0xc00u + sb, abort_flag);
-                // (from here on: these scores are there, so the outputs of tile u - 3 have been issued,
-                // so those of tile u - 4, whose places these are, have been joined)
+                // (from here on: these scores are there, so the outputs of tile u - kSBufs have been
+                // issued, so those of tile u - kSBufs - kOBufs have been joined: kRing places do)
                 if (lane == 0) {
-                    fac[u & 3] = chunk[0].w;
-                    nan[(u & 3) * 4 + ew] = word;
+                    fac[u % kRing] = chunk[0].w;
+                    nan[(u % kRing) * 4 + ew] = word;
                 }
                 tc_fence_after();
                 const uint32_t ts = tmem + (uint32_t)(sb * kTokens) + lanes;
                 // loops over 32 tokens are not unrolled: the body must stay in the instruction cache
                 float mx = -INFINITY;
 #pragma unroll 1
-                for (int h = 0; h < kTokens; h += 64) {
-                    float x[64];
+                for (int h = h0; h < h0 + kTake; h += kWide) {
+                    float x[kWide];
                     tmem_ld32(ts + h, x);
-                    tmem_ld32(ts + h + 32, x + 32);
+                    if constexpr (kWide == 64) tmem_ld32(ts + h + 32, x + 32);
                     tmem_ld_wait(x);
                     if (special) {
 #pragma unroll
-                        for (int i = 0; i < 64; i++) x[i] = h + i < lim ? x[i] : -INFINITY;
+                        for (int i = 0; i < kWide; i++) x[i] = h + i < lim ? x[i] : -INFINITY;
                     }
 #pragma unroll
-                    for (int q = 0; q < 4; q++) {
+                    for (int q = 0; q < kWide / 16; q++) {
                         float m4[4];
 #pragma unroll
                         for (int i = 0; i < 4; i++)
@@ -470,7 +516,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                 const float mt = mx * ri.qs, base = mt == -INFINITY ? 0.f : mt;
                 float l = 0.f;
 #pragma unroll 1
-                for (int h = 0; h < kTokens; h += 32) {
+                for (int h = h0; h < h0 + kTake; h += 32) {
                     float x[32];
                     tmem_ld32(ts + h, x);
                     uint64_t A2[2], C2[2];
@@ -516,13 +562,23 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                     }
                     tmem_st16(ts + (h >> 1), w);  // over scores that have been read
                 }
+                if constexpr (COPIES > 1) {  // the other copies' tokens have no weight in this one
+                    uint32_t w[16];
+#pragma unroll
+                    for (int i = 0; i < 16; i++) w[i] = 0u;
+#pragma unroll
+                    for (int i = 1; i < COPIES; i++)
+#pragma unroll
+                        for (int h = 0; h < kTake; h += 32) tmem_st16(ts + (((h0 + i * kTake + h) & (kTokens - 1)) >> 1), w);
+                }
                 tmem_st_wait();
-                ml[(u & 3) * kRows + row] = make_float2(mt, l);
+                ml[(u % kRing) * kRows + row] = make_float2(mt, l);
                 tc_fence_before();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(B.p_ready(sb));
             }
 
+            if (seg < 0) continue;
             done += count;
             if (lane == 0) {
                 mbar_arrive(B.q_empty(buf));
@@ -540,43 +596,41 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         const size_t slot_floats = (size_t)a.rpt * D + 2 * a.rpt;
         float o[D];
         int u = 0, shared = 0;  // tiles joined; units shared with other CTAs
-        // segment s's queries, 32 rows in each of these warps: loaded at the start of segment s - 1,
-        // whose first output is still far
-        auto queries = [&](int s) {
-            if (!warp_wait(B.seg_full(s % kSegs), (uint32_t)(s / kSegs) & 1u, 0xe20u, abort_flag) ||
-                !warp_wait(B.q_empty(s & 1), ((uint32_t)(s >> 1) & 1u) ^ 1u, 0xe00u, abort_flag))
-                return;
-            const Seg &g = reinterpret_cast<const Seg *>(smem + L.seg)[s % kSegs];
-            if (g.count > 0)
-                load_queries<D, kRows, 4>(a, reinterpret_cast<RowInfo *>(smem + L.rows) + (s & 1) * kRows,
-                                          smem + L.q + (uint32_t)(s & 1) * (2u * kRows * D), g, ew, 4);
-            if (lane == 0) mbar_arrive(B.q_full(s & 1));
-        };
-        queries(0);
+        // segment s's queries are loaded at the start of segment s - 1, whose first output is still far
+        if constexpr (COPIES == 1) segment_queries<D, COPIES>(a, smem, L, B, 0, ew, 4, true, abort_flag);
 
 #pragma unroll 1
         for (int seg = 0;; seg++) {
             const int buf = seg & 1;
-            if (!warp_wait(B.q_full(buf), (uint32_t)(seg >> 1) & 1u, 0xc32u, abort_flag)) break;
+            if constexpr (COPIES == 1) {
+                if (!warp_wait(B.q_full(buf), (uint32_t)(seg >> 1) & 1u, 0xc32u, abort_flag)) break;
+            } else {
+                // (one thread decides for all whether to go on, as barriers of the warpgroup follow)
+                if (row == 0) *go = lane_wait(B.q_full(buf), (uint32_t)(seg >> 1) & 1u, 0xc32u, abort_flag) ? 1 : 0;
+                named_barrier(kBarJoin, 128);
+                if (*(volatile int *)go == 0) break;
+                soft_wait(B.q_full(buf), (uint32_t)(seg >> 1) & 1u, 0xc34u, abort_flag);
+            }
             const Seg *sg = reinterpret_cast<const Seg *>(smem + L.seg) + seg % kSegs;
             const RowInfo ri = reinterpret_cast<const RowInfo *>(smem + L.rows)[buf * kRows + row];
             const int count = sg->count, tile0 = sg->tile0;
             if (count == 0) break;
-            queries(seg + 1);
+            if constexpr (COPIES == 1) segment_queries<D, COPIES>(a, smem, L, B, seg + 1, ew, 4, true, abort_flag);
             float m_run = -INFINITY, l_run = 0.f;
 #pragma unroll
             for (int i = 0; i < D; i++) o[i] = 0.f;
 #pragma unroll 1
             for (int t = 0; t < count; t++, u++) {
-                soft_wait(B.o_full(0), (uint32_t)u & 1u, 0xc20u, abort_flag);
+                const int ob = u % kOBufs;
+                soft_wait(B.o_full(ob), (uint32_t)(u / kOBufs) & 1u, 0xc20u, abort_flag);
                 tc_fence_after();
-                const float2 v = ml[(u & 3) * kRows];
-                const uint4 nm = *reinterpret_cast<const uint4 *>(nan + (u & 3) * 4);
+                const float2 v = ml[(u % kRing) * kRows];
+                const uint4 nm = *reinterpret_cast<const uint4 *>(nan + (u % kRing) * 4);
                 const float m = fmaxf(m_run, v.x);
                 const float f_old = m_run == -INFINITY ? 0.f : ex2(m_run - m), f_new = v.x == -INFINITY ? 0.f : ex2(v.x - m);
                 m_run = m;
                 l_run = fmaf(l_run, f_old, v.y * f_new);
-                const float g = f_new * fac[u & 3];
+                const float g = f_new * fac[u % kRing];
                 const uint64_t g2 = pack2(g, g);
                 if (__any_sync(0xffffffffu, f_old != 1.f)) {  // some row's maximum has moved
                     const uint64_t k2 = pack2(f_old, f_old);
@@ -586,12 +640,12 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
 #pragma unroll
                 for (int h = 0; h < D; h += 32) {
                     float y[32];
-                    tmem_ld32(tmem_o + (uint32_t)h + lanes, y);
+                    tmem_ld32(tmem_o + (uint32_t)(ob * D + h) + lanes, y);
                     tmem_ld_wait(y);
                     if (h + 32 == D) {
                         tc_fence_before();
                         __syncwarp();
-                        if (lane == 0) mbar_arrive(B.o_empty(0));
+                        if (lane == 0) mbar_arrive(B.o_empty(ob));
                     }
 #pragma unroll
                     for (int i = 0; i < 32; i += 2)
@@ -613,9 +667,56 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                 }
             }
 
+            if constexpr (COPIES > 1) {
+                // the copies' results: all to the same reference, then added up in the first one's
+                // warps, 32 values of the head at a time
+                constexpr int kSpan = kRows / COPIES, kFirst = 4 / COPIES;
+                float2 *mlc = reinterpret_cast<float2 *>(smem + F.mlc);
+                float4 *merge = reinterpret_cast<float4 *>(smem + F.merge) + lane * 9;
+                mlc[row] = make_float2(m_run, l_run);
+                named_barrier(kBarJoin, 128);
+                float2 v[COPIES];
+                float m = -INFINITY, l = 0.f;
+#pragma unroll
+                for (int i = 0; i < COPIES; i++) {
+                    v[i] = mlc[(row & (kSpan - 1)) + i * kSpan];
+                    m = fmaxf(m, v[i].x);
+                }
+#pragma unroll
+                for (int i = 0; i < COPIES; i++)
+                    l += v[i].y == 0.f ? 0.f : v[i].y * ex2(v[i].x - m);  // (sum 0: it saw nothing; NaN stays)
+                const float f = l_run == 0.f ? 0.f : ex2(m_run - m);
+                m_run = m;
+                l_run = l;
+                const uint64_t f2 = pack2(f, f);
+#pragma unroll
+                for (int i = 0; i < D; i += 2) unpack2(mul2(pack2(o[i], o[i + 1]), f2), o[i], o[i + 1]);
+#pragma unroll
+                for (int h = 0; h < D; h += 32) {
+                    if (ew >= kFirst) {
+#pragma unroll
+                        for (int i = 0; i < 32; i += 4)
+                            merge[(ew - kFirst) * (32 * 9) + i / 4] =
+                                make_float4(o[h + i], o[h + i + 1], o[h + i + 2], o[h + i + 3]);
+                    }
+                    named_barrier(kBarJoin, 128);
+                    if (ew < kFirst) {
+#pragma unroll 1
+                        for (int k = ew; k < 4 - kFirst; k += kFirst) {
+#pragma unroll
+                            for (int i = 0; i < 32; i += 4) {
+                                const float4 y = merge[k * (32 * 9) + i / 4];
+                                unpack2(add2(pack2(o[h + i], o[h + i + 1]), pack2(y.x, y.y)), o[h + i], o[h + i + 1]);
+                                unpack2(add2(pack2(o[h + i + 2], o[h + i + 3]), pack2(y.z, y.w)), o[h + i + 2], o[h + i + 3]);
+                            }
+                        }
+                    }
+                    if (h + 32 < D) named_barrier(kBarJoin, 128);
+                }
+            }
             float *part = count < sg->nt ? a.part + (size_t)(2 * (int)blockIdx.x + (tile0 == 0 ? 1 : 0)) * slot_floats
                                         : nullptr;
-            if (ri.row >= 0 && !*(volatile int *)abort_flag) {
+            if (ri.row >= 0 && ew * COPIES < 4 && !*(volatile int *)abort_flag) {
                 if (part != nullptr) {
                     float *d = part + (size_t)row * D;
 #pragma unroll
@@ -665,7 +766,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
     if (warp == 1) tmem_dealloc(tmem, 512);
 }
 
-template <int D>
+template <int D, int COPIES>
 cudaError_t launch(const CUtensorMap &tm, AttnArgs a, int sms, int smem_max, cudaStream_t st) {
     static PerDevice smem_set(0);
     a.over = 3;  // (2 to 5 measure alike)
@@ -678,12 +779,12 @@ cudaError_t launch(const CUtensorMap &tm, AttnArgs a, int sms, int smem_max, cud
             b.nk++;
         else
             break;
-        if (RowsSmem(D, b.nk, b.nv).total + 1024u > (uint32_t)smem_max) break;
+        if (RowsSmem(D, b.nk, b.nv, COPIES).total + 1024u > (uint32_t)smem_max) break;
         a = b;
     }
-    const size_t smem = RowsSmem(D, a.nk, a.nv).total + 1024;
+    const size_t smem = RowsSmem(D, a.nk, a.nv, COPIES).total + 1024;
     if (smem > (size_t)smem_max) return cudaErrorNotSupported;
-    cudaError_t e = ensure_dynamic_smem(kv_attention_rows_kernel<D>, smem, smem_set);
+    cudaError_t e = ensure_dynamic_smem(kv_attention_rows_kernel<D, COPIES>, smem, smem_set);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)sms);
@@ -695,7 +796,7 @@ cudaError_t launch(const CUtensorMap &tm, AttnArgs a, int sms, int smem_max, cud
     attr[0].val.cooperative = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kv_attention_rows_kernel<D>, tm, a);
+    return cudaLaunchKernelEx(&cfg, kv_attention_rows_kernel<D, COPIES>, tm, a);
 }
 
 }  // namespace
@@ -703,7 +804,13 @@ cudaError_t launch(const CUtensorMap &tm, AttnArgs a, int sms, int smem_max, cud
 cudaError_t set_wait_limit_kv_attention_rows(uint64_t ns) { return set_wait_limit_here(ns); }
 
 cudaError_t launch_attention_rows(const CUtensorMap &tm, AttnArgs a, int sms, int smem_max, cudaStream_t st) {
-    return a.k.kv.dim == 128 ? launch<128>(tm, a, sms, smem_max, st) : launch<64>(tm, a, sms, smem_max, st);
+    const int copies = a.rpt <= 32 ? 4 : a.rpt <= 64 ? 2 : 1;
+    if (a.k.kv.dim == 128) {
+        if (copies == 4) return launch<128, 4>(tm, a, sms, smem_max, st);
+        return copies == 2 ? launch<128, 2>(tm, a, sms, smem_max, st) : launch<128, 1>(tm, a, sms, smem_max, st);
+    }
+    if (copies == 4) return launch<64, 4>(tm, a, sms, smem_max, st);
+    return copies == 2 ? launch<64, 2>(tm, a, sms, smem_max, st) : launch<64, 1>(tm, a, sms, smem_max, st);
 }
 
 }  // namespace moe
