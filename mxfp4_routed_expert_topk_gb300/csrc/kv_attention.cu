@@ -25,9 +25,9 @@
 namespace moe {
 namespace {
 
-// Rows of a row tile.  (A form of 32 with two outputs' worth of registers took 165 us for 4 rows
-// in each of 24 sequences of 8192, where the rows form takes 144; with 16 or fewer the rows form
-// takes 138 us where this one takes 98.)
+// Rows of a row tile.  (This form with 32 took 165 us for 4 rows in each of 24 sequences of
+// 8192, where the rows form takes 117; with 16 or fewer the rows form takes 116 us where this one
+// takes 92.)
 constexpr int kRows = 16;
 // Workers of a CTA, a softmax warpgroup each.
 constexpr int kWorkers = 3;

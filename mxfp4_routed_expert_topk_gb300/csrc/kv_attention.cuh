@@ -115,9 +115,16 @@ struct Line {
     static __device__ __forceinline__ int64_t ratio(int64_t x, int64_t y) {
         return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
     }
-    __device__ __forceinline__ void set(int64_t total_, int max_workers) {
+    // No more workers than pay: k of them on a unit of L positions take its tiles in L / k steps
+    // but leave k parts to be joined one after the other, kJoin of which take a tile's time; L / k +
+    // k / kJoin is least at k = sqrt(kJoin L), so sqrt(kJoin units total) in all.  (One sequence of
+    // 100000 tokens, one head: 49 us, with every worker on it 133; 17 rows over 30000 38 and 66.
+    // kJoin = 2: 55 and 41; 10: 49 and 39.)
+    __device__ __forceinline__ void set(int64_t total_, int64_t units, int max_workers) {
+        constexpr float kJoin = 5.f;
         total = total_;
-        workers = (int)min((int64_t)max_workers, total);
+        const float pay = ceilf(__fsqrt_rn(kJoin * (float)units * (float)total));
+        workers = (int)min((int64_t)fminf(pay, (float)max_workers), total);
         share = workers > 0 ? ratio(total, workers) : 0;
         more = (int)(total - share * workers);
     }
@@ -190,7 +197,7 @@ __device__ __forceinline__ Line cut_line(const AttnArgs &a, int64_t *sums, Start
             total += sums[w];
         }
         pre -= mine;
-        l.set(total, (int)gridDim.x * NW);
+        l.set(total, (int64_t)items * a.k.kv.heads, (int)gridDim.x * NW);
         bool holds = false;
 #pragma unroll
         for (int w = 0; w < NW; w++) {
