@@ -8,7 +8,7 @@
 // its token (P^T is N-major); the maximum and sum of a row run across lanes.
 //
 // What bounds it is HBM for long sequences: one token for each of 64 sequences of up to 16384
-// (8 heads of 128, 7 query heads each) takes 197 us at 1119 MB, 5.7 TB/s (84 % of a copy's rate).
+// (8 heads of 128, 7 query heads each) takes 199 us at 1119 MB, 5.6 TB/s (83 % of a copy's rate).
 // A tile takes about 2800 clocks from its scores to its output (TMEM read, two cross-lane
 // reductions, a warpgroup barrier, the exponentials, the fences and the two MMA groups), twice
 // what its 32 KB take from HBM.  So a CTA has three workers, each a softmax warpgroup with a
@@ -16,7 +16,7 @@
 // them, and one's end of a unit overlaps with the others' tiles.  (Three warpgroups on one
 // share, joined at each unit's end: 256 sequences of 128 tokens 84 us, so 44, both from cold
 // caches.  Four such: 66 us in place of 62 for 96 sequences of 512.)  Short calls are bound by
-// the start (8 us: launch, shares, the first loads) and by code that runs once: fetching it from
+// the start (6 us: launch, shares, the first loads) and by code that runs once: fetching it from
 // cold caches takes 300 clocks per 8 instructions.
 #include <algorithm>
 
