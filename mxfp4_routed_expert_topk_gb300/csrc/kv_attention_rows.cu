@@ -769,7 +769,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
 template <int D, int COPIES>
 cudaError_t launch(const CUtensorMap &tm, AttnArgs a, int sms, int smem_max, cudaStream_t st) {
     static PerDevice smem_set(0);
-    a.over = 3;  // (2 to 5 measure alike)
+    // (adding up the copies makes a unit's fixed cost larger; 24 ragged sequences of up to 8192, 4 rows:
+    // 91 us with 3 tiles for it, 87 with 4, 80 with 6; one copy: 80, 81 and 84 for 48 x 9 rows, heads of 64)
+    a.over = COPIES == 1 ? 3 : COPIES == 2 ? 4 : 6;
     a.nk = a.nv = 2;
     while (true) {  // as many stages as fit, values first
         AttnArgs b = a;
