@@ -45,7 +45,7 @@ struct FewSmem {
         scales = o; o += (uint32_t)kWorkers * kStages * 2u * kMaxSlots * 4u;        // [worker][stage][keys', values']
         rows = o;   o += (uint32_t)kWorkers * 2u * kRows * (uint32_t)sizeof(RowInfo);  // [worker][buffer]
         smax = o;   o += (uint32_t)kWorkers * 2u * 4u * kRows * 4u;                 // [worker][2][warp][row]
-        ref = o;    o += (uint32_t)kWorkers * 4u * kRows * 8u;                      // [warp][row] (query scale, reference)
+        ref = o;    o += (uint32_t)kWorkers * 4u * 2u * kRows * 4u;                 // [warp][query scales, references][row]
         ab = o;     o += (uint32_t)kWorkers * 4u * kRows * 8u;                      // [warp][row] (factors of the outputs)
         lsum = o;   o += (uint32_t)kWorkers * 4u * kRows * 4u;                      // [warp][row]
         nan = o;    o += (uint32_t)kWorkers * 2u * 4u * 4u;                         // [worker][2][warp] tokens with NaN values
@@ -322,7 +322,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_few_kernel(const __g
         const uint32_t lanes = (uint32_t)(32 * ew) << 16;
         const int row = lane >> 1;                      // the row whose maximum and sum this lane holds
         float *smax = reinterpret_cast<float *>(smem + F.smax) + wg * 8 * R;
-        float2 *ref = reinterpret_cast<float2 *>(smem + F.ref) + sw * R;
+        float *qscale = reinterpret_cast<float *>(smem + F.ref) + sw * 2 * R, *ref = qscale + R;
         float2 *ab = reinterpret_cast<float2 *>(smem + F.ab) + sw * R;
         float *lsum = reinterpret_cast<float *>(smem + F.lsum) + wg * 4 * R;
         uint32_t *nan = reinterpret_cast<uint32_t *>(smem + F.nan) + wg * 8;
@@ -346,7 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_few_kernel(const __g
             const RowInfo *rows = reinterpret_cast<const RowInfo *>(smem + F.rows) + (2 * wg + (seg & 1)) * R;
             const int count = sg->count, tile0 = sg->tile0, see_all = sg->see_all, see_max = sg->see_max;
             if (count == 0) break;
-            const float qs = rows[row].qs;
+            qscale[row] = rows[row].qs;
+            __syncwarp();
             float m_run = -INFINITY, l_run = 0.f;
 #pragma unroll
             for (int i = 0; i < R; i++) o[i] = 0.f;
@@ -398,16 +399,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_few_kernel(const __g
                 soft_wait(B.v_full(stage), (uint32_t)(mine / kStages) & 1u, 0xc10u, abort_flag);
                 const float *sc = reinterpret_cast<const float *>(smem + F.scales) + (wg * kStages + stage) * 2 * kMaxSlots;
                 const float ks = sc[tok >> page_shift] * a.scale2;
-                // value scales relative to the tile's largest (finite) one
-                float vone = 0.f;
-                for (int j = 0; j < (kTokens >> page_shift); j++) {
-                    const float v = sc[kMaxSlots + j];
-                    vone = v < INFINITY ? fmaxf(vone, v) : vone;
-                }
-                vone = vone > 0.f ? vone : 1.f;
-                const float vs = sc[kMaxSlots + (tok >> page_shift)];
-                float c = vs < INFINITY ? 256.f * __fdividef(vs, vone) : kNan;
-                if (tk >= see_max) c = 0.f;
+                const float sv = sc[kMaxSlots + (tok >> page_shift)];
+                const float vs = fabsf(sv) < INFINITY ? sv : kNan;
+                const float lv = fmaxf(lg2(fabsf(vs)), kLowScale);  // (NaN: the output is NaN at any reference)
                 const bool special = (tile0 + t + 1) * kTokens > see_all;
                 tmem_ld_wait(x);
                 tmem_ld_wait(x2);
@@ -426,16 +420,19 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_few_kernel(const __g
                 float *mx = smax + (mine & 1) * 4 * R;
 #pragma unroll
                 for (int i = 0; i < R; i += 4) {
-                    const float4 v = make_float4(warp_max(x[i]), warp_max(x[i + 1]), warp_max(x[i + 2]), warp_max(x[i + 3]));
+                    const float4 k = *reinterpret_cast<const float4 *>(qscale + i);
+                    const float4 v = make_float4(warp_max(fmaf(x[i], k.x, lv)), warp_max(fmaf(x[i + 1], k.y, lv)),
+                                                 warp_max(fmaf(x[i + 2], k.z, lv)), warp_max(fmaf(x[i + 3], k.w, lv)));
                     if (lane == 0) *reinterpret_cast<float4 *>(mx + ew * R + i) = v;
                 }
                 named_barrier(bar, 128);
-                const float mt = fmaxf(fmaxf(mx[row], mx[R + row]), fmaxf(mx[2 * R + row], mx[3 * R + row])) * qs;
+                const float mt = fmaxf(fmaxf(mx[row], mx[R + row]), fmaxf(mx[2 * R + row], mx[3 * R + row])) - kTop;
                 const float m = fmaxf(m_run, mt);
-                const float f_old = m_run == -INFINITY ? 0.f : ex2(m_run - m), f_new = mt == -INFINITY ? 0.f : ex2(mt - m);
+                const float f_old = m_run == -INFINITY ? 0.f : ex2_low(m_run - m),
+                            f_new = mt == -INFINITY ? 0.f : ex2_low(mt - m);
                 m_run = m;
-                ref[row] = make_float2(qs, mt == -INFINITY ? 0.f : mt);
-                ab[row] = make_float2(f_old, f_new * (vone * (1.f / 256.f)));
+                ref[row] = mt == -INFINITY ? 0.f : mt;
+                ab[row] = make_float2(f_old, f_new);
                 __syncwarp();
                 uint8_t *pw = smem + F.p + (uint32_t)wg * (2u * kPBytes) + (uint32_t)tok * 16u;
                 float p[R];
@@ -443,12 +440,14 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_few_kernel(const __g
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     float h[4], l[4];
+                    const float4 q4 = *reinterpret_cast<const float4 *>(qscale + 4 * j);
+                    const float4 r4 = *reinterpret_cast<const float4 *>(ref + 4 * j);
+                    const float qk[4] = {q4.x, q4.y, q4.z, q4.w}, rk[4] = {r4.x, r4.y, r4.z, r4.w};
 #pragma unroll
                     for (int k = 0; k < 4; k++) {
                         const int r = 4 * j + k;
-                        const float2 rq = ref[r];
-                        p[r] = ex2(fmaf(x[r], rq.x, -rq.y));
-                        float w = p[r] * c;
+                        p[r] = ex2(fmaf(x[r], qk[k], -rk[k]));
+                        float w = p[r] * vs;
                         if (special) w = x[r] == -INFINITY ? 0.f : w;
                         h[k] = part_hi(w);
                         l[k] = w - h[k];

@@ -11,11 +11,13 @@
 //     exactly the sum of two E4M3 parts (4 + 4 significant bits) after a power of two per
 //     row, and a weight is written as two parts as well (8 bits, as bf16 has).  Each product
 //     runs twice into the same accumulator; the tensor pipe has room for it.
-//   - Weights are taken relative to their 128-token tile's own maximum, and each tile's output
-//     is a fresh accumulator joined with the running one in registers: what E4M3's range
-//     cannot hold is then below 2^-17 of the tile's largest term, however far another token
-//     stands above the tile.  The pages' value scales, relative to the tile's largest,
-//     multiply the weights before they are split.
+//   - A weight carries its page's value scale into the tensor cores: w = 2^(s - ref) vs.  ref is a
+//     row's own, over the tokens that it sees of the 128-token tile: max(s + log2 vs) - 8, so that
+//     its largest w is 256, and what E4M3's range cannot hold is below 2^-17 of that, whatever
+//     scales other tokens of the tile have.  (One reference for the scales of the whole tile lost
+//     the weights on pages with scales far below the tile's largest.)  The sums of 2^(s - ref)
+//     go by the same reference; so that they stay in range, a scale below 2^-90 counts as 2^-90 in
+//     it.  Each tile's output is a fresh accumulator joined with the running one in registers.
 //   - Work: the (sequence, row tile, head, 128-token tile) units of the call in one line, cut
 //     into equal shares, one per worker (one or three of an SM).  A share may begin and end
 //     inside a sequence: such partial results go to the workspace and, after a grid barrier
@@ -41,6 +43,8 @@ constexpr int kStKvArrive = 40, kStKvExit = 5;  // StatusWord::pad
 constexpr int kFirstSoft = 4;            // first softmax warp
 constexpr float kLn2 = 0.6931471805599453f;
 constexpr float kNan = __builtin_nanf("");
+constexpr float kLowScale = -90.f;       // log2 of the smallest value scale in a reference
+constexpr float kTop = 8.f;              // log2 of a tile's largest weight
 
 }  // namespace
 
@@ -311,6 +315,14 @@ __device__ __forceinline__ float ex2(float x) {
     return y;
 }
 
+// The same with results down to 2^-149: references differ by value scales, too, and a sum far
+// below another reference may be the larger one.
+__device__ __forceinline__ float ex2_low(float x) {
+    float y;
+    asm("ex2.approx.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
 // 4 bytes global -> shared, asynchronously; zero without reading if !ok.
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void *src, bool ok) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4, %2;" ::"r"(dst), "l"(src), "r"(ok ? 4 : 0) : "memory");
@@ -378,8 +390,8 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity, unsign
 // waits, and the code runs on to its end.
 __device__ __forceinline__ void soft_wait(uint64_t *bar, uint32_t parity, unsigned where, int *abort_flag) {
     uint64_t t0 = 0;
-    while (!mbar_try_wait(bar, parity))
-        if (expired(t0, where, abort_flag)) break;
+    for (int n = 1; !mbar_try_wait(bar, parity); n++)  // (the timer costs issue slots: not each time)
+        if ((n & 15) == 0 && expired(t0, where, abort_flag)) break;
     __syncwarp();
 }
 
@@ -779,7 +791,7 @@ __device__ __forceinline__ void join_role(const AttnArgs &a, const Line &line, i
             for (int p = lane + 32; p < parts_; p += 32) m = fmaxf(m, __ldcg(slot_of(p) + (size_t)a.rpt * D + 2 * r));
 #pragma unroll
             for (int d = 16; d > 0; d >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, d));
-            const float mine = ml.y == 0.f ? 0.f : ex2(ml.x - m);  // (sum 0: it saw nothing; NaN stays)
+            const float mine = ml.y == 0.f ? 0.f : ex2_low(ml.x - m);  // (sum 0: it saw nothing; NaN stays)
 #pragma unroll 1
             for (int p = 0; p < parts_; p += U) {
 #pragma unroll
@@ -791,7 +803,7 @@ __device__ __forceinline__ void join_role(const AttnArgs &a, const Line &line, i
                         s = __shfl_sync(0xffffffffu, ml.y, p + i);
                     } else {
                         const float2 t = __ldcg(reinterpret_cast<const float2 *>(slot_of(p + i) + (size_t)a.rpt * D + 2 * r));
-                        f = t.y == 0.f ? 0.f : ex2(t.x - m);
+                        f = t.y == 0.f ? 0.f : ex2_low(t.x - m);
                         s = t.y;
                     }
                     l = fmaf(s, f, l);

@@ -6,7 +6,11 @@
 // N-major).  The TMEM lane of a score is its row, so a row's maximum and sum need no exchange
 // between lanes and its reference is one register; the pages' key scales and the logarithm of
 // their value scales are constants of a run of 16 tokens and go into the exponent's multiply-
-// add.  Weights replace the scores they came from in TMEM.
+// add, so that the exponential is the weight with its value scale; a run's sum times 2^-(that
+// logarithm) is what it adds to the row's sum.  Where that logarithm is so far below the row's
+// others that the exponential would leave fp32's range while the sum needs it, both take a larger
+// one (the weight, below E4M3's range, becomes 0 all the same).  Weights replace the scores they
+// came from in TMEM.
 //
 // What bounds it is instruction issue and latency: 128 x 128 scores a tile at 7 to 8
 // instructions each are about 1000 clocks of all four schedulers, next to 1400 that the tile's
@@ -147,22 +151,28 @@ __device__ __forceinline__ void copy_role(const AttnArgs &a, const CUtensorMap *
 
 struct RowsSmem {
     CommonSmem c;
-    uint32_t ml, fac, chunk, nan, merge = 0, mlc = 0, total;
+    uint32_t ml, chunk, nan, merge = 0, mlc = 0, total;
     __host__ __device__ RowsSmem(int dim, int nk, int nv, int copies) : c(dim, kRows, nk, nv) {
         uint32_t o = (c.total + 127u) & ~127u;
         ml = o;    o += (uint32_t)kRing * kRows * 8u;  // [tile][row] (reference, sum)
-        fac = o;   o += (uint32_t)kRing * 4u;    // [tile] value of a weight unit
         nan = o;   o += (uint32_t)kRing * 4u * 4u;  // [tile][warp] tokens whose values hold partial NaN
         if (copies > 1) {
             merge = o; o += 3u * 32u * 36u * 4u; // [warp of the copies but the first][lane][32 + 4] values of the head
             mlc = o;   o += kRows * 8u;          // [place] (reference, sum)
         }
         o = (o + 15u) & ~15u;
-        // [value stage][page] (key scale, log2 weight scale, 1 / weight scale, value of a weight unit)
+        // [value stage][page] (key scale, log2 of the value scale as references take it and as it is, its inverse)
         chunk = o; o += (uint32_t)nv * kMaxSlots * 16u;
         total = o;
     }
 };
+
+// The larger of two values; NaN if either is.
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
 
 __device__ __forceinline__ uint64_t pack2(float a, float b) {
     uint64_t r;
@@ -229,16 +239,13 @@ __device__ __forceinline__ void segment_role(const AttnArgs &a, unsigned char *s
             const int vb = u % a.nv;
             const float *sc = scales + vb * 2 * kMaxSlots;
             __syncwarp();  // (lane 1 has seen the copies land)
-            const float ks = sc[lane & 7] * a.scale2, vs = lane < slots ? sc[kMaxSlots + lane] : 0.f;
-            const bool fin = vs < INFINITY;
-            float vone = fin ? vs : 0.f;
-#pragma unroll
-            for (int d = 4; d > 0; d >>= 1) vone = fmaxf(vone, __shfl_xor_sync(0xffffffffu, vone, d));
-            vone = vone > 0.f ? vone : 1.f;
-            const float c = fmaxf(256.f * __fdividef(vs, vone), 8.67361738e-19f);  // at least 2^-60
-            if (lane < kMaxSlots)
-                chunk[vb * kMaxSlots + lane] =
-                    make_float4(ks, fin ? lg2(c) : kNan, fin ? __fdividef(1.f, c) : 1.f, vone * (1.f / 256.f));
+            // (a loop of one turn: as straight code the compiler copies this into the polling loop, and
+            // all roles feel it: 4 x 17 rows 354 us, so 323)
+#pragma unroll 1
+            for (int j = lane; j < slots; j += 32) {
+                const float vs = sc[kMaxSlots + j], v = fabsf(vs) < INFINITY ? lg2(vs) : kNan;
+                chunk[vb * kMaxSlots + j] = make_float4(sc[j] * a.scale2, fmaxf(v, kLowScale), v, ex2(-v));
+            }
             __syncwarp();
             if (lane == 0) mbar_arrive(B.c_full(vb));
             u++;
@@ -442,7 +449,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         const int row = 32 * ew + lane;  // row of the tile (TMEM lane); also the token it cleans
         const uint32_t lanes = (uint32_t)(32 * ew) << 16;
         float2 *ml = reinterpret_cast<float2 *>(smem + F.ml);
-        float *fac = reinterpret_cast<float *>(smem + F.fac);
         uint32_t *nan = reinterpret_cast<uint32_t *>(smem + F.nan);
         const int page_shift = 31 - __clz(a.k.kv.page);
         // the tokens of a tile that this warp's copy of the rows takes
@@ -484,14 +490,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                 soft_wait(B.s_full(sb), (uint32_t)(u / kSBufs) & 1u, 0xc00u + sb, abort_flag);
                 // (from here on: these scores are there, so the outputs of tile u - kSBufs have been
                 // issued, so those of tile u - kSBufs - kOBufs have been joined: kRing places do)
-                if (lane == 0) {
-                    fac[u % kRing] = chunk[0].w;
-                    nan[(u % kRing) * 4 + ew] = word;
-                }
+                if (lane == 0) nan[(u % kRing) * 4 + ew] = word;
                 tc_fence_after();
                 const uint32_t ts = tmem + (uint32_t)(sb * kTokens) + lanes;
                 // loops over 32 tokens are not unrolled: the body must stay in the instruction cache
-                float mx = -INFINITY;
+                float mx = -INFINITY, mv = -INFINITY;  // largest score; and with its value scale
 #pragma unroll 1
                 for (int h = h0; h < h0 + kTake; h += kWide) {
                     float x[kWide];
@@ -509,11 +512,15 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                         for (int i = 0; i < 4; i++)
                             m4[i] = fmaxf(fmaxf(x[16 * q + i], x[16 * q + 4 + i]),
                                           fmaxf(x[16 * q + 8 + i], x[16 * q + 12 + i]));
-                        mx = fmaxf(mx, fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) *
-                                           chunk[(h + 16 * q) >> page_shift].x);
+                        const float2 c = *reinterpret_cast<const float2 *>(chunk + ((h + 16 * q) >> page_shift));
+                        const float s = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * c.x;
+                        mx = fmaxf(mx, s);
+                        mv = fmaxf(mv, fmaf(s, ri.qs, c.y));
                     }
                 }
-                const float mt = mx * ri.qs, base = mt == -INFINITY ? 0.f : mt;
+                const float mt = mv - kTop, base = mt == -INFINITY ? 0.f : mt;
+                // a value scale's logarithm counts as `low` at least: weights on it are below 2^(kTop - 30)
+                const float low = mt == -INFINITY ? 0.f : fmaf(-mx, ri.qs, mv) - 30.f, inv_low = ex2(-low);
                 float l = 0.f;
 #pragma unroll 1
                 for (int h = h0; h < h0 + kTake; h += 32) {
@@ -524,10 +531,10 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
 #pragma unroll
                     for (int q = 0; q < 2; q++) {
                         const float4 c = chunk[(h + 16 * q) >> page_shift];
-                        const float A = c.x * ri.qs, C = c.y - base;
+                        const float A = c.x * ri.qs, C = max_nan(c.z, low) - base;
                         A2[q] = pack2(A, A);
                         C2[q] = pack2(C, C);
-                        r[q] = c.z;
+                        r[q] = fminf(c.w, inv_low);
                     }
                     tmem_ld_wait(x);
 #pragma unroll
@@ -591,7 +598,6 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
         const int ew = warp & 3, row = 32 * ew + lane;
         const uint32_t lanes = (uint32_t)(32 * ew) << 16;
         const float2 *ml = reinterpret_cast<const float2 *>(smem + F.ml) + row;
-        const float *fac = reinterpret_cast<const float *>(smem + F.fac);
         const uint32_t *nan = reinterpret_cast<const uint32_t *>(smem + F.nan);
         const size_t slot_floats = (size_t)a.rpt * D + 2 * a.rpt;
         float o[D];
@@ -627,11 +633,11 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                 const float2 v = ml[(u % kRing) * kRows];
                 const uint4 nm = *reinterpret_cast<const uint4 *>(nan + (u % kRing) * 4);
                 const float m = fmaxf(m_run, v.x);
-                const float f_old = m_run == -INFINITY ? 0.f : ex2(m_run - m), f_new = v.x == -INFINITY ? 0.f : ex2(v.x - m);
+                const float f_old = m_run == -INFINITY ? 0.f : ex2_low(m_run - m),
+                            f_new = v.x == -INFINITY ? 0.f : ex2_low(v.x - m);
                 m_run = m;
                 l_run = fmaf(l_run, f_old, v.y * f_new);
-                const float g = f_new * fac[u % kRing];
-                const uint64_t g2 = pack2(g, g);
+                const uint64_t g2 = pack2(f_new, f_new);
                 if (__any_sync(0xffffffffu, f_old != 1.f)) {  // some row's maximum has moved
                     const uint64_t k2 = pack2(f_old, f_old);
 #pragma unroll
@@ -684,8 +690,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                 }
 #pragma unroll
                 for (int i = 0; i < COPIES; i++)
-                    l += v[i].y == 0.f ? 0.f : v[i].y * ex2(v[i].x - m);  // (sum 0: it saw nothing; NaN stays)
-                const float f = l_run == 0.f ? 0.f : ex2(m_run - m);
+                    l += v[i].y == 0.f ? 0.f : v[i].y * ex2_low(v[i].x - m);  // (sum 0: it saw nothing; NaN stays)
+                const float f = l_run == 0.f ? 0.f : ex2_low(m_run - m);
                 m_run = m;
                 l_run = l;
                 const uint64_t f2 = pack2(f, f);
