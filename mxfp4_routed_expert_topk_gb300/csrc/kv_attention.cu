@@ -551,8 +551,10 @@ cudaError_t kv_attention_workspace_bytes(const KvView &kv, int max_rows, int hea
     int sms = 0;
     const cudaError_t e = device_attr(cudaDevAttrMultiProcessorCount, g_sms, &sms);
     if (e != cudaSuccess) return e;
-    // two slots per worker, the larger need of the two forms (so a size serves fewer rows too)
-    const size_t rows = (size_t)std::max(rows_per_tile(max_rows, heads_q / kv.heads), kWorkers * kRows);
+    // two slots per worker, the larger need of the two forms; a size serves fewer rows too, whose
+    // tiles may be larger (17 x 8 rows are two tiles of 80, 16 x 8 are one of 128)
+    const int group = heads_q / kv.heads;
+    const size_t rows = std::max(max_rows * group > 128 ? 128 : rows_per_tile(max_rows, group), kWorkers * kRows);
     *bytes = sizeof(StatusWord) + (size_t)2 * sms * rows * (kv.dim + 2) * sizeof(float);
     return cudaSuccess;
 }

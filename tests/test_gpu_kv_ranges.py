@@ -158,3 +158,26 @@ def test_value_scales_alike_at_the_ends(group, e):
     c = Case([5], [300], 2, group, 64, 16, seed=group)
     spread_values(c, (e,), np.random.default_rng(0))
     check(c)
+
+
+# ------------------------------------------------------------- workspaces
+
+
+@pytest.mark.parametrize("heads,group", [(2, 1), (1, 7), (2, 8), (1, 16), (1, 20), (1, 136)])
+def test_workspace_serves_fewer_rows(heads, group):
+    """A workspace made for max_rows rows serves every smaller number, across 128 rows a tile and more."""
+    cache = moe.KvCache(2, 1, heads, 64, 16)
+    sizes = [moe.moe_kv_attention_workspace_size(cache, m, heads * group) for m in range(40)]
+    assert sizes == sorted(sizes)
+
+
+@pytest.mark.parametrize("group,most", [(7, 19), (8, 17), (16, 9)])
+def test_fewer_rows_in_a_workspace_for_more(group, most):
+    c = Case([most, 1], [100, 300], 1, group, 64, 16, seed=group)
+    ws = moe.workspace(moe.moe_kv_attention_workspace_size(c.cache, most, group))
+    for m in range(1, most + 1):
+        cu, lens = [0, m, m + 1], [100 + m, 301]
+        args = (c.cache, 0, c.q[:m + 1], c.dev(cu), c.dev(lens), c.dev(c.table))
+        want = moe.moe_kv_attention(*args, max_rows=m)
+        got = moe.moe_kv_attention(*args, max_rows=m, ws=ws)
+        assert torch.equal(got, want) and moe.moe_check_status(ws) == moe.MOE_OK
