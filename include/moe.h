@@ -371,8 +371,8 @@ moe_status moe_kv_append(const moe_kv *kv, int layer, const uint16_t *k, size_t 
  * natural logarithm of sum_t exp(scale * q . k_t).  A row that sees no token gives out = 0
  * and lse = -infinity.  Keys and values a row does not see do not reach it, whatever they
  * are.  scale: positive and finite.
- * The query is split exactly into two E4M3 parts (a row's values below 2^-16 of its
- * largest lose their last bits) and the products of softmax weight and value scale into two
+ * The query is split into two E4M3 parts, exactly for values from 2^-9 of their row's largest
+ * on and to 2^-17 of that largest for smaller ones, and the products of softmax weight and value scale into two
  * more, so keys and values enter the tensor cores (kind::f8f6f4) as they lie in the cache.
  * Such a product keeps 8 significant bits, as bf16 has, or is off by 2^-17 of the largest that
  * the row sees in the same 128 tokens, taking a value scale below 2^-90 as 2^-90.  Scores,

@@ -8,8 +8,8 @@
 //
 //   - Codes go from HBM to shared memory to the tensor cores (kind::f8f6f4) as they lie in
 //     the cache, with no conversion.  What multiplies them must be E4M3 too: a bf16 query is
-//     exactly the sum of two E4M3 parts (4 + 4 significant bits) after a power of two per
-//     row, and a weight is written as two parts as well (8 bits, as bf16 has).  Each product
+//     the sum of two E4M3 parts (4 + 4 significant bits) after a power of two per row, exactly
+//     from 2^-9 of the row's largest value on and to 2^-17 of that below, and a weight is written as two parts as well (8 bits, as bf16 has).  Each product
 //     runs twice into the same accumulator; the tensor pipe has room for it.
 //   - A weight carries its page's value scale into the tensor cores: w = 2^(s - ref) vs.  ref is a
 //     row's own, over the tokens that it sees of the 128-token tile: max(s + log2 vs) - 8, so that
@@ -338,6 +338,11 @@ __device__ __forceinline__ float part_hi(float x) {
     return __uint_as_float((__float_as_uint(x) + 0x80000u) & 0xfff00000u);
 }
 
+// The same for queries: none below E4M3's normal range, where the first part would be rounded
+// when it is encoded and the second, left from the unrounded one, again.  So the two are off
+// by half of E4M3's smallest step, 2^-10, at most.
+__device__ __forceinline__ float query_hi(float x) { return fabsf(x) < 0.015625f ? 0.f : part_hi(x); }
+
 // A ring of stages: slot and phase parity of the next use.
 struct Ring {
     int s = 0;
@@ -590,7 +595,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs &a, RowInfo *rows, u
 #pragma unroll kUnroll
         for (int j = 0; j < 4; j++) {
             const float y0 = __uint_as_float(v[0] << 16) * f, y1 = __uint_as_float(v[0] & 0xffff0000u) * f;
-            const float h0 = part_hi(y0), h1 = part_hi(y1);
+            const float h0 = query_hi(y0), h1 = query_hi(y1);
             hi = hi >> 16 | (uint64_t)e4m3x2_rn(h0, h1) << 48;
             lo = lo >> 16 | (uint64_t)e4m3x2_rn(y0 - h0, y1 - h1) << 48;
             v[0] = v[1];

@@ -160,6 +160,32 @@ def test_value_scales_alike_at_the_ends(group, e):
     check(c)
 
 
+# ----------------------------------------------------------------- queries
+
+
+@pytest.mark.parametrize("group", [16, 32, 64, 128])
+def test_small_query_values(group):
+    """Every significand at 2^-7 to 2^-18 of the row's largest value, read from lse: one token, whose
+    key has one value at the small one's place, so that lse is the score.  The parts are multiples
+    of 2^-16 of the largest (E4M3's step 2^-9 at 2^7), which lse tells apart.  Exact from 2^-9 on;
+    to 2^-17 of the largest below."""
+    x = np.concatenate([np.arange(128, 256) / 128 * 2.0 ** e for e in range(-18, -6)])
+    x[::2] *= -1
+    seqs = len(x) // group
+    c = Case([1] * seqs, [0] * seqs, 1, group, 64, 16)
+    page = c.table[:, 0]
+    c.codes_np[page, 0, 0, 0] = 0
+    c.codes_np[page, 0, 0, 0, 9] = 0x38                   # 1
+    c.scales_np[page] = 1.0
+    c.upload()
+    q = np.zeros((seqs, group, 64))
+    q[..., 3], q[..., 9] = 1.0, x.reshape(seqs, group)
+    c.q = torch.from_numpy(q).to(torch.bfloat16).cuda()
+    _, lse = c.run(scale=256.0)
+    got = np.round(lse.double().cpu().numpy().reshape(-1) / 256 * 2.0 ** 16) * 2.0 ** -16
+    assert (np.abs(got - x) <= np.where(np.abs(x) >= 2.0 ** -9, 0, 2.0 ** -17)).all()
+
+
 # ------------------------------------------------------------- workspaces
 
 
