@@ -29,6 +29,7 @@ __device__ __forceinline__ bool append_range(const KvAppendArgs &a, int b, int &
     bool ok = seq_rows(a.cu_rows, b, a.rows, lo, hi);
     start = a.start[b];
     n = hi - lo;
+    if (n == 0) return ok;  // an idle sequence may start anywhere
     if (start < 0) {
         n = 0;
         return false;

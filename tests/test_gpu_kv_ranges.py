@@ -16,7 +16,7 @@ import pytest
 import torch
 
 from tests._util import bf16_half_ulp
-from tests.test_gpu_kv import Case, e4m3_values
+from tests.test_gpu_kv import Case, _append_case, e4m3_values, ref_append
 
 pytestmark = pytest.mark.gpu
 
@@ -207,3 +207,20 @@ def test_fewer_rows_in_a_workspace_for_more(group, most):
         want = moe.moe_kv_attention(*args, max_rows=m)
         got = moe.moe_kv_attention(*args, max_rows=m, ws=ws)
         assert torch.equal(got, want) and moe.moe_check_status(ws) == moe.MOE_OK
+
+
+# ----------------------------------------------------------------- appends
+
+
+def test_append_with_idle_sequences():
+    """A sequence without rows is left alone wherever it is said to start."""
+    cache, codes, scales, table, k, v = _append_case([3, 0, 2, 0], [10, 4, 30, 7], 2, 128, 16, seed=2)
+    dev = lambda a: torch.from_numpy(np.asarray(a, dtype=np.int32)).cuda()  # noqa: E731
+    cu = [0, 3, 3, 5, 5]
+    ws = moe.workspace(moe.moe_kv_append_workspace_size())
+    for idle in (-1, -2 ** 31, table.shape[1] * 16 + 1, 2 ** 31 - 1):
+        moe.moe_kv_append(cache, 1, k, v, dev(cu), dev([10, idle, 30, idle]), dev(table), ws=ws)
+        assert moe.moe_check_status(ws) == moe.MOE_OK
+    ref_append(codes, scales, k.double().cpu().numpy(), v.double().cpu().numpy(), cu, [10, 0, 30, 0], table, 16)
+    assert np.array_equal(cache.codes(1).double().cpu().numpy(), codes)
+    assert np.array_equal(cache.scales(1).double().cpu().numpy(), scales)
