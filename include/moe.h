@@ -352,8 +352,8 @@ void moe_kv_destroy(moe_kv *kv);
  * tokens (start[b] % page_tokens of them) keeps max(that, its old scale), and the kept
  * codes are rounded again as code * (old scale / new scale).  Codes are rounded to nearest
  * even; infinities saturate to +-448 and NaN stays NaN.  Two sequences must not append
- * to the same page.  Rows that would land outside the table, or in a page outside the
- * cache, are not written and MOE_ERR_BAD_PAGE is recorded.  ws:
+ * to the same page.  Rows that would land outside the table, past 2^30 tokens, or in a page
+ * outside the cache, are not written and MOE_ERR_BAD_PAGE is recorded.  ws:
  * moe_kv_append_workspace_size() bytes (the status word). */
 size_t moe_kv_append_workspace_size(void);
 moe_status moe_kv_append(const moe_kv *kv, int layer, const uint16_t *k, size_t ldk, const uint16_t *v, size_t ldv,

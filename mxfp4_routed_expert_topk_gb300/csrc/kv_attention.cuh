@@ -37,7 +37,6 @@ namespace {
 
 constexpr int kTokens = 128;             // tokens per tile
 constexpr int kMaxSlots = kTokens / 16;  // pages per tile
-constexpr int kMaxLen = 1 << 30;         // tokens of a sequence
 constexpr uint32_t kSwizzle64B = 4;
 constexpr int kStKvArrive = 40, kStKvExit = 5;  // StatusWord::pad
 constexpr int kFirstSoft = 4;            // first softmax warp

@@ -34,7 +34,7 @@ __device__ __forceinline__ bool append_range(const KvAppendArgs &a, int b, int &
         n = 0;
         return false;
     }
-    const int64_t room = (int64_t)a.table_width * a.kv.page - start;
+    const int64_t room = min((int64_t)a.table_width * a.kv.page, (int64_t)kMaxLen) - start;
     if ((int64_t)n > room) {
         n = room > 0 ? (int)room : 0;
         ok = false;

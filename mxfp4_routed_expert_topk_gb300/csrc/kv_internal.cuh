@@ -6,6 +6,8 @@
 
 namespace moe {
 
+constexpr int kMaxLen = 1 << 30;  // tokens of a sequence
+
 // Device-side view of a paged cache (layout in moe.h).
 struct KvView {
     uint8_t *base;

@@ -224,3 +224,30 @@ def test_append_with_idle_sequences():
     ref_append(codes, scales, k.double().cpu().numpy(), v.double().cpu().numpy(), cu, [10, 0, 30, 0], table, 16)
     assert np.array_equal(cache.codes(1).double().cpu().numpy(), codes)
     assert np.array_equal(cache.scales(1).double().cpu().numpy(), scales)
+
+
+def test_append_at_the_longest_lengths():
+    """A table with room for more than 2^31 tokens: up to 2^30 of them rows are written."""
+    rng = np.random.default_rng(1)
+    cache = moe.KvCache(2, 1, 1, 64, 128)
+    cache.buffer.fill_(0x31)
+    table = torch.full((1, (1 << 24) + 1), 1, dtype=torch.int32, device="cuda")
+    k, v = (torch.from_numpy(rng.standard_normal((2, 1, 64))).to(torch.bfloat16).cuda() for _ in range(2))
+    cu = torch.tensor([0, 2], dtype=torch.int32, device="cuda")
+    ws = moe.workspace(moe.moe_kv_append_workspace_size())
+    before = cache.buffer.clone()
+    for start in (2 ** 30, 2 ** 31 - 2, 2 ** 31 - 1):
+        moe.moe_kv_append(cache, 0, k, v, cu, torch.tensor([start], dtype=torch.int32, device="cuda"), table, ws=ws)
+        assert moe.moe_check_status(ws) == moe.MOE_ERR_BAD_PAGE and torch.equal(cache.buffer, before)
+        moe.moe_clear_status(ws)
+    for start, written in ((2 ** 30 - 130, 2), (2 ** 30 - 1, 1)):
+        cache.buffer.copy_(before)
+        cache.scales(0).fill_(1.0)
+        moe.moe_kv_append(cache, 0, k, v, cu, torch.tensor([start], dtype=torch.int32, device="cuda"), table, ws=ws)
+        assert moe.moe_check_status(ws) == (moe.MOE_OK if written == 2 else moe.MOE_ERR_BAD_PAGE)
+        moe.moe_clear_status(ws)
+        slot = start % 128
+        for side, x in enumerate((k, v)):
+            want = x[:written].float().to(torch.float8_e4m3fn)
+            assert torch.equal(cache.codes(0)[1, side, 0, slot:slot + written].float(), want[:, 0].float())
+            assert cache.scales(0)[1, side, 0] == 1.0
