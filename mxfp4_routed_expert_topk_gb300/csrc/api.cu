@@ -339,8 +339,8 @@ moe_status moe_kv_append(const moe_kv *kv, int layer, const uint16_t *k, size_t 
                          int table_width, int seqs, void *ws, size_t ws_bytes, moe_stream_t stream) {
     if (kv == nullptr || ws == nullptr) return MOE_ERR_INVALID_ARG;
     if (layer < 0 || layer >= kv->v.n_layers || rows < 0 || seqs < 0 || table_width < 0) return MOE_ERR_INVALID_ARG;
-    if (rows == 0 || seqs == 0 || table_width == 0) return MOE_OK;  // nothing to write (arrays may be null)
-    if (cu_rows == nullptr || start == nullptr || page_table == nullptr) return MOE_ERR_INVALID_ARG;
+    if (rows == 0 || seqs == 0) return MOE_OK;  // nothing to write (arrays may be null)
+    if (cu_rows == nullptr || start == nullptr || (page_table == nullptr && table_width > 0)) return MOE_ERR_INVALID_ARG;
     if (!rows_ok(k, ldk, kv->v.heads, kv->v.dim) || !rows_ok(v, ldv, kv->v.heads, kv->v.dim) || !aligned(ws, 256))
         return MOE_ERR_INVALID_ARG;
     if (ws_bytes < sizeof(StatusWord)) return MOE_ERR_WORKSPACE;

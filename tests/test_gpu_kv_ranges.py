@@ -251,3 +251,16 @@ def test_append_at_the_longest_lengths():
             want = x[:written].float().to(torch.float8_e4m3fn)
             assert torch.equal(cache.codes(0)[1, side, 0, slot:slot + written].float(), want[:, 0].float())
             assert cache.scales(0)[1, side, 0] == 1.0
+
+
+def test_append_into_no_table():
+    """Rows that have no table to land in are reported; sequences without rows need none."""
+    cache, _, _, _, k, v = _append_case([3], [0], 2, 64, 16, seed=2)
+    dev = lambda a: torch.from_numpy(np.asarray(a, dtype=np.int32)).cuda()  # noqa: E731
+    none = torch.empty((2, 0), dtype=torch.int32, device="cuda")
+    ws = moe.workspace(moe.moe_kv_append_workspace_size())
+    before = cache.buffer.clone()
+    moe.moe_kv_append(cache, 1, k, v, dev([1, 1, 1]), dev([0, 5]), none, ws=ws)
+    assert moe.moe_check_status(ws) == moe.MOE_OK
+    moe.moe_kv_append(cache, 1, k, v, dev([0, 2, 3]), dev([0, 0]), none, ws=ws)
+    assert moe.moe_check_status(ws) == moe.MOE_ERR_BAD_PAGE and torch.equal(cache.buffer, before)
