@@ -494,6 +494,7 @@ class KvCache:
         _check(lib().moe_kv_create(ctypes.byref(h), _ptr(buffer), buffer.numel(), n_pages, n_layers, heads, head_dim,
                                    page_tokens), "moe_kv_create")
         self.handle = h
+        self.device = buffer.get_device()
 
     def _layer(self, layer: int) -> torch.Tensor:
         if not 0 <= layer < self.n_layers:
@@ -525,13 +526,32 @@ class KvCache:
 _raw_stream_of = getattr(torch._C, "_cuda_getCurrentRawStream", None)
 
 
-def _raw_stream(stream, like):
-    """The stream's handle: `stream`, or the current one of the tensor's device."""
+def _raw_stream(stream, device):
+    """The stream's handle: `stream`, or the device's current one."""
     if stream is not None:
         return stream.cuda_stream
     if _raw_stream_of is None:
-        return torch.cuda.current_stream().cuda_stream
-    return _raw_stream_of(like.get_device())
+        return torch.cuda.current_stream(device).cuda_stream
+    return _raw_stream_of(device)
+
+
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+
+
+def _call(f, where, device, stream, tensors, *args):
+    """f(*args, stream) with `device` current, once every tensor and the stream are found to be on it."""
+    for t in tensors:
+        if t is not None and t.get_device() != device:
+            raise ValueError(f"{where}: expected every tensor on device {device}")
+    if stream is not None and stream.device_index != device:
+        raise ValueError(f"{where}: expected a stream of device {device}")
+    if _current_device() == device:
+        code = f(*args, _raw_stream(stream, device))
+    else:
+        with torch.cuda.device(device):
+            code = f(*args, _raw_stream(stream, device))
+    if code:
+        raise MoeError(code, where)
 
 
 def _need_heads(t, heads, dim, name):
@@ -587,17 +607,16 @@ def moe_kv_append(cache: KvCache, layer: int, k: torch.Tensor, v: torch.Tensor, 
     _need_index(start, seqs, "start")
     if ws is None:
         ws = _workspace_on(moe_kv_append_workspace_size(), k, stream)
-    code = lib().moe_kv_append(cache.handle, layer, k.data_ptr(), ldk, v.data_ptr(), ldv, rows, cu_rows.data_ptr(),
-                               start.data_ptr(), page_table.data_ptr(), width, seqs, ws.data_ptr(), ws.numel(),
-                               _raw_stream(stream, k))
-    if code:
-        raise MoeError(code, "moe_kv_append")
+    _call(lib().moe_kv_append, "moe_kv_append", cache.device, stream, (k, v, cu_rows, start, page_table, ws),
+          cache.handle, layer, k.data_ptr(), ldk, v.data_ptr(), ldv, rows, cu_rows.data_ptr(), start.data_ptr(),
+          page_table.data_ptr(), width, seqs, ws.data_ptr(), ws.numel())
 
 
 def moe_kv_attention_workspace_size(cache: KvCache, max_rows: int, heads_q: int) -> int:
     n = ctypes.c_size_t()
-    _check(lib().moe_kv_attention_workspace_size(cache.handle, max_rows, heads_q, ctypes.byref(n)),
-           "moe_kv_attention_workspace_size")
+    with torch.cuda.device(cache.device):
+        _check(lib().moe_kv_attention_workspace_size(cache.handle, max_rows, heads_q, ctypes.byref(n)),
+               "moe_kv_attention_workspace_size")
     return int(n.value)
 
 
@@ -625,13 +644,11 @@ def moe_kv_attention(cache: KvCache, layer: int, q: torch.Tensor, cu_rows: torch
             raise ValueError(f"lse: expected [{rows}, {heads_q}]")
     if ws is None:
         ws = _workspace_on(moe_kv_attention_workspace_size(cache, max_rows, heads_q), q, stream)
-    code = lib().moe_kv_attention(cache.handle, layer, q.data_ptr(), ldq, rows, heads_q, cu_rows.data_ptr(),
-                                  kv_len.data_ptr(), page_table.data_ptr(), width, seqs, max_rows,
-                                  dim ** -0.5 if scale is None else scale, out.data_ptr(), ldo,
-                                  None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel(),
-                                  _raw_stream(stream, q))
-    if code:
-        raise MoeError(code, "moe_kv_attention")
+    _call(lib().moe_kv_attention, "moe_kv_attention", cache.device, stream,
+          (q, cu_rows, kv_len, page_table, out, lse, ws), cache.handle, layer, q.data_ptr(), ldq, rows, heads_q,
+          cu_rows.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), width, seqs, max_rows,
+          dim ** -0.5 if scale is None else scale, out.data_ptr(), ldo, None if lse is None else lse.data_ptr(),
+          ws.data_ptr(), ws.numel())
     return out
 
 
@@ -685,12 +702,10 @@ def moe_verify_sampled(p: torch.Tensor, q: torch.Tensor | None, tokens: torch.Te
     _need(u_sample, torch.float32, "u_sample")
     if u_accept.numel() != rows or u_sample.numel() != seqs:
         raise ValueError("u_accept, u_sample: expected one value per row and one per sequence")
-    code = lib().moe_verify_sampled(p.data_ptr(), ldp, None if q is None else q.data_ptr(), ldq, dt, rows, vocab,
-                                    tokens.data_ptr(), cu_rows.data_ptr(), seqs, u_accept.data_ptr(),
-                                    u_sample.data_ptr(), accepted.data_ptr(), next_token.data_ptr(), ws.data_ptr(),
-                                    ws.numel(), _raw_stream(stream, p))
-    if code:
-        raise MoeError(code, "moe_verify_sampled")
+    _call(lib().moe_verify_sampled, "moe_verify_sampled", p.get_device(), stream,
+          (q, tokens, cu_rows, u_accept, u_sample, accepted, next_token, ws), p.data_ptr(), ldp,
+          None if q is None else q.data_ptr(), ldq, dt, rows, vocab, tokens.data_ptr(), cu_rows.data_ptr(), seqs,
+          u_accept.data_ptr(), u_sample.data_ptr(), accepted.data_ptr(), next_token.data_ptr(), ws.data_ptr(), ws.numel())
     return accepted, next_token
 
 
@@ -700,11 +715,9 @@ def moe_verify_greedy(logits: torch.Tensor, tokens: torch.Tensor, cu_rows: torch
     """(accepted, next_token), int32 [seqs]: drafts that equal the arg max, and the arg max after them."""
     rows, vocab, ld, dt = _need_probs(logits, "logits")
     seqs, accepted, next_token, ws = _verify_outputs(logits, rows, tokens, cu_rows, accepted, next_token, ws, stream)
-    code = lib().moe_verify_greedy(logits.data_ptr(), ld, dt, rows, vocab, tokens.data_ptr(), cu_rows.data_ptr(), seqs,
-                                   accepted.data_ptr(), next_token.data_ptr(), ws.data_ptr(), ws.numel(),
-                                   _raw_stream(stream, logits))
-    if code:
-        raise MoeError(code, "moe_verify_greedy")
+    _call(lib().moe_verify_greedy, "moe_verify_greedy", logits.get_device(), stream,
+          (tokens, cu_rows, accepted, next_token, ws), logits.data_ptr(), ld, dt, rows, vocab, tokens.data_ptr(),
+          cu_rows.data_ptr(), seqs, accepted.data_ptr(), next_token.data_ptr(), ws.data_ptr(), ws.numel())
     return accepted, next_token
 
 
