@@ -185,8 +185,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_few_kernel(const __g
     int *abort_flag = reinterpret_cast<int *>(misc + 1);
     int *go = reinterpret_cast<int *>(misc + 2);  // [worker]
     int64_t *sums = reinterpret_cast<int64_t *>(misc + 8);
-    Start *start = reinterpret_cast<Start *>(misc + 48);  // [worker]
-    static_assert(kThreads / 32 <= 20 && kWorkers * sizeof(Start) <= 320, "misc");
+    Start *start = reinterpret_cast<Start *>(misc + 56);  // [worker]
+    static_assert(kThreads / 32 * 12 <= 48 * 4 && kWorkers * sizeof(Start) <= 72 * 4, "misc");
     StatusWord *st = a.k.st;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 

@@ -118,15 +118,16 @@ struct Line {
     static __device__ __forceinline__ int64_t ratio(int64_t x, int64_t y) {
         return ((x | y) >> 32) == 0 ? (int64_t)((uint32_t)x / (uint32_t)y) : x / y;
     }
-    // No more workers than pay: k of them on a unit of L positions take its tiles in L / k steps
+    // Shares no shorter than pays: k workers on a unit of L positions take its tiles in L / k steps
     // but leave k parts to be joined one after the other, kJoin of which take a tile's time; L / k +
-    // k / kJoin is least at k = sqrt(kJoin L), so sqrt(kJoin units total) in all.  (One sequence of
-    // 100000 tokens, one head: 49 us, with every worker on it 133; 17 rows over 30000 38 and 66.
-    // kJoin = 2: 55 and 41; 10: 49 and 39.)
-    __device__ __forceinline__ void set(int64_t total_, int64_t units, int max_workers) {
+    // k / kJoin is least at shares of sqrt(L / kJoin).  The longest unit sets the limit, as it is the
+    // one that is waited for.  (One sequence of 100000 tokens, one head, 4 query heads: 50 us, alone
+    // or beside 63 short ones; with every worker on it 133.  With a limit by the number of units,
+    // 118 beside the short ones.  kJoin = 2: 55, 10: 49.)
+    __device__ __forceinline__ void set(int64_t total_, int longest, int max_workers) {
         constexpr float kJoin = 5.f;
         total = total_;
-        const float pay = ceilf(__fsqrt_rn(kJoin * (float)units * (float)total));
+        const float pay = ceilf((float)total * __fsqrt_rn(kJoin / (float)longest));
         workers = (int)min((int64_t)fminf(pay, (float)max_workers), total);
         share = workers > 0 ? ratio(total, workers) : 0;
         more = (int)(total - share * workers);
@@ -150,7 +151,7 @@ struct Start {
     Item x;
 };
 
-// Cut the line (all NT threads; `sums`: NT / 32 words of shared memory); the CTA's workers'
+// Cut the line (all NT threads; `sums`: NT / 32 x 12 bytes of shared memory); the CTA's workers'
 // starts are in start[] after the caller's next barrier.
 template <int NT, int NW>
 __device__ __forceinline__ Line cut_line(const AttnArgs &a, int64_t *sums, Start *start) {
@@ -161,6 +162,7 @@ __device__ __forceinline__ Line cut_line(const AttnArgs &a, int64_t *sums, Start
     // two rounds over the thread's items: their sum, then those that hold the workers' starts
     Line l;
     int64_t mine = 0, pre = 0, lo[NW];
+    int longest = 0, *tops = reinterpret_cast<int *>(sums + NT / 32);  // length of the longest unit
 #pragma unroll 1
     for (int round = 0; round < 2; round++) {
         int64_t at = pre;
@@ -169,7 +171,9 @@ __device__ __forceinline__ Line cut_line(const AttnArgs &a, int64_t *sums, Start
         for (int i = i0; i < i1; i++) {
             const Item x = load_item(a, i);
             good &= x.ok;
-            const int64_t u = (int64_t)unit_length(a, x) * a.k.kv.heads;
+            const int len = unit_length(a, x);
+            longest = max(longest, len);
+            const int64_t u = (int64_t)len * a.k.kv.heads;
             if (round == 1) {
 #pragma unroll
                 for (int w = 0; w < NW; w++) {
@@ -191,16 +195,21 @@ __device__ __forceinline__ Line cut_line(const AttnArgs &a, int64_t *sums, Start
             const int64_t o = __shfl_up_sync(0xffffffffu, pre, d);
             if (lane >= d) pre += o;
         }
-        if (lane == 31) sums[warp] = pre;
+        longest = __reduce_max_sync(0xffffffffu, longest);
+        if (lane == 31) {
+            sums[warp] = pre;
+            tops[warp] = longest;
+        }
         __syncthreads();
         int64_t total = 0;
 #pragma unroll 1
         for (int w = 0; w < NT / 32; w++) {
             if (w < warp) pre += sums[w];
             total += sums[w];
+            longest = max(longest, tops[w]);
         }
         pre -= mine;
-        l.set(total, (int64_t)items * a.k.kv.heads, (int)gridDim.x * NW);
+        l.set(total, longest, (int)gridDim.x * NW);
         bool holds = false;
 #pragma unroll
         for (int w = 0; w < NW; w++) {

@@ -310,6 +310,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
     int *n_shared = reinterpret_cast<int *>(misc + 2), *go = reinterpret_cast<int *>(misc + 3);
     int64_t *sums = reinterpret_cast<int64_t *>(misc + 8);
     Start *start = reinterpret_cast<Start *>(misc + 64);
+    static_assert(kThreads / 32 * 12 <= 56 * 4 && sizeof(Start) <= 64 * 4, "misc");
     StatusWord *st = a.k.st;
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
 

@@ -209,6 +209,27 @@ def test_fewer_rows_in_a_workspace_for_more(group, most):
         assert torch.equal(got, want) and moe.moe_check_status(ws) == moe.MOE_OK
 
 
+# ---------------------------------------------------------- division of work
+
+
+@pytest.mark.parametrize("group", [4, 20, 70])
+def test_long_sequence_beside_short_ones(group):
+    """The parts that a long sequence is cut into, each of them joined after all others, are as many
+    beside short sequences as alone; they are counted by what the call leaves in the workspace."""
+    parts = []
+    for short in (0, 10, 63):
+        n = [1] * (1 + short)
+        c = Case(n, [100000] + [4] * short, 1, group, 64, 128, seed=3)
+        ws = moe.workspace(moe.moe_kv_attention_workspace_size(c.cache, 1, group))
+        ws[256:] = 0xFF
+        moe.moe_kv_attention(c.cache, 0, c.q, c.dev(c.cu), c.dev(c.lens), c.dev(c.table), max_rows=1, ws=ws)
+        assert moe.moe_check_status(ws) == moe.MOE_OK
+        words = (ws[256:].view(torch.int32) != -1).sum().item()
+        assert words % (group * 66) == 0                  # whole parts: a row's 64 values, reference and sum
+        parts.append(words // (group * 66))
+    assert parts[0] > 1 and max(parts) <= 1.25 * parts[0], parts
+
+
 # ----------------------------------------------------------------- appends
 
 
