@@ -115,9 +115,10 @@ __device__ __forceinline__ void feed(const AttnArgs &a, const CUtensorMap *tm, u
                 t++;
                 if (lane == 0) eye.next();
             } else if (!told && (m & 6u) == 6u) {
+                __syncwarp();  // (lanes 1 and 2 have seen the places free; a vote orders no memory)
                 if (lane == 0) ring[seg & 1] = g;
                 if (g.count > 0)
-                    load_queries<D, kRows, 1>(a, reinterpret_cast<RowInfo *>(smem + F.rows) + (2 * w + (seg & 1)) * kRows,
+                    load_queries<D, kRows>(a, reinterpret_cast<RowInfo *>(smem + F.rows) + (2 * w + (seg & 1)) * kRows,
                                               smem + F.q + (uint32_t)w * (2u * kRows * D), g, 0, 1);
                 __syncwarp();
                 if (lane == 0) mbar_arrive(B.q_full(seg & 1));
@@ -262,6 +263,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_few_kernel(const __g
                 const uint32_t m = __ballot_sync(0xffffffffu, (lane >> 2) == w && eye.ready()) >> (4 * w);
                 const FewBars B{bars + 16 * w};
                 const bool out = np[w] < ns[w] && (m & 3u) == 3u;
+                __syncwarp();  // what one lane has seen holds for all (a vote orders no memory)
                 if (out) {
                     tc_fence_after();
                     const int s = np[w] & (kStages - 1);

@@ -534,9 +534,9 @@ struct Pages {
 // lane takes 8 values, so a pass covers 2 rows of 128 or 4 of 64; the next pass's loads are in
 // flight while one is converted.  One pass per turn: this code runs once per segment, and
 // fetching an unrolled loop costs more than the latency that it hides (four passes in flight:
-// one sequence of 300 tokens 31 us in place of 27).  kUnroll: words converted at once;
-// kCopies: how often the rows stand in the tile.
-template <int D, int R, int kUnroll, int kCopies = 1>
+// one sequence of 300 tokens 31 us in place of 27; all four words of a lane at once in the rows
+// form: 4 x 17 rows 325 us in place of 321).  kCopies: how often the rows stand in the tile.
+template <int D, int R, int kCopies = 1>
 __device__ __forceinline__ void load_queries(const AttnArgs &a, RowInfo *rows, unsigned char *q0, const Seg &g, int w,
                                              int nw) {
     constexpr int kLanes = D / 8, kPass = 32 / kLanes;
@@ -590,7 +590,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs &a, RowInfo *rows, u
             }
         }
         top = max(top & 0xffffu, top >> 16);
-#pragma unroll kUnroll
+#pragma unroll 1
         for (int d = kLanes / 2; d > 0; d >>= 1) top = max(top, __shfl_xor_sync(0xffffffffu, top, d));
         const int up = top == 0 ? 0 : min(126, 7 - ((int)(top >> 7) - 127));
         const float f = __uint_as_float((uint32_t)(127 + up) << 23);
@@ -600,7 +600,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs &a, RowInfo *rows, u
         const uint32_t swz = D == 128 ? (uint32_t)(rr & 7) : (uint32_t)((rr >> 1) & 3);
         unsigned char *dst = q0 + (uint32_t)rr * D + (((uint32_t)(col >> 1) ^ swz) << 4) + (uint32_t)(col & 1) * 8u;
         uint64_t hi = 0, lo = 0;  // codes of the 8 values
-#pragma unroll kUnroll
+#pragma unroll 1
         for (int j = 0; j < 4; j++) {
             const float y0 = __uint_as_float(v[0] << 16) * f, y1 = __uint_as_float(v[0] & 0xffff0000u) * f;
             const float h0 = query_hi(y0), h1 = query_hi(y1);

@@ -284,7 +284,7 @@ __device__ __forceinline__ bool segment_queries(const AttnArgs &a, unsigned char
     }
     const Seg &g = reinterpret_cast<const Seg *>(smem + L.seg)[s % kSegs];
     if (g.count > 0)
-        load_queries<D, kRows, 4, COPIES>(a, reinterpret_cast<RowInfo *>(smem + L.rows) + (s & 1) * kRows,
+        load_queries<D, kRows, COPIES>(a, reinterpret_cast<RowInfo *>(smem + L.rows) + (s & 1) * kRows,
                                           smem + L.q + (uint32_t)(s & 1) * (2u * kRows * D), g, w, nw);
     if ((threadIdx.x & 31) == 0) mbar_arrive(B.q_full(s & 1));
     return true;
@@ -385,6 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                 const uint32_t m = __ballot_sync(0xffffffffu, lane < 5 && eye.ready());
                 const bool out = np < ns && (m & 7u) == 7u;
                 if (ns == seg_end && !last && (m & 16u) != 0u) {  // the next segment's queries are there
+                    __syncwarp();  // what one lane has seen holds for all (a vote orders no memory)
                     const volatile Seg *sg = reinterpret_cast<const volatile Seg *>(smem + L.seg) + seg % kSegs;
                     const int count = __shfl_sync(0xffffffffu, sg->count, 0);
                     qb = seg & 1;
@@ -399,6 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                     continue;
                 }
                 idle = 0;
+                __syncwarp();
                 tc_fence_after();
                 if (out) {
                     const uint64_t va = vd + (uint64_t)((uint32_t)vs * kTile >> 4);
