@@ -28,8 +28,7 @@
 // outputs are added up at the end of the unit.  That halves (quarters) the softmax warps' work;
 // the joining warpgroup is then the slowest (1700 clocks a tile), so the softmax warps load the
 // queries.  24 sequences of 8192: 3 rows 136 -> 116 us, 9 rows 148 -> 136; heads of 64, 4 rows
-// 76 -> 55, 8 rows 79 -> 65; only units of one tile get slower (256 sequences of 128 tokens, 5
-// rows: 105 -> 115).
+// 76 -> 55, 8 rows 79 -> 65.  The choice is made where the kernel is launched.
 //
 // Not better: weights as one fp16 part with V's tile converted to fp16 in shared memory (4 x 17:
 // 346 us with two softmax warpgroups, 352 with three, where two parts took 338).
@@ -815,7 +814,12 @@ cudaError_t launch(const CUtensorMap &tm, AttnArgs a, int sms, int smem_max, cud
 cudaError_t set_wait_limit_kv_attention_rows(uint64_t ns) { return set_wait_limit_here(ns); }
 
 cudaError_t launch_attention_rows(const CUtensorMap &tm, AttnArgs a, int sms, int smem_max, cudaStream_t st) {
-    const int copies = a.rpt <= 32 ? 4 : a.rpt <= 64 ? 2 : 1;
+    // Copies pay by the tile and cost by the unit, so not for heads of 128 where the table has room for
+    // one tile of tokens only: 256 sequences of 128 tokens, 3 rows of 7 heads 96 us with copies, 90
+    // without; 5 rows 114 and 99; of 256 tokens 105 and 113, 121 and 132.  (Heads of 64, half the
+    // values to add up: 43 with copies at 128 tokens, 45 without.)
+    const bool one_tile = a.k.kv.dim == 128 && (int64_t)a.k.table_width * a.k.kv.page <= kTokens;
+    const int copies = a.rpt > 64 || one_tile ? 1 : a.rpt <= 32 ? 4 : 2;
     if (a.k.kv.dim == 128) {
         if (copies == 4) return launch<128, 4>(tm, a, sms, smem_max, st);
         return copies == 2 ? launch<128, 2>(tm, a, sms, smem_max, st) : launch<128, 1>(tm, a, sms, smem_max, st);

@@ -230,6 +230,21 @@ def test_long_sequence_beside_short_ones(group):
     assert parts[0] > 1 and max(parts) <= 1.25 * parts[0], parts
 
 
+@pytest.mark.parametrize("group", [4, 7, 12, 24])
+@pytest.mark.parametrize("dim", [64, 128])
+def test_tables_of_one_tile(group, dim):
+    """Tables that have room for 128 tokens take the rows in one copy where longer ones take several."""
+    c = Case([5, 1, 3], [107, 0, 40], 2, group, dim, 16, seed=group)
+    assert c.table.shape[1] * 16 == 128
+    check(c)
+    few, lse = c.run()
+    c.table = np.concatenate([c.table, np.full((3, 4), -1, dtype=np.int32)], 1)
+    check(c)
+    more, lse2 = c.run()
+    assert torch.allclose(few.float(), more.float(), rtol=2.0 ** -6, atol=2.0 ** -6)
+    assert torch.allclose(lse, lse2, rtol=0, atol=2.0 ** -12)
+
+
 # ----------------------------------------------------------------- appends
 
 
