@@ -372,16 +372,17 @@ moe_status moe_kv_append(const moe_kv *kv, int layer, const uint16_t *k, size_t 
  * and lse = -infinity.  Keys and values a row does not see do not reach it, whatever they
  * are.  scale: positive and finite.
  * The query is split into two E4M3 parts, exactly for values from 2^-9 of their row's largest
- * on and to 2^-17 of that largest for smaller ones, and the products of softmax weight and value scale into two
- * more, so keys and values enter the tensor cores (kind::f8f6f4) as they lie in the cache.
- * Such a product keeps 8 significant bits, as bf16 has, or is off by 2^-17 of the largest that
- * the row sees in the same 128 tokens, taking a value scale below 2^-90 as 2^-90.  Scores,
- * maxima, sums and outputs are fp32; sums stay exact to that where a sequence's value scales,
- * taken so, lie within 2^120 of one another.  The result does not depend on
- * timing, and a token whose page is outside the cache or past the table is reported as
- * MOE_ERR_BAD_PAGE (the sequence's rows are then not valid), as are more rows than
- * max_rows.  ws: moe_kv_attention_workspace_size() bytes for the current device (what serves
- * max_rows serves fewer, too). */
+ * on and to 2^-17 of that largest for smaller ones, and the products of softmax weight and
+ * value scale into two more, so keys and values enter the tensor cores (kind::f8f6f4) as they
+ * lie in the cache.  Such a product keeps 8 significant bits, as bf16 has, or is off by 2^-17
+ * of the largest that the row sees in the same 128 tokens, taking a value scale below 2^-90 as
+ * 2^-90.  Scores, maxima, sums and outputs are fp32; sums stay exact to that where a sequence's
+ * value scales, taken so, lie within 2^120 of one another and below 2^100.
+ * Rows that no sequence takes are not written.  The result does not depend on timing, and a
+ * token whose page is outside the cache or past the table is reported as MOE_ERR_BAD_PAGE (the
+ * sequence's rows are then not valid), as are more rows than max_rows.  ws:
+ * moe_kv_attention_workspace_size() bytes for the current device (what serves max_rows serves
+ * fewer, too). */
 moe_status moe_kv_attention_workspace_size(const moe_kv *kv, int max_rows, int heads_q, size_t *bytes);
 moe_status moe_kv_attention(const moe_kv *kv, int layer, const uint16_t *q, size_t ldq, int rows, int heads_q,
                             const int32_t *cu_rows, const int32_t *kv_len, const int32_t *page_table,

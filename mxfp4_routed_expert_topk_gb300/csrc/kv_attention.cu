@@ -8,7 +8,7 @@
 // its token (P^T is N-major); the maximum and sum of a row run across lanes.
 //
 // What bounds it is HBM for long sequences: one token for each of 64 sequences of up to 16384
-// (8 heads of 128, 7 query heads each) takes 192 us at 1119 MB, 5.8 TB/s (86 % of a copy's rate).
+// (8 heads of 128, 7 query heads each) takes 189 us at 1119 MB, 5.9 TB/s (87 % of a copy's rate).
 // A tile takes about 2800 clocks from its scores to its output (TMEM read, two cross-lane
 // reductions, a warpgroup barrier, the exponentials, the fences and the two MMA groups), twice
 // what its 32 KB take from HBM.  So a CTA has three workers, each a softmax warpgroup with a
@@ -25,9 +25,10 @@
 namespace moe {
 namespace {
 
-// Rows of a row tile.  (This form with 32 took 165 us for 4 rows in each of 24 sequences of
-// 8192, where the rows form takes 117; with 16 or fewer the rows form takes 116 us where this one
-// takes 92.)
+// Rows of a row tile.  This form with 32 took 165 us for 4 rows in each of 24 sequences of 8192,
+// where the rows form took 117.  With 7, 14 and 16 rows of heads of 128 this one takes 102, 106 and
+// 107 us there, the rows form 107, 109 and 109; with 8 and 16 rows of heads of 64 53 and 54, so 54
+// and 56.  96 sequences of 512: 14 rows of 128 56 and 67; only 16 rows of 64 37 and 35.
 constexpr int kRows = 16;
 // Workers of a CTA, a softmax warpgroup each.
 constexpr int kWorkers = 3;

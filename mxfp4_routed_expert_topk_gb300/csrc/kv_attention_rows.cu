@@ -12,23 +12,24 @@
 // one (the weight, below E4M3's range, becomes 0 all the same).  Weights replace the scores they
 // came from in TMEM.
 //
-// What bounds it is instruction issue and latency: 128 x 128 scores a tile at 7 to 8
+// What bounds it is instruction issue and latency: 128 x 128 scores a tile at about 8
 // instructions each are about 1000 clocks of all four schedulers, next to 1400 that the tile's
 // 32 KB take from HBM and 1024 of the tensor pipe; a tile takes 2500.  So the work is split by
 // role: softmax warpgroups take tiles in turn (a thread per row) over two or three score buffers,
 // so that the next scores are ready when a warpgroup comes for them, one more warpgroup joins
 // each tile's output with the running one as soon as it is there, and a warp of its own prepares
 // the tiles' constants.  Registers go to the warpgroups by need (setmaxnreg).  17 rows in each of
-// 4 sequences of up to 131072 tokens (7 query heads of 8 x 128) take 313 us: 0.50 of the HBM and
-// 0.43 of the bf16 rate; with the constants in the softmax warps 331, and without the joining
-// warpgroup and the third score buffer 438.
+// 4 sequences of up to 131072 tokens (7 query heads of 8 x 128) take 318 us: 0.49 of the HBM and
+// 0.42 of the bf16 rate (313 with one reference for a tile's value scales, which was wrong); with
+// the constants in the softmax warps 331, and without the joining warpgroup and the third score
+// buffer 438, both before that.
 //
 // Row tiles of up to 64 (32) rows stand two (four) times in the 128 places, and each copy takes a
 // half (quarter) of every tile's tokens: its weights for the others are zero, and the copies'
 // outputs are added up at the end of the unit.  That halves (quarters) the softmax warps' work;
 // the joining warpgroup is then the slowest (1700 clocks a tile), so the softmax warps load the
-// queries.  24 sequences of 8192: 3 rows 136 -> 116 us, 9 rows 148 -> 136; heads of 64, 4 rows
-// 76 -> 55, 8 rows 79 -> 65.  The choice is made where the kernel is launched.
+// queries.  24 sequences of 8192, when they came: 3 rows 136 -> 116 us (now 112), 9 rows 148 -> 136;
+// heads of 64, 4 rows 76 -> 55 (now 54), 8 rows 79 -> 65.  The choice is made where the kernel is launched.
 //
 // Not better: weights as one fp16 part with V's tile converted to fp16 in shared memory (4 x 17:
 // 346 us with two softmax warpgroups, 352 with three, where two parts took 338).
