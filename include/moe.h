@@ -325,7 +325,8 @@ moe_status moe_grouped_set_cta_pairs(int mode);
  * consecutive tokens of one sequence for all n_layers layers.  Its record is, per layer,
  * the E4M3 codes [2][heads][page_tokens][head_dim] (keys, then values; one byte each),
  * then the scales [2][heads] in fp32, then padding to a multiple of 128 bytes: a key or
- * value is code * scale of its page, side and head.  Pages of a sequence are named by its
+ * value is code * scale of its page, side and head (a caller that writes scales itself writes
+ * none below 0).  Pages of a sequence are named by its
  * row of a page table: token t of sequence b lies in page page_table[b][t / page_tokens]
  * at slot t % page_tokens.  Entries past a sequence's tokens are not read.
  *
