@@ -9,8 +9,9 @@
 //   - Codes go from HBM to shared memory to the tensor cores (kind::f8f6f4) as they lie in
 //     the cache, with no conversion.  What multiplies them must be E4M3 too: a bf16 query is
 //     the sum of two E4M3 parts (4 + 4 significant bits) after a power of two per row, exactly
-//     from 2^-9 of the row's largest value on and to 2^-17 of that below, and a weight is written as two parts as well (8 bits, as bf16 has).  Each product
-//     runs twice into the same accumulator; the tensor pipe has room for it.
+//     from 2^-9 of the row's largest value on and to 2^-17 of that below, and a weight is written
+//     as two parts as well (8 bits, as bf16 has).  Each product runs twice into the same
+//     accumulator; the tensor pipe has room for it.
 //   - A weight carries its page's value scale into the tensor cores: w = 2^(s - ref) vs.  ref is a
 //     row's own, over the tokens that it sees of the 128-token tile: max(s + log2 vs) - 8, so that
 //     its largest w is 256, and what E4M3's range cannot hold is below 2^-17 of that, whatever
