@@ -48,8 +48,9 @@ typedef enum {
                                       often in one multi-row decode call */
     MOE_ERR_TIMEOUT = 6,           /* device: a bounded wait gave up */
     MOE_ERR_NONFINITE = 7,         /* device: non-finite router input or logit */
-    MOE_ERR_BAD_PAGE = 8           /* device: a page outside the cache, or a length, row range
+    MOE_ERR_BAD_PAGE = 8,          /* device: a page outside the cache, or a length, row range
                                       or token outside what the call was given room for */
+    MOE_ERR_NO_PAGE = 9            /* device: fewer free pages than the call needs */
 } moe_status;
 
 typedef void *moe_stream_t;        /* a cudaStream_t */
@@ -390,6 +391,94 @@ moe_status moe_kv_attention(const moe_kv *kv, int layer, const uint16_t *q, size
                             int table_width, int seqs, int max_rows, float scale, uint16_t *out, size_t ldo,
                             float *lse, void *ws, size_t ws_bytes, moe_stream_t stream);
 
+/* Attention of sequences that share prefixes (several continuations sampled from one prompt,
+ * requests about one document): the same result as moe_kv_attention, with the shared tokens read
+ * once for all rows of a group.  Group g has the sequences cu_groups[g] .. cu_groups[g+1]-1
+ * (cu_groups [groups+1], ascending from 0 to seqs: every sequence is in one, alone if need be),
+ * whose first prefix_len[g] tokens are the same (0: nothing is shared).  What is taken as shared
+ * are the prefix's whole pages, as named by the first columns of the table row of the group's first
+ * sequence (the other sequences' entries there are not read); tokens of a page that the prefix does
+ * not fill are read for each sequence, from its own table.  New rows stand behind the prefix: a
+ * sequence with rows has kv_len[b] - (its rows) >= prefix_len[g], counted in whole pages, or is
+ * reported as MOE_ERR_BAD_PAGE, as are groups that do not take the sequences in order, and the
+ * errors of moe_kv_attention; rows are then not valid.  A group has at most max_group_rows rows in
+ * all (max_group_rows * heads_q / heads <= 2^24), a sequence at most max_rows.  q, out, lse, scale and
+ * the rest as for moe_kv_attention; the two parts of a row's result are held and added in fp32.
+ * ws: moe_kv_attention_shared_workspace_size() bytes for `rows` rows and the current device (what
+ * serves more rows serves fewer). */
+moe_status moe_kv_attention_shared_workspace_size(const moe_kv *kv, int rows, int max_rows, int max_group_rows,
+                                                  int heads_q, size_t *bytes);
+moe_status moe_kv_attention_shared(const moe_kv *kv, int layer, const uint16_t *q, size_t ldq, int rows, int heads_q,
+                                   const int32_t *cu_rows, const int32_t *kv_len, const int32_t *page_table,
+                                   int table_width, int seqs, const int32_t *cu_groups, const int32_t *prefix_len,
+                                   int groups, int max_rows, int max_group_rows, float scale, uint16_t *out, size_t ldo,
+                                   float *lse, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* ------------------------------------------------- pages from lengths
+ * What a step's page tables and row maps follow from, worked out on the GPU, so that a captured step
+ * serves any lengths.  refs [n_pages] counts the sequences that hold each page of a cache; a page is
+ * free while its count is 0.  (A caller that lets several sequences share pages writes those into
+ * their tables itself and counts them once for each.)
+ *
+ * moe_kv_reserve finds room for new_rows[b] tokens behind the start[b] that sequence b has.  Its
+ * columns ceil(start / page_tokens) .. ceil((start + new_rows) / page_tokens) - 1 of page_table
+ * [seqs][table_width] receive pages: in order of (sequence, column), the lowest-numbered free ones,
+ * whose count becomes 1.  Out: cu_rows [seqs+1] (running sum of new_rows) and kv_len [seqs] = start +
+ * new_rows, as moe_kv_append and moe_kv_attention take them (kv_len may be start itself); and, each
+ * unless NULL, for every row r: row_seq [r] its sequence, row_pos [r] the token it is in that, and
+ * row_slot [r] = page * page_tokens + place in it.  Entries behind the last row are not written.
+ * Nothing is reserved unless all is: with too few free pages (MOE_ERR_NO_PAGE), or with a negative
+ * count or length, more tokens than the table has room for or 2^30, more than `rows` rows in all, or
+ * new rows that would join tokens in a page that is not held once (MOE_ERR_BAD_PAGE), the table and
+ * the counts stay as they were, cu_rows becomes all 0 and kv_len = start.  A sequence without new
+ * rows may have any length.  seqs <= 16384, n_pages <= 2^24.
+ *
+ * moe_kv_release gives back what tokens keep[b] .. kv_len[b]-1 occupied (rejected drafts; keep 0:
+ * a finished sequence): columns ceil(keep / page_tokens) .. ceil(kv_len / page_tokens) - 1 become -1
+ * and their pages' counts fall by one each.  keep >= kv_len gives nothing back.  A negative keep, a
+ * length past the table (the sequence is left alone), or an entry that names no held page, is
+ * reported as MOE_ERR_BAD_PAGE.
+ *
+ * page_tokens 16, 32, 64 or 128.  ws: moe_kv_pages_workspace_size() bytes (the status word). */
+moe_status moe_kv_pages_workspace_size(int seqs, int n_pages, size_t *bytes);
+moe_status moe_kv_reserve(const int32_t *new_rows, const int32_t *start, int seqs, int32_t *page_table, int table_width,
+                          int32_t *refs, int n_pages, int page_tokens, int rows, int32_t *cu_rows, int32_t *kv_len,
+                          int32_t *row_seq, int32_t *row_pos, int64_t *row_slot, void *ws, size_t ws_bytes,
+                          moe_stream_t stream);
+moe_status moe_kv_release(const int32_t *keep, const int32_t *kv_len, int seqs, int32_t *page_table, int table_width,
+                          int32_t *refs, int n_pages, int page_tokens, void *ws, size_t ws_bytes, moe_stream_t stream);
+
+/* -------------------------------------------------------------- sampling
+ * The next token of each row from its logits x [rows][vocab] in `dtype` (MOE_PROB_*), row r at
+ * x + r * ld elements, 1 <= vocab <= 2^20.  temperature, top_k, top_p, min_p, u: one per row; top_k,
+ * top_p and min_p may be NULL (no such cut).
+ *
+ * It is defined in whole numbers, so that it does not depend on the order of sums.  NaN and -infinity
+ * take no part.  Tokens stand in the order of falling logit, ties by rising index.  With m the row's
+ * largest, c = log2(e) / temperature (at most 2^128 - 2^104), and every operation rounded to fp32:
+ * y = (x - m) c (0 where x = m), n = y rounded to the nearest whole number, ties to even, f = y - n,
+ *   p = 2^n (1 + f (C1 + f (C2 + f (C3 + f (C4 + f C5))))),
+ *   C1 = 0x1.62e42ap-1, C2 = 0x1.ebf9bcp-3, C3 = 0x1.c6b752p-5, C4 = 0x1.3cea88p-7, C5 = 0x1.5bba14p-10
+ * (2^y to a part in 2^22), and the weight W = floor(2^38 p), 0 unless y > -39.  Then, in this order:
+ *  - top_k keeps the first top_k tokens (< 1: all);
+ *  - top_p, as t = floor(2^24 min(max(top_p, 0), 1)), at least 1 (NaN: 2^24): of the sum S of the
+ *    weights kept so far, a token stays if those before it sum to less than S t / 2^24;
+ *  - min_p, as t = floor(2^24 min(max(min_p, 0), 1)) (NaN: 0): a token stays if W >= 2^14 t.
+ * moe_sample: with S the sum of what is left and t = floor(2^24 u) (clamped to 0 .. 2^24 - 1), next =
+ * the lowest index i at which the kept weights of tokens 0 .. i sum to more than floor(S t / 2^24).
+ * moe_sample_probs: probs [rows][vocab] in `dtype`, row r at probs + r * ldp, the kept weights divided
+ * by S (both rounded to fp32, then to `dtype`), 0 elsewhere: what moe_verify_sampled takes as p or q.
+ * probs may be x itself.  temperature <= 0 or NaN: the first token of the order (probability 1), whatever
+ * the cuts.  A row of nothing but NaN and -infinity: next = -1, probabilities 0.
+ * ws: moe_sample_workspace_size() bytes. */
+moe_status moe_sample_workspace_size(int rows, int vocab, size_t *bytes);
+moe_status moe_sample(const void *x, size_t ld, int dtype, int rows, int vocab, const float *temperature,
+                      const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *next,
+                      void *ws, size_t ws_bytes, moe_stream_t stream);
+moe_status moe_sample_probs(const void *x, size_t ld, int dtype, int rows, int vocab, const float *temperature,
+                            const int32_t *top_k, const float *top_p, const float *min_p, void *probs, size_t ldp,
+                            void *ws, size_t ws_bytes, moe_stream_t stream);
+
 /* ----------------------------------------------------- draft verification
  * The verdict after the last layer of a verify step ("可选的 Qwen 扩展": several drafted
  * tokens checked in one forward pass).  Sequence b was fed the tokens tokens[cu_rows[b]]
@@ -451,8 +540,8 @@ moe_status moe_debug_set_barrier_extra(int extra);
  * kernel ("route_single", "route_logits", "route_select", "decode_fused",
  * "decode_prep", "decode_gateup", "decode_down", "sort_rank", "sort_scan",
  * "sort_scatter", "sort_small", "gather_quant", "gather_split", "gemm_gateup", "gemm_down",
- * "combine", "prescale", "kv_append", "kv_attention", "verify_sampled",
- * "verify_greedy") is bracketed by CUDA events
+ * "combine", "prescale", "kv_append", "kv_attention", "kv_attention_shared", "kv_reserve",
+ * "kv_release", "sample", "sample_probs", "verify_sampled", "verify_greedy") is bracketed by CUDA events
  * on its stream (at most 65536 launches are recorded).  moe_trace_end()
  * synchronises the device and returns the number of recorded launches and their
  * summed device time in milliseconds.  Tracing is process-wide and not

@@ -24,6 +24,7 @@ MOE_ERR_BAD_INDEX = 5
 MOE_ERR_TIMEOUT = 6
 MOE_ERR_NONFINITE = 7
 MOE_ERR_BAD_PAGE = 8
+MOE_ERR_NO_PAGE = 9
 
 MOE_OP_ROUTE, MOE_OP_DECODE, MOE_OP_GROUPED = 0, 1, 2
 MOE_ACT_MXFP8, MOE_ACT_MXFP4 = 1, 2
@@ -43,6 +44,9 @@ EXPORTED = [
     "moe_stream_pool_map", "moe_stream_pool_stats", "moe_host_alloc", "moe_host_free", "moe_host_numa_node",
     "moe_kv_page_bytes", "moe_kv_create", "moe_kv_destroy", "moe_kv_append_workspace_size", "moe_kv_append",
     "moe_kv_attention_workspace_size", "moe_kv_attention",
+    "moe_kv_attention_shared_workspace_size", "moe_kv_attention_shared",
+    "moe_kv_pages_workspace_size", "moe_kv_reserve", "moe_kv_release",
+    "moe_sample_workspace_size", "moe_sample", "moe_sample_probs",
     "moe_verify_workspace_size", "moe_verify_sampled", "moe_verify_greedy",
 ]
 
@@ -105,6 +109,15 @@ def lib() -> ctypes.CDLL:
             "moe_kv_attention_workspace_size": (_i, [_vp, _i, _i, ctypes.POINTER(_sz)]),
             "moe_kv_attention": (_i, [_vp, _i, _vp, _sz, _i, _i, _vp, _vp, _vp, _i, _i, _i, ctypes.c_float, _vp, _sz,
                                       _vp, _vp, _sz, _vp]),
+            "moe_kv_attention_shared_workspace_size": (_i, [_vp, _i, _i, _i, _i, ctypes.POINTER(_sz)]),
+            "moe_kv_attention_shared": (_i, [_vp, _i, _vp, _sz, _i, _i, _vp, _vp, _vp, _i, _i, _vp, _vp, _i, _i, _i,
+                                             ctypes.c_float, _vp, _sz, _vp, _vp, _sz, _vp]),
+            "moe_kv_pages_workspace_size": (_i, [_i, _i, ctypes.POINTER(_sz)]),
+            "moe_kv_reserve": (_i, [_vp, _vp, _i, _vp, _i, _vp, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+            "moe_kv_release": (_i, [_vp, _vp, _i, _vp, _i, _vp, _i, _i, _vp, _sz, _vp]),
+            "moe_sample_workspace_size": (_i, [_i, _i, ctypes.POINTER(_sz)]),
+            "moe_sample": (_i, [_vp, _sz, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]),
+            "moe_sample_probs": (_i, [_vp, _sz, _i, _i, _i, _vp, _vp, _vp, _vp, _vp, _sz, _vp, _sz, _vp]),
             "moe_verify_workspace_size": (_i, [_i, _i, ctypes.POINTER(_sz)]),
             "moe_verify_sampled": (_i, [_vp, _sz, _vp, _sz, _i, _i, _i, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _sz,
                                         _vp]),
@@ -650,6 +663,161 @@ def moe_kv_attention(cache: KvCache, layer: int, q: torch.Tensor, cu_rows: torch
           dim ** -0.5 if scale is None else scale, out.data_ptr(), ldo, None if lse is None else lse.data_ptr(),
           ws.data_ptr(), ws.numel())
     return out
+
+
+def moe_kv_attention_shared_workspace_size(cache: KvCache, rows: int, max_rows: int, max_group_rows: int,
+                                           heads_q: int) -> int:
+    n = ctypes.c_size_t()
+    with torch.cuda.device(cache.device):
+        _check(lib().moe_kv_attention_shared_workspace_size(cache.handle, rows, max_rows, max_group_rows, heads_q,
+                                                            ctypes.byref(n)), "moe_kv_attention_shared_workspace_size")
+    return int(n.value)
+
+
+def moe_kv_attention_shared(cache: KvCache, layer: int, q: torch.Tensor, cu_rows: torch.Tensor, kv_len: torch.Tensor,
+                            page_table: torch.Tensor, cu_groups: torch.Tensor, prefix_len: torch.Tensor, max_rows: int,
+                            max_group_rows: int, scale: float | None = None, out: torch.Tensor | None = None,
+                            lse: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """moe_kv_attention of sequences in groups cu_groups [groups + 1] that share their first prefix_len [groups]
+    tokens, which are read once for each group; returns out (bf16, like q)."""
+    rows, heads_q, _ = q.shape
+    dim = cache.head_dim
+    ldq = _need_heads(q, heads_q, dim, "q")
+    seqs, width = _need_table(page_table)
+    groups = prefix_len.numel()
+    _need_index(cu_rows, seqs + 1, "cu_rows")
+    _need_index(kv_len, seqs, "kv_len")
+    _need_index(prefix_len, groups, "prefix_len")
+    _need_index(cu_groups, groups + 1, "cu_groups")
+    if out is None:
+        out, ldo = _empty((rows, heads_q, dim), torch.bfloat16, q, stream), heads_q * dim
+    else:
+        ldo = _need_heads(out, heads_q, dim, "out")
+        if out.shape[0] != rows:
+            raise ValueError(f"out: expected {rows} rows")
+    if lse is not None:
+        _need(lse, torch.float32, "lse")
+        if lse.numel() != rows * heads_q:
+            raise ValueError(f"lse: expected [{rows}, {heads_q}]")
+    if ws is None:
+        ws = _workspace_on(moe_kv_attention_shared_workspace_size(cache, rows, max_rows, max_group_rows, heads_q), q, stream)
+    _call(lib().moe_kv_attention_shared, "moe_kv_attention_shared", cache.device, stream,
+          (q, cu_rows, kv_len, page_table, cu_groups, prefix_len, out, lse, ws), cache.handle, layer, q.data_ptr(), ldq,
+          rows, heads_q, cu_rows.data_ptr(), kv_len.data_ptr(), page_table.data_ptr(), width, seqs, cu_groups.data_ptr(),
+          prefix_len.data_ptr(), groups, max_rows, max_group_rows, dim ** -0.5 if scale is None else scale,
+          out.data_ptr(), ldo, None if lse is None else lse.data_ptr(), ws.data_ptr(), ws.numel())
+    return out
+
+
+# ----------------------------------------------------- pages from lengths
+
+
+def moe_kv_pages_workspace_size(seqs: int, n_pages: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_kv_pages_workspace_size(seqs, n_pages, ctypes.byref(n)), "moe_kv_pages_workspace_size")
+    return int(n.value)
+
+
+def moe_kv_reserve(new_rows: torch.Tensor, start: torch.Tensor, page_table: torch.Tensor, refs: torch.Tensor,
+                   page_tokens: int, rows: int, cu_rows: torch.Tensor | None = None, kv_len: torch.Tensor | None = None,
+                   row_seq: torch.Tensor | None = None, row_pos: torch.Tensor | None = None,
+                   row_slot: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """Find pages for new_rows [seqs] tokens behind the start [seqs] of each sequence; page_table and refs [n_pages]
+    are updated.  Returns (cu_rows, kv_len, row_seq, row_pos, row_slot), the last three with room for `rows` rows."""
+    seqs, width = _need_table(page_table)
+    _need_index(new_rows, seqs, "new_rows")
+    _need_index(start, seqs, "start")
+    n_pages = refs.numel()
+    _need_index(refs, n_pages, "refs")
+    outs = []
+    for t, n, dtype, name in ((cu_rows, seqs + 1, torch.int32, "cu_rows"), (kv_len, seqs, torch.int32, "kv_len"),
+                              (row_seq, rows, torch.int32, "row_seq"), (row_pos, rows, torch.int32, "row_pos"),
+                              (row_slot, rows, torch.int64, "row_slot")):
+        if t is None:
+            t = _empty((n,), dtype, page_table, stream)
+        elif not (t.is_cuda and t.dtype == dtype and t.is_contiguous() and t.numel() == n):
+            raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor of {n} values")
+        outs.append(t)
+    if ws is None:
+        ws = _workspace_on(moe_kv_pages_workspace_size(seqs, n_pages), page_table, stream)
+    _call(lib().moe_kv_reserve, "moe_kv_reserve", page_table.get_device(), stream, (new_rows, start, refs, *outs, ws),
+          new_rows.data_ptr(), start.data_ptr(), seqs, page_table.data_ptr(), width, refs.data_ptr(), n_pages, page_tokens,
+          rows, *(t.data_ptr() for t in outs), ws.data_ptr(), ws.numel())
+    return tuple(outs)
+
+
+def moe_kv_release(keep: torch.Tensor, kv_len: torch.Tensor, page_table: torch.Tensor, refs: torch.Tensor,
+                   page_tokens: int, ws: torch.Tensor | None = None, stream=None):
+    """Give back the pages of tokens keep [seqs] .. kv_len [seqs] - 1; page_table and refs are updated."""
+    seqs, width = _need_table(page_table)
+    _need_index(keep, seqs, "keep")
+    _need_index(kv_len, seqs, "kv_len")
+    n_pages = refs.numel()
+    _need_index(refs, n_pages, "refs")
+    if ws is None:
+        ws = _workspace_on(moe_kv_pages_workspace_size(seqs, n_pages), page_table, stream)
+    _call(lib().moe_kv_release, "moe_kv_release", page_table.get_device(), stream, (keep, kv_len, refs, ws),
+          keep.data_ptr(), kv_len.data_ptr(), seqs, page_table.data_ptr(), width, refs.data_ptr(), n_pages, page_tokens,
+          ws.data_ptr(), ws.numel())
+
+
+# ---------------------------------------------------------------- sampling
+
+
+def moe_sample_workspace_size(rows: int, vocab: int) -> int:
+    n = ctypes.c_size_t()
+    _check(lib().moe_sample_workspace_size(rows, vocab, ctypes.byref(n)), "moe_sample_workspace_size")
+    return int(n.value)
+
+
+def _sample_args(logits, rows, vocab, temperature, top_k, top_p, min_p, ws, stream):
+    """The rows' settings as pointers, and the workspace."""
+    for t, dtype, name in ((temperature, torch.float32, "temperature"), (top_k, torch.int32, "top_k"),
+                           (top_p, torch.float32, "top_p"), (min_p, torch.float32, "min_p")):
+        if t is None and name != "temperature":
+            continue
+        if not (t.is_cuda and t.dtype == dtype and t.is_contiguous() and t.numel() == rows):
+            raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor of {rows} values")
+    if ws is None:
+        ws = _workspace_on(moe_sample_workspace_size(rows, vocab), logits, stream)
+    return [None if t is None else t.data_ptr() for t in (temperature, top_k, top_p, min_p)], ws
+
+
+def moe_sample(logits: torch.Tensor, temperature: torch.Tensor, u: torch.Tensor, top_k: torch.Tensor | None = None,
+               top_p: torch.Tensor | None = None, min_p: torch.Tensor | None = None,
+               next_token: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """next_token, int32 [rows]: drawn from each row of logits [rows, vocab] by its uniform number u [rows]."""
+    rows, vocab, ld, dt = _need_probs(logits, "logits")
+    cuts, ws = _sample_args(logits, rows, vocab, temperature, top_k, top_p, min_p, ws, stream)
+    _need(u, torch.float32, "u")
+    if u.numel() != rows:
+        raise ValueError(f"u: expected {rows} values")
+    if next_token is None:
+        next_token = _empty((rows,), torch.int32, logits, stream)
+    else:
+        _need_index(next_token, rows, "next_token")
+    _call(lib().moe_sample, "moe_sample", logits.get_device(), stream,
+          (temperature, top_k, top_p, min_p, u, next_token, ws), logits.data_ptr(), ld, dt, rows, vocab, *cuts,
+          u.data_ptr(), next_token.data_ptr(), ws.data_ptr(), ws.numel())
+    return next_token
+
+
+def moe_sample_probs(logits: torch.Tensor, temperature: torch.Tensor, top_k: torch.Tensor | None = None,
+                     top_p: torch.Tensor | None = None, min_p: torch.Tensor | None = None,
+                     probs: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
+    """probs [rows, vocab], of the logits' type: the distributions that moe_sample draws from."""
+    rows, vocab, ld, dt = _need_probs(logits, "logits")
+    cuts, ws = _sample_args(logits, rows, vocab, temperature, top_k, top_p, min_p, ws, stream)
+    if probs is None:
+        probs, ldp = _empty((rows, vocab), logits.dtype, logits, stream), vocab
+    else:
+        rows_p, vocab_p, ldp, dt_p = _need_probs(probs, "probs")
+        if rows_p != rows or vocab_p != vocab or dt_p != dt:
+            raise ValueError("probs: expected the shape and type of logits")
+    _call(lib().moe_sample_probs, "moe_sample_probs", logits.get_device(), stream,
+          (temperature, top_k, top_p, min_p, probs, ws), logits.data_ptr(), ld, dt, rows, vocab, *cuts, probs.data_ptr(),
+          ldp, ws.data_ptr(), ws.numel())
+    return probs
 
 
 # ----------------------------------------------------- draft verification

@@ -3,6 +3,8 @@
 #include <stdlib.h>
 #include <string.h>
 
+#include <algorithm>
+
 #include "kv_internal.cuh"
 #include "moe_internal.cuh"
 
@@ -228,6 +230,7 @@ const char *moe_status_string(moe_status s) {
         case MOE_ERR_TIMEOUT: return "bounded device wait expired";
         case MOE_ERR_NONFINITE: return "non-finite router input";
         case MOE_ERR_BAD_PAGE: return "page, length, row range or token out of range";
+        case MOE_ERR_NO_PAGE: return "too few free pages";
         default: return "unknown status";
     }
 }
@@ -376,6 +379,140 @@ moe_status moe_kv_attention(const moe_kv *kv, int layer, const uint16_t *q, size
     KvAttentionArgs a = {kv->v,      layer, q,        ldq,   rows, heads_q, cu_rows, kv_len,          page_table,
                          table_width, seqs,  max_rows, scale, out,  ldo,     lse,     (StatusWord *)ws};
     return cuda_status(launch_kv_attention(a, ws, (cudaStream_t)stream));
+}
+
+moe_status moe_kv_attention_shared_workspace_size(const moe_kv *kv, int rows, int max_rows, int max_group_rows,
+                                                  int heads_q, size_t *bytes) {
+    if (kv == nullptr || bytes == nullptr) return MOE_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (rows < 0 || max_rows < 0 || max_group_rows < 0 || heads_q < 1 || heads_q % kv->v.heads != 0)
+        return MOE_ERR_INVALID_ARG;
+    const int64_t group = heads_q / kv->v.heads;
+    if (heads_q > 32768 || std::max(max_rows, max_group_rows) > (1 << 20) ||
+        std::max(max_rows, max_group_rows) * group > (1 << 24))
+        return MOE_ERR_UNSUPPORTED_SHAPE;
+    return cuda_status(kv_attention_shared_workspace_bytes(kv->v, rows, max_rows, max_group_rows, heads_q, bytes));
+}
+
+moe_status moe_kv_attention_shared(const moe_kv *kv, int layer, const uint16_t *q, size_t ldq, int rows, int heads_q,
+                                   const int32_t *cu_rows, const int32_t *kv_len, const int32_t *page_table,
+                                   int table_width, int seqs, const int32_t *cu_groups, const int32_t *prefix_len,
+                                   int groups, int max_rows, int max_group_rows, float scale, uint16_t *out, size_t ldo,
+                                   float *lse, void *ws, size_t ws_bytes, moe_stream_t stream) {
+    if (kv == nullptr || ws == nullptr) return MOE_ERR_INVALID_ARG;
+    if (layer < 0 || layer >= kv->v.n_layers || rows < 0 || seqs < 0 || table_width < 0 || groups < 0)
+        return MOE_ERR_INVALID_ARG;
+    if (!(scale > 0.f) || !(scale <= 3.4028235e38f)) return MOE_ERR_INVALID_ARG;
+    size_t need = 0;
+    const moe_status s = moe_kv_attention_shared_workspace_size(kv, rows, max_rows, max_group_rows, heads_q, &need);
+    if (s != MOE_OK) return s;
+    if (rows == 0 || seqs == 0) return MOE_OK;  // nothing to write (arrays may be null)
+    if (groups == 0 || cu_rows == nullptr || kv_len == nullptr || (page_table == nullptr && table_width > 0) ||
+        cu_groups == nullptr || prefix_len == nullptr)
+        return MOE_ERR_INVALID_ARG;
+    if (!rows_ok(q, ldq, heads_q, kv->v.dim) || !rows_ok(out, ldo, heads_q, kv->v.dim) || !aligned(ws, 256))
+        return MOE_ERR_INVALID_ARG;
+    if (ws_bytes < need) return MOE_ERR_WORKSPACE;
+    KvAttentionArgs a = {kv->v,      layer, q,        ldq,   rows, heads_q, cu_rows, kv_len,          page_table,
+                         table_width, seqs,  max_rows, scale, out,  ldo,     lse,     (StatusWord *)ws};
+    return cuda_status(
+        launch_kv_attention_shared(a, cu_groups, prefix_len, groups, max_group_rows, ws, (cudaStream_t)stream));
+}
+
+moe_status moe_kv_pages_workspace_size(int seqs, int n_pages, size_t *bytes) {
+    if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (seqs < 0 || n_pages < 0) return MOE_ERR_INVALID_ARG;
+    if (seqs > kMaxReserveSeqs || n_pages > (1 << 24)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    *bytes = sizeof(StatusWord);
+    return MOE_OK;
+}
+
+namespace {
+
+// What reserving and releasing pages both check.
+moe_status pages_check(int seqs, const void *page_table, int table_width, const void *refs, int n_pages, int page,
+                       const void *ws, size_t ws_bytes) {
+    size_t need = 0;
+    const moe_status s = moe_kv_pages_workspace_size(seqs, n_pages, &need);
+    if (s != MOE_OK) return s;
+    if (ws == nullptr || !aligned(ws, 256) || table_width < 0) return MOE_ERR_INVALID_ARG;
+    if (!kv_shape_ok(1, 1, 64, page)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    if ((page_table == nullptr && seqs > 0 && table_width > 0) || (refs == nullptr && n_pages > 0)) return MOE_ERR_INVALID_ARG;
+    return ws_bytes < need ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+}  // namespace
+
+moe_status moe_kv_reserve(const int32_t *new_rows, const int32_t *start, int seqs, int32_t *page_table, int table_width,
+                          int32_t *refs, int n_pages, int page_tokens, int rows, int32_t *cu_rows, int32_t *kv_len,
+                          int32_t *row_seq, int32_t *row_pos, int64_t *row_slot, void *ws, size_t ws_bytes,
+                          moe_stream_t stream) {
+    const moe_status s = pages_check(seqs, page_table, table_width, refs, n_pages, page_tokens, ws, ws_bytes);
+    if (s != MOE_OK) return s;
+    if (rows < 0 || cu_rows == nullptr || (seqs > 0 && (new_rows == nullptr || start == nullptr || kv_len == nullptr)))
+        return MOE_ERR_INVALID_ARG;
+    KvReserveArgs a = {new_rows, start,   seqs,   page_table, table_width, refs,    n_pages,         page_tokens,
+                       rows,     cu_rows, kv_len, row_seq,    row_pos,     row_slot, (StatusWord *)ws};
+    return cuda_status(launch_kv_reserve(a, (cudaStream_t)stream));
+}
+
+moe_status moe_kv_release(const int32_t *keep, const int32_t *kv_len, int seqs, int32_t *page_table, int table_width,
+                          int32_t *refs, int n_pages, int page_tokens, void *ws, size_t ws_bytes, moe_stream_t stream) {
+    const moe_status s = pages_check(seqs, page_table, table_width, refs, n_pages, page_tokens, ws, ws_bytes);
+    if (s != MOE_OK) return s;
+    if (seqs == 0) return MOE_OK;
+    if (keep == nullptr || kv_len == nullptr) return MOE_ERR_INVALID_ARG;
+    KvReleaseArgs a = {keep, kv_len, seqs, page_table, table_width, refs, n_pages, page_tokens, (StatusWord *)ws};
+    return cuda_status(launch_kv_release(a, (cudaStream_t)stream));
+}
+
+moe_status moe_sample_workspace_size(int rows, int vocab, size_t *bytes) {
+    if (bytes == nullptr) return MOE_ERR_INVALID_ARG;
+    *bytes = 0;
+    if (rows < 0 || vocab < 1) return MOE_ERR_INVALID_ARG;
+    if (vocab > (1 << 20) || rows > (1 << 20)) return MOE_ERR_UNSUPPORTED_SHAPE;
+    *bytes = sizeof(StatusWord);
+    return MOE_OK;
+}
+
+namespace {
+
+// What both kinds of sampling check.
+moe_status sample_check(const SampleArgs &a, int dtype, const void *ws, size_t ws_bytes) {
+    size_t need = 0;
+    const moe_status s = moe_sample_workspace_size(a.rows, a.vocab, &need);
+    if (s != MOE_OK) return s;
+    if (dtype != MOE_PROB_F32 && dtype != MOE_PROB_BF16) return MOE_ERR_INVALID_ARG;
+    if (ws == nullptr || !aligned(ws, 256) || a.ld < (size_t)a.vocab) return MOE_ERR_INVALID_ARG;
+    if (a.rows > 0 && (a.x == nullptr || a.temperature == nullptr || !aligned(a.x, a.bf16 ? 2 : 4)))
+        return MOE_ERR_INVALID_ARG;
+    return ws_bytes < need ? MOE_ERR_WORKSPACE : MOE_OK;
+}
+
+}  // namespace
+
+moe_status moe_sample(const void *x, size_t ld, int dtype, int rows, int vocab, const float *temperature,
+                      const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *next,
+                      void *ws, size_t ws_bytes, moe_stream_t stream) {
+    SampleArgs a = {x,     ld,    dtype == MOE_PROB_BF16, rows, vocab, temperature, top_k, top_p, min_p, u, next,
+                    nullptr, 0, (StatusWord *)ws};
+    const moe_status s = sample_check(a, dtype, ws, ws_bytes);
+    if (s != MOE_OK) return s;
+    if (rows > 0 && (u == nullptr || next == nullptr)) return MOE_ERR_INVALID_ARG;
+    return cuda_status(launch_sample(a, (cudaStream_t)stream));
+}
+
+moe_status moe_sample_probs(const void *x, size_t ld, int dtype, int rows, int vocab, const float *temperature,
+                            const int32_t *top_k, const float *top_p, const float *min_p, void *probs, size_t ldp,
+                            void *ws, size_t ws_bytes, moe_stream_t stream) {
+    SampleArgs a = {x,     ld,    dtype == MOE_PROB_BF16, rows, vocab, temperature, top_k, top_p, min_p, nullptr, nullptr,
+                    probs, ldp, (StatusWord *)ws};
+    const moe_status s = sample_check(a, dtype, ws, ws_bytes);
+    if (s != MOE_OK) return s;
+    if (ldp < (size_t)vocab || (rows > 0 && (probs == nullptr || !aligned(probs, a.bf16 ? 2 : 4)))) return MOE_ERR_INVALID_ARG;
+    if (rows == 0) return MOE_OK;
+    return cuda_status(launch_sample(a, (cudaStream_t)stream));
 }
 
 moe_status moe_verify_workspace_size(int seqs, int rows, size_t *bytes) {

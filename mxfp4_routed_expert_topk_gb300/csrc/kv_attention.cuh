@@ -30,6 +30,8 @@
 // walk in the rows form); the rest are softmax warpgroups.
 #pragma once
 
+#include <type_traits>
+
 #include "kv_internal.cuh"
 #include "sm100_tensor.cuh"
 
@@ -57,6 +59,12 @@ struct AttnArgs {
     int over;       // what starting a unit costs, in tiles
     float scale2;   // scale * log2(e)
     float *part;    // partial results: 2 slots per worker of [rpt][dim] + [rpt][2]
+    // Attention with shared prefixes runs twice: over the groups' prefixes, every row of a group
+    // seeing all of it, and over what each sequence has of its own.
+    const int32_t *cu_groups, *prefix_len;
+    int groups;
+    bool prefix;    // which of the two
+    float *half, *half_lse;  // its results: outputs in fp32 [rows][heads_q][dim], log2 of the sums [rows][heads_q]
 };
 
 namespace {
@@ -70,6 +78,12 @@ struct Seg {
     int nt;                // the unit's tiles: more than `count` if other CTAs have some of them
     int64_t u0;            // position of its first tile on the line
 };
+// With shared prefixes: the first column of the table that its tokens lie in.
+struct SharedSeg : Seg {
+    int col0;
+};
+template <bool SHARED>
+using SegOf = std::conditional_t<SHARED, SharedSeg, Seg>;
 
 // One row of a row tile.
 struct RowInfo {
@@ -83,11 +97,80 @@ struct Item {
     int b, rt, row0, n, len, nt;
     bool ok;
 };
+struct SharedItem : Item {
+    int col0;
+};
+template <bool SHARED>
+using ItemOf = std::conditional_t<SHARED, SharedItem, Item>;
 
-__device__ __forceinline__ Item load_item(const AttnArgs &a, int it) {
-    Item x;
+// Tokens of a group's prefix that lie in whole pages.
+__device__ __forceinline__ int whole_pages(const AttnArgs &a, int g) {
+    return max(a.prefix_len[g], 0) & -a.k.kv.page;
+}
+
+// What load_item finds, where a group's prefix or a sequence's own tokens are the item.
+__device__ __forceinline__ void load_shared(const AttnArgs &a, SharedItem &x) {
+    const int64_t room = min((int64_t)a.k.table_width * a.k.kv.page, (int64_t)kMaxLen);
+    int hi, len;
+    if (a.prefix) {
+        const int g = x.b, g0 = a.cu_groups[g], g1 = a.cu_groups[g + 1];
+        // the groups take all sequences, in order
+        x.ok = g0 >= 0 && g0 <= g1 && g1 <= a.k.seqs && (g > 0 || g0 == 0) && (g + 1 < a.groups || g1 == a.k.seqs);
+        x.b = x.ok ? g0 : 0;
+        x.row0 = hi = 0;
+        if (x.ok) {
+            x.row0 = a.k.cu_rows[g0];
+            hi = a.k.cu_rows[g1];
+            if (x.row0 < 0 || x.row0 > hi || hi > a.k.rows) {
+                x.row0 = hi = 0;
+                x.ok = false;
+            }
+        }
+        x.n = hi - x.row0;
+        x.col0 = 0;
+        len = whole_pages(a, g);
+    } else {
+        x.ok = seq_rows(a.k.cu_rows, x.b, a.k.rows, x.row0, hi);
+        x.n = hi - x.row0;
+        int g = 0, end = a.groups;  // the last group that begins at or before the sequence
+        while (end - g > 1) {
+            const int mid = (g + end) >> 1;
+            if (a.cu_groups[mid] <= x.b)
+                g = mid;
+            else
+                end = mid;
+        }
+        const int before = (int)min((int64_t)whole_pages(a, g), room);
+        x.col0 = before / a.k.kv.page;
+        const int all = max(a.k.kv_len[x.b], 0);
+        if ((int64_t)all > room) x.ok = false;
+        len = (int)min((int64_t)all, room) - before;
+        if (x.n > 0 && before > 0 && len < x.n) x.ok = false;  // new rows stand in the prefix
+        len = max(len, 0);
+    }
+    if (x.n > a.k.max_rows) {
+        x.n = a.k.max_rows;
+        x.ok = false;
+    }
+    if (x.n > 0 && (int64_t)len > room) x.ok = false;
+    x.len = (int)min((int64_t)len, room);
+    x.nt = 0;
+    if (x.rt * a.rpt < x.n * a.group) {
+        const int last = a.nrt == 1 ? x.n - 1 : min(x.n - 1, ((x.rt + 1) * a.rpt - 1) / a.group);
+        const int see = a.prefix ? x.len : min(x.len, max(0, x.len - x.n + last + 1));
+        x.nt = max(1, (see + kTokens - 1) / kTokens);
+    }
+}
+
+template <bool SHARED>
+__device__ __forceinline__ ItemOf<SHARED> load_item(const AttnArgs &a, int it) {
+    ItemOf<SHARED> x;
     x.b = a.nrt == 1 ? it : it / a.nrt;
     x.rt = it - x.b * a.nrt;
+    if constexpr (SHARED) {
+        load_shared(a, x);
+        return x;
+    }
     int hi;
     x.ok = seq_rows(a.k.cu_rows, x.b, a.k.rows, x.row0, hi);
     x.n = hi - x.row0;
@@ -146,18 +229,19 @@ struct Line {
 __device__ __forceinline__ int unit_length(const AttnArgs &a, const Item &x) { return x.nt == 0 ? 0 : x.nt + a.over; }
 
 // A worker's share, and the item it starts in: its first position, number and description.
+template <bool SHARED>
 struct Start {
     int64_t lo, hi, first;
     int item;
-    Item x;
+    ItemOf<SHARED> x;
 };
 
 // Cut the line (all NT threads; `sums`: NT / 32 x 12 bytes of shared memory); the CTA's workers'
 // starts are in start[] after the caller's next barrier.
-template <int NT, int NW>
-__device__ __forceinline__ Line cut_line(const AttnArgs &a, int64_t *sums, Start *start) {
+template <int NT, int NW, bool SHARED>
+__device__ __forceinline__ Line cut_line(const AttnArgs &a, int64_t *sums, Start<SHARED> *start) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int items = a.k.seqs * a.nrt;
+    const int items = (SHARED && a.prefix ? a.groups : a.k.seqs) * a.nrt;
     const int per = (items + NT - 1) / NT;
     const int i0 = min(tid * per, items), i1 = min(i0 + per, items);
     // two rounds over the thread's items: their sum, then those that hold the workers' starts
@@ -170,7 +254,7 @@ __device__ __forceinline__ Line cut_line(const AttnArgs &a, int64_t *sums, Start
         bool good = true;
 #pragma unroll 1
         for (int i = i0; i < i1; i++) {
-            const Item x = load_item(a, i);
+            const ItemOf<SHARED> x = load_item<SHARED>(a, i);
             good &= x.ok;
             const int len = unit_length(a, x);
             longest = max(longest, len);
@@ -473,9 +557,11 @@ struct Pages {
         set_status(st, MOE_ERR_BAD_PAGE, 3);
         return n_pages;
     }
-    __device__ __forceinline__ void start(const AttnArgs &a, const Seg &g) {
+    template <typename SEG>
+    __device__ __forceinline__ void start(const AttnArgs &a, const SEG &g) {
         const int lane = threadIdx.x & 31, c0 = g.tile0 * kSlots;
         row = a.k.page_table + (size_t)g.b * a.k.table_width;
+        if constexpr (std::is_same_v<SEG, SharedSeg>) row += g.col0;
         st = a.k.st;
         n_pages = a.k.kv.n_pages;
         c1 = min((g.see_max + P - 1) / P, (g.tile0 + g.count) * kSlots);
@@ -537,7 +623,7 @@ struct Pages {
 // fetching an unrolled loop costs more than the latency that it hides (four passes in flight:
 // one sequence of 300 tokens 31 us in place of 27; all four words of a lane at once in the rows
 // form: 4 x 17 rows 325 us in place of 321).  kCopies: how often the rows stand in the tile.
-template <int D, int R, int kCopies = 1>
+template <int D, int R, bool SHARED, int kCopies = 1>
 __device__ __forceinline__ void load_queries(const AttnArgs &a, RowInfo *rows, unsigned char *q0, const Seg &g, int w,
                                              int nw) {
     constexpr int kLanes = D / 8, kPass = 32 / kLanes;
@@ -576,7 +662,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs &a, RowInfo *rows, u
         RowInfo ri;
         ri.row = g.row0 + qi;
         ri.head = g.head * a.group + hd;
-        ri.pos = g.len - g.n + qi;
+        ri.pos = SHARED && a.prefix ? g.len - 1 : g.len - g.n + qi;
         hd += kPass;
         load(r + kPass);
         // largest magnitude over finite values, two columns of them
@@ -626,18 +712,19 @@ __device__ __forceinline__ void load_queries(const AttnArgs &a, RowInfo *rows, u
 
 // ------------------------------------------------------------------- segments
 // Walks a worker's share.
+template <bool SHARED>
 struct Walk {
     const AttnArgs &a;
     int64_t w, hi, first;  // next position, end of the share; first position of the item
     int it;
-    Item x;
+    ItemOf<SHARED> x;
 
-    __device__ __forceinline__ Walk(const AttnArgs &a_, const Start &st)
+    __device__ __forceinline__ Walk(const AttnArgs &a_, const Start<SHARED> &st)
         : a(a_), w(st.lo), hi(st.hi), first(st.first), it(st.item), x(st.x) {}
 
     // The next segment; count 0 at the end of the share.
-    __device__ __forceinline__ Seg next() {
-        Seg g;
+    __device__ __forceinline__ SegOf<SHARED> next() {
+        SegOf<SHARED> g;
         g.count = 0;
 #pragma unroll 1
         while (w < hi) {  // the next positions with tiles
@@ -645,7 +732,7 @@ struct Walk {
             const int64_t units = (int64_t)len * a.k.kv.heads, local = w - first;
             if (local >= units) {
                 first += units;
-                x = load_item(a, ++it);
+                x = load_item<SHARED>(a, ++it);
                 continue;
             }
             // (a division of 32 bits wherever the numbers allow)
@@ -675,6 +762,10 @@ struct Walk {
             g.h0 = x.rt * a.rpt - q0 * a.group;
             g.see_all = min(x.len, max(0, x.len - x.n + q0 + 1));
             g.see_max = min(x.len, max(0, x.len - x.n + q1 + 1));
+            if constexpr (SHARED) {
+                if (a.prefix) g.see_all = g.see_max = x.len;
+                g.col0 = x.col0;
+            }
             g.nt = x.nt;
             g.u0 = first + (int64_t)g.head * unit_length(a, x) + a.over;
         }
@@ -723,19 +814,22 @@ __device__ __forceinline__ bool clean_values(unsigned char *tile, int tok, int t
 }
 
 // Code of value d of token t as it lies in the cache (0 if its page is outside).
-__device__ __forceinline__ const uint8_t *value_codes(const AttnArgs &a, int b, int head, int t) {
+template <typename SEG>
+__device__ __forceinline__ const uint8_t *value_codes(const AttnArgs &a, const SEG &g, int t) {
     const int P = a.k.kv.page;
-    const int page = a.k.page_table[(size_t)b * a.k.table_width + t / P];
+    const int32_t *row = a.k.page_table + (size_t)g.b * a.k.table_width;
+    if constexpr (std::is_same_v<SEG, SharedSeg>) row += g.col0;
+    const int page = row[t / P];
     if (page < 0 || page >= a.k.kv.n_pages) return nullptr;
-    return a.k.kv.codes(page, a.k.layer, 1, head) + (size_t)(t % P) * a.k.kv.dim;
+    return a.k.kv.codes(page, a.k.layer, 1, g.head) + (size_t)(t % P) * a.k.kv.dim;
 }
 
 // ---------------------------------------- units shared with other workers
 // All NT threads of a worker (tid: 0 .. NT-1), after its last segment: partial results are
 // published, and once every worker has done so this one joins its rows of the (at most two)
 // units it shares, `shared` of which stand in `list`.
-template <int D, int NT>
-__device__ __forceinline__ void join_role(const AttnArgs &a, const Line &line, int worker, const Seg *list, int shared,
+template <int D, int NT, bool SHARED>
+__device__ __forceinline__ void join_role(const AttnArgs &a, const Line &line, int worker, const SegOf<SHARED> *list, int shared,
                                           int tid, int bar_id, int *abort_flag) {
     StatusWord *st = a.k.st;
     const int lane = tid & 31, sw = tid >> 5;
@@ -831,6 +925,14 @@ __device__ __forceinline__ void join_role(const AttnArgs &a, const Line &line, i
             const int R = g.rt * a.rpt + r, qi = R / a.group, row = g.row0 + qi;
             const int hq = g.head * a.group + R - qi * a.group;
             const float inv = l == 0.f ? 0.f : 1.f / l;
+            if constexpr (SHARED) {
+                const size_t at = (size_t)row * a.k.heads_q + hq;
+                float *out = a.half + at * D + lane * V;
+#pragma unroll
+                for (int j = 0; j < V; j++) out[j] = acc[j] * inv;
+                if (lane == 0) a.half_lse[at] = l == 0.f ? -INFINITY : m + log2f(l);
+                continue;
+            }
             uint16_t *out = a.k.out + (size_t)row * a.k.ldo + (size_t)hq * D + lane * V;
 #pragma unroll
             for (int j = 0; j < V; j++) out[j] = __bfloat16_as_ushort(__float2bfloat16(acc[j] * inv));
@@ -849,8 +951,9 @@ __device__ __forceinline__ void join_role(const AttnArgs &a, const Line &line, i
 }  // namespace
 
 // The two forms, by the number of rows of a row tile: tokens along the tensor cores' M for
-// up to 16 rows (kv_attention.cu), rows along M for up to 128 (kv_attention_rows.cu).
+// up to 16 rows (kv_attention_few.cuh), rows along M for up to 128 (kv_attention_rows.cuh).
 cudaError_t launch_attention_rows(const CUtensorMap &tm, AttnArgs a, int sms, int smem_max, cudaStream_t st);
 cudaError_t set_wait_limit_kv_attention_rows(uint64_t ns);
+cudaError_t set_wait_limit_kv_attention_shared(uint64_t ns);
 
 }  // namespace moe

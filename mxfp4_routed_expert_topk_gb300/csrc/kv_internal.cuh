@@ -87,6 +87,53 @@ cudaError_t kv_attention_workspace_bytes(const KvView &kv, int max_rows, int hea
 cudaError_t launch_kv_attention(const KvAttentionArgs &a, void *ws, cudaStream_t st);
 cudaError_t set_wait_limit_kv_attention(uint64_t ns);
 
+// The same with the first prefix_len[g] tokens of the sequences cu_groups[g] .. shared.
+cudaError_t kv_attention_shared_workspace_bytes(const KvView &kv, int rows, int max_rows, int max_group_rows, int heads_q,
+                                                size_t *bytes);
+cudaError_t launch_kv_attention_shared(const KvAttentionArgs &k, const int32_t *cu_groups, const int32_t *prefix_len,
+                                       int groups, int max_group_rows, void *ws, cudaStream_t st);
+
+struct KvReserveArgs {
+    const int32_t *new_rows, *start;
+    int seqs;
+    int32_t *page_table;
+    int table_width;
+    int32_t *refs;
+    int n_pages, page;  // tokens of a page
+    int rows;           // room of the maps
+    int32_t *cu_rows, *kv_len, *row_seq, *row_pos;
+    int64_t *row_slot;
+    StatusWord *st;
+};
+constexpr int kMaxReserveSeqs = 16384;  // what a CTA keeps of each sequence fits its shared memory
+cudaError_t launch_kv_reserve(const KvReserveArgs &a, cudaStream_t st);
+
+struct KvReleaseArgs {
+    const int32_t *keep, *kv_len;
+    int seqs;
+    int32_t *page_table;
+    int table_width;
+    int32_t *refs;
+    int n_pages, page;
+    StatusWord *st;
+};
+cudaError_t launch_kv_release(const KvReleaseArgs &a, cudaStream_t st);
+
+struct SampleArgs {
+    const void *x;
+    size_t ld;
+    int bf16;  // element type of x and probs: 0 fp32, 1 bf16
+    int rows, vocab;
+    const float *temperature;
+    const int32_t *top_k;
+    const float *top_p, *min_p, *u;
+    int32_t *next;
+    void *probs;  // not null: the distribution in place of the draw
+    size_t ldp;
+    StatusWord *st;
+};
+cudaError_t launch_sample(const SampleArgs &a, cudaStream_t st);
+
 struct VerifyArgs {
     const void *p, *q;  // (greedy: p = the logits)
     size_t ldp, ldq;

@@ -17,7 +17,7 @@ OBJDIR = os.path.join(HERE, "_build")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC"]
 SOURCES = ["api.cu", "pool.cu", "route.cu", "route_static.cu", "decode.cu", "decode_fused.cu", "prefill.cu", "gemm.cu", "stream_pool.cu",
-           "kv_cache.cu", "kv_attention.cu", "kv_attention_rows.cu", "verify.cu"]
+           "kv_cache.cu", "kv_pages.cu", "kv_attention.cu", "kv_attention_rows.cu", "kv_attention_shared.cu", "verify.cu", "sample.cu"]
 
 
 def _nvcc() -> str:
