@@ -729,20 +729,25 @@ def moe_kv_reserve(new_rows: torch.Tensor, start: torch.Tensor, page_table: torc
     _need_index(start, seqs, "start")
     n_pages = refs.numel()
     _need_index(refs, n_pages, "refs")
-    outs = []
-    for t, n, dtype, name in ((cu_rows, seqs + 1, torch.int32, "cu_rows"), (kv_len, seqs, torch.int32, "kv_len"),
-                              (row_seq, rows, torch.int32, "row_seq"), (row_pos, rows, torch.int32, "row_pos"),
-                              (row_slot, rows, torch.int64, "row_slot")):
-        if t is None:
-            t = _empty((n,), dtype, page_table, stream)
-        elif not (t.is_cuda and t.dtype == dtype and t.is_contiguous() and t.numel() == n):
-            raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor of {n} values")
-        outs.append(t)
+    if stream is None and cu_rows is None and kv_len is None and row_seq is None and row_pos is None and row_slot is None:
+        i32, dev = torch.int32, page_table.device
+        outs = (torch.empty(seqs + 1, dtype=i32, device=dev), torch.empty_like(start), torch.empty(rows, dtype=i32, device=dev),
+                torch.empty(rows, dtype=i32, device=dev), torch.empty(rows, dtype=torch.int64, device=dev))
+    else:
+        outs = []
+        for t, n, dtype, name in ((cu_rows, seqs + 1, torch.int32, "cu_rows"), (kv_len, seqs, torch.int32, "kv_len"),
+                                  (row_seq, rows, torch.int32, "row_seq"), (row_pos, rows, torch.int32, "row_pos"),
+                                  (row_slot, rows, torch.int64, "row_slot")):
+            if t is None:
+                t = _empty((n,), dtype, page_table, stream)
+            elif not (t.is_cuda and t.dtype == dtype and t.is_contiguous() and t.numel() == n):
+                raise ValueError(f"{name}: expected a contiguous CUDA {dtype} tensor of {n} values")
+            outs.append(t)
     if ws is None:
         ws = _workspace_on(moe_kv_pages_workspace_size(seqs, n_pages), page_table, stream)
     _call(lib().moe_kv_reserve, "moe_kv_reserve", page_table.get_device(), stream, (new_rows, start, refs, *outs, ws),
           new_rows.data_ptr(), start.data_ptr(), seqs, page_table.data_ptr(), width, refs.data_ptr(), n_pages, page_tokens,
-          rows, *(t.data_ptr() for t in outs), ws.data_ptr(), ws.numel())
+          rows, *[t.data_ptr() for t in outs], ws.data_ptr(), ws.numel())
     return tuple(outs)
 
 

@@ -50,6 +50,10 @@ constexpr float kTop = 8.f;              // log2 of a tile's largest weight
 
 }  // namespace
 
+// The groups' prefixes, every row of a group seeing all of its; what each sequence has of its own; or
+// each sequence's prefix and own tokens together, nothing shared.
+enum SharedPart { kPrefixes, kOwn, kWhole };
+
 struct AttnArgs {
     KvAttentionArgs k;
     int group;      // query heads per key/value head
@@ -59,12 +63,13 @@ struct AttnArgs {
     int over;       // what starting a unit costs, in tiles
     float scale2;   // scale * log2(e)
     float *part;    // partial results: 2 slots per worker of [rpt][dim] + [rpt][2]
-    // Attention with shared prefixes runs twice: over the groups' prefixes, every row of a group
-    // seeing all of it, and over what each sequence has of its own.
+    // With shared prefixes: what a launch is about.
     const int32_t *cu_groups, *prefix_len;
-    int groups;
-    bool prefix;    // which of the two
-    float *half, *half_lse;  // its results: outputs in fp32 [rows][heads_q][dim], log2 of the sums [rows][heads_q]
+    int groups, group_rows;  // groups, and the most rows of one
+    SharedPart what;
+    // outputs over the prefixes in fp32 [rows][heads_q][dim], and the base-2 logarithms of their sums
+    // [rows][heads_q]: written over prefixes, and added to what is found over own tokens
+    float *half, *half_lse;
 };
 
 namespace {
@@ -78,9 +83,9 @@ struct Seg {
     int nt;                // the unit's tiles: more than `count` if other CTAs have some of them
     int64_t u0;            // position of its first tile on the line
 };
-// With shared prefixes: the first column of the table that its tokens lie in.
+// With shared prefixes: the columns of the prefix, and the sequence whose row of the table names them.
 struct SharedSeg : Seg {
-    int col0;
+    int col0, lead;
 };
 template <bool SHARED>
 using SegOf = std::conditional_t<SHARED, SharedSeg, Seg>;
@@ -98,7 +103,7 @@ struct Item {
     bool ok;
 };
 struct SharedItem : Item {
-    int col0;
+    int col0, lead;
 };
 template <bool SHARED>
 using ItemOf = std::conditional_t<SHARED, SharedItem, Item>;
@@ -112,7 +117,7 @@ __device__ __forceinline__ int whole_pages(const AttnArgs &a, int g) {
 __device__ __forceinline__ void load_shared(const AttnArgs &a, SharedItem &x) {
     const int64_t room = min((int64_t)a.k.table_width * a.k.kv.page, (int64_t)kMaxLen);
     int hi, len;
-    if (a.prefix) {
+    if (a.what == kPrefixes) {
         const int g = x.b, g0 = a.cu_groups[g], g1 = a.cu_groups[g + 1];
         // the groups take all sequences, in order
         x.ok = g0 >= 0 && g0 <= g1 && g1 <= a.k.seqs && (g > 0 || g0 == 0) && (g + 1 < a.groups || g1 == a.k.seqs);
@@ -128,6 +133,7 @@ __device__ __forceinline__ void load_shared(const AttnArgs &a, SharedItem &x) {
         }
         x.n = hi - x.row0;
         x.col0 = 0;
+        x.lead = x.b;
         len = whole_pages(a, g);
     } else {
         x.ok = seq_rows(a.k.cu_rows, x.b, a.k.rows, x.row0, hi);
@@ -140,13 +146,20 @@ __device__ __forceinline__ void load_shared(const AttnArgs &a, SharedItem &x) {
             else
                 end = mid;
         }
-        const int before = (int)min((int64_t)whole_pages(a, g), room);
+        // (over all, the groups are not looked at one by one)
+        const int g0 = a.cu_groups[g], g1 = a.cu_groups[g + 1];
+        if (a.what == kWhole && (!(g0 >= 0 && g0 <= x.b && x.b < g1 && g1 <= a.k.seqs) ||
+                                 a.k.cu_rows[g1] - a.k.cu_rows[g0] > a.group_rows))
+            x.ok = false;
+        const int prefix = whole_pages(a, g), before = (int)min((int64_t)prefix, room);
+        if (prefix > before) x.ok = false;
         x.col0 = before / a.k.kv.page;
+        x.lead = min(max(g0, 0), x.b);
         const int all = max(a.k.kv_len[x.b], 0);
         if ((int64_t)all > room) x.ok = false;
         len = (int)min((int64_t)all, room) - before;
         if (x.n > 0 && before > 0 && len < x.n) x.ok = false;  // new rows stand in the prefix
-        len = max(len, 0);
+        len = max(len, 0) + (a.what == kWhole ? before : 0);
     }
     if (x.n > a.k.max_rows) {
         x.n = a.k.max_rows;
@@ -157,7 +170,7 @@ __device__ __forceinline__ void load_shared(const AttnArgs &a, SharedItem &x) {
     x.nt = 0;
     if (x.rt * a.rpt < x.n * a.group) {
         const int last = a.nrt == 1 ? x.n - 1 : min(x.n - 1, ((x.rt + 1) * a.rpt - 1) / a.group);
-        const int see = a.prefix ? x.len : min(x.len, max(0, x.len - x.n + last + 1));
+        const int see = a.what == kPrefixes ? x.len : min(x.len, max(0, x.len - x.n + last + 1));
         x.nt = max(1, (see + kTokens - 1) / kTokens);
     }
 }
@@ -241,7 +254,7 @@ struct Start {
 template <int NT, int NW, bool SHARED>
 __device__ __forceinline__ Line cut_line(const AttnArgs &a, int64_t *sums, Start<SHARED> *start) {
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-    const int items = (SHARED && a.prefix ? a.groups : a.k.seqs) * a.nrt;
+    const int items = (SHARED && a.what == kPrefixes ? a.groups : a.k.seqs) * a.nrt;
     const int per = (items + NT - 1) / NT;
     const int i0 = min(tid * per, items), i1 = min(i0 + per, items);
     // two rounds over the thread's items: their sum, then those that hold the workers' starts
@@ -543,25 +556,30 @@ __device__ __forceinline__ void tma_load_3d_elected(void *dst, const CUtensorMap
 // The page numbers of a segment, 32 columns of the table at a time: lane l holds column
 // base + l, and the next 32.  One past the last page stands for a page outside the cache (it
 // lies outside the tensor: zeros arrive) and for columns past the sequence's end.
-template <int P>
+template <int P, bool SHARED>
 struct Pages {
     static constexpr int kSlots = kTokens / P;
     const int32_t *row;
     StatusWord *st;
     int n_pages, c1, at, left, id, id2, ahead;  // column of the tile in the 32; columns from the tile on
+    const int32_t *lead;  // (SHARED) the row that names the first `split` columns
+    int split;
 
     __device__ __forceinline__ int number(int col) const {
         if (col >= c1) return n_pages;
-        const int page = row[col];
+        const int page = SHARED && col < split ? lead[col] : row[col];
         if (page >= 0 && page < n_pages) return page;
         set_status(st, MOE_ERR_BAD_PAGE, 3);
         return n_pages;
     }
-    template <typename SEG>
-    __device__ __forceinline__ void start(const AttnArgs &a, const SEG &g) {
+    __device__ __forceinline__ void start(const AttnArgs &a, const SegOf<SHARED> &g) {
         const int lane = threadIdx.x & 31, c0 = g.tile0 * kSlots;
         row = a.k.page_table + (size_t)g.b * a.k.table_width;
-        if constexpr (std::is_same_v<SEG, SharedSeg>) row += g.col0;
+        if constexpr (SHARED) {
+            if (a.what == kOwn) row += g.col0;
+            lead = a.k.page_table + (size_t)g.lead * a.k.table_width;
+            split = a.what == kWhole ? g.col0 : 0;
+        }
         st = a.k.st;
         n_pages = a.k.kv.n_pages;
         c1 = min((g.see_max + P - 1) / P, (g.tile0 + g.count) * kSlots);
@@ -662,7 +680,7 @@ __device__ __forceinline__ void load_queries(const AttnArgs &a, RowInfo *rows, u
         RowInfo ri;
         ri.row = g.row0 + qi;
         ri.head = g.head * a.group + hd;
-        ri.pos = SHARED && a.prefix ? g.len - 1 : g.len - g.n + qi;
+        ri.pos = SHARED && a.what == kPrefixes ? g.len - 1 : g.len - g.n + qi;
         hd += kPass;
         load(r + kPass);
         // largest magnitude over finite values, two columns of them
@@ -763,8 +781,9 @@ struct Walk {
             g.see_all = min(x.len, max(0, x.len - x.n + q0 + 1));
             g.see_max = min(x.len, max(0, x.len - x.n + q1 + 1));
             if constexpr (SHARED) {
-                if (a.prefix) g.see_all = g.see_max = x.len;
+                if (a.what == kPrefixes) g.see_all = g.see_max = x.len;
                 g.col0 = x.col0;
+                g.lead = x.lead;
             }
             g.nt = x.nt;
             g.u0 = first + (int64_t)g.head * unit_length(a, x) + a.over;
@@ -818,11 +837,30 @@ template <typename SEG>
 __device__ __forceinline__ const uint8_t *value_codes(const AttnArgs &a, const SEG &g, int t) {
     const int P = a.k.kv.page;
     const int32_t *row = a.k.page_table + (size_t)g.b * a.k.table_width;
-    if constexpr (std::is_same_v<SEG, SharedSeg>) row += g.col0;
+    if constexpr (std::is_same_v<SEG, SharedSeg>) {
+        if (a.what == kOwn) row += g.col0;
+        if (a.what == kWhole && t / P < g.col0) row = a.k.page_table + (size_t)g.lead * a.k.table_width;
+    }
     const int page = row[t / P];
     if (page < 0 || page >= a.k.kv.n_pages) return nullptr;
     return a.k.kv.codes(page, a.k.layer, 1, g.head) + (size_t)(t % P) * a.k.kv.dim;
 }
+
+// A row's result over its own tokens (e: the base-2 logarithm of its sum) with that over the prefix of
+// its group.
+struct Halves {
+    float own, prefix, lse;  // factors of the two; the logarithm of the whole sum
+    __device__ __forceinline__ Halves(const AttnArgs &a, size_t at, float e) {
+        // (a half that saw nothing has 0 and -infinity; NaN stays)
+        const float p = a.what == kOwn ? __ldg(a.half_lse + at) : -INFINITY, m = fmaxf(e, p);
+        const float we = e == -INFINITY ? 0.f : ex2(e - m), wp = p == -INFINITY ? 0.f : ex2(p - m);
+        const float l = we + wp, inv = l == 0.f ? 0.f : 1.f / l;
+        own = we * inv;
+        prefix = wp * inv;
+        lse = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+    }
+    __device__ __forceinline__ float add(float o, float p) const { return fmaf(o, own, p * prefix); }
+};
 
 // ---------------------------------------- units shared with other workers
 // All NT threads of a worker (tid: 0 .. NT-1), after its last segment: partial results are
@@ -925,19 +963,28 @@ __device__ __forceinline__ void join_role(const AttnArgs &a, const Line &line, i
             const int R = g.rt * a.rpt + r, qi = R / a.group, row = g.row0 + qi;
             const int hq = g.head * a.group + R - qi * a.group;
             const float inv = l == 0.f ? 0.f : 1.f / l;
+            uint16_t *out = a.k.out + (size_t)row * a.k.ldo + (size_t)hq * D + lane * V;
             if constexpr (SHARED) {
                 const size_t at = (size_t)row * a.k.heads_q + hq;
-                float *out = a.half + at * D + lane * V;
+                float *half = a.half + at * D + lane * V;
+                const float e = l == 0.f ? -INFINITY : m + log2f(l);
+                if (a.what == kPrefixes) {
 #pragma unroll
-                for (int j = 0; j < V; j++) out[j] = acc[j] * inv;
-                if (lane == 0) a.half_lse[at] = l == 0.f ? -INFINITY : m + log2f(l);
-                continue;
+                    for (int j = 0; j < V; j++) half[j] = acc[j] * inv;
+                    if (lane == 0) a.half_lse[at] = e;
+                    continue;
+                }
+                const Halves h(a, at, e);
+#pragma unroll
+                for (int j = 0; j < V; j++)
+                    out[j] = __bfloat16_as_ushort(__float2bfloat16(h.add(acc[j] * inv, a.what == kOwn ? __ldg(half + j) : 0.f)));
+                if (a.k.lse != nullptr && lane == 0) a.k.lse[at] = h.lse;
+            } else {
+#pragma unroll
+                for (int j = 0; j < V; j++) out[j] = __bfloat16_as_ushort(__float2bfloat16(acc[j] * inv));
+                if (a.k.lse != nullptr && lane == 0)
+                    a.k.lse[(size_t)row * a.k.heads_q + hq] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
             }
-            uint16_t *out = a.k.out + (size_t)row * a.k.ldo + (size_t)hq * D + lane * V;
-#pragma unroll
-            for (int j = 0; j < V; j++) out[j] = __bfloat16_as_ushort(__float2bfloat16(acc[j] * inv));
-            if (a.k.lse != nullptr && lane == 0)
-                a.k.lse[(size_t)row * a.k.heads_q + hq] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
         }
     }
     named_barrier(bar_id, NT);

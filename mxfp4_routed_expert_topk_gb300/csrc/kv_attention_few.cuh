@@ -88,7 +88,7 @@ __device__ __forceinline__ void feed(const AttnArgs &a, const CUtensorMap *tm, u
     float *scales = reinterpret_cast<float *>(smem + F.scales) + w * kStages * 2 * kMaxSlots;
     SegOf<SHARED> *ring = reinterpret_cast<SegOf<SHARED> *>(smem + F.seg) + 2 * w;
     Walk<SHARED> W(a, start);
-    Pages<P> pg;
+    Pages<P, SHARED> pg;
     Watch eye = lane == 0 ? Watch{B.empty(0), kStages, 0, 1u}
                 : lane == 1 ? Watch{B.q_free(), 1, 0, 1u}
                             : Watch{B.seg_empty(0), 2, 0, 1u};
@@ -475,21 +475,40 @@ __global__ void __launch_bounds__(kFewThreads, 1) kv_attention_few_kernel(const 
             named_barrier(bar, 128);
             const float l = (lsum[row] + lsum[R + row]) + (lsum[2 * R + row] + lsum[3 * R + row]);
             const bool part_of = count < sg->nt;
+            float lse_shared = 0.f;
             float *part = part_of ? a.part + (size_t)(2 * worker + (tile0 == 0 ? 1 : 0)) * slot_floats : nullptr;
             // (a row that saw nothing is told by its sum; NaN stays)
             ab[row].y = part_of ? 1.f : l == 0.f ? 0.f : 1.f / l;
             const bool live = *(volatile int *)abort_flag == 0;
+            if constexpr (SHARED) {
+                if (!part_of && a.what != kPrefixes && rows[row].row >= 0) {
+                    const Halves h(a, (size_t)rows[row].row * a.k.heads_q + rows[row].head,
+                                   l == 0.f ? -INFINITY : m_run + log2f(l));
+                    ab[row] = make_float2(h.prefix, h.own * (l == 0.f ? 0.f : 1.f / l));
+                    lse_shared = h.lse;
+                }
+            }
             if (ew == 0 && (lane & 1) == 0 && rows[row].row >= 0 && live) {  // one lane per row
                 if (part_of)
                     *reinterpret_cast<float2 *>(part + (size_t)R * D + 2 * row) = make_float2(m_run, l);
-                else if constexpr (SHARED)
+                else if (SHARED && a.what == kPrefixes)
                     a.half_lse[(size_t)rows[row].row * a.k.heads_q + rows[row].head] = l == 0.f ? -INFINITY : m_run + log2f(l);
+                else if (SHARED && a.k.lse != nullptr)
+                    a.k.lse[(size_t)rows[row].row * a.k.heads_q + rows[row].head] = lse_shared;
                 else if (a.k.lse != nullptr)
                     a.k.lse[(size_t)rows[row].row * a.k.heads_q + rows[row].head] =
                         l == 0.f ? -INFINITY : kLn2 * (m_run + log2f(l));
             }
             __syncwarp();
             if (dlive && live) {
+                float half[R];  // (loads in flight together)
+                if (SHARED && a.what == kOwn && !part_of) {
+#pragma unroll
+                    for (int i = 0; i < R; i++) {
+                        const RowInfo ri = rows[i];
+                        half[i] = ri.row < 0 ? 0.f : __ldg(a.half + ((size_t)ri.row * a.k.heads_q + ri.head) * D + dcol);
+                    }
+                }
 #pragma unroll
                 for (int i = 0; i < R; i++) {
                     const RowInfo ri = rows[i];
@@ -497,8 +516,11 @@ __global__ void __launch_bounds__(kFewThreads, 1) kv_attention_few_kernel(const 
                     const float y = o[i] * ab[i].y;
                     if (part_of)
                         part[(size_t)i * D + dcol] = y;
-                    else if constexpr (SHARED)
+                    else if (SHARED && a.what == kPrefixes)
                         a.half[((size_t)ri.row * a.k.heads_q + ri.head) * D + dcol] = y;
+                    else if (SHARED && a.what == kOwn)
+                        a.k.out[(size_t)ri.row * a.k.ldo + (size_t)ri.head * D + dcol] = __bfloat16_as_ushort(__float2bfloat16(
+                            fmaf(ab[i].x, half[i], y)));
                     else
                         a.k.out[(size_t)ri.row * a.k.ldo + (size_t)ri.head * D + dcol] =
                             __bfloat16_as_ushort(__float2bfloat16(y));

@@ -105,7 +105,7 @@ __device__ __forceinline__ void copy_pages(const AttnArgs &a, const CUtensorMap 
     unsigned char *ring = smem + (SIDE ? L.v : L.k);
     const uint32_t elected = elect_one();
     Ring R;
-    Pages<P> pg;
+    Pages<P, SHARED> pg;
     int issued = 0;
     bool run = true;
 #pragma unroll 1
@@ -736,7 +736,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                     for (int i = 0; i < D; i += 4)
                         *reinterpret_cast<float4 *>(d + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                     *reinterpret_cast<float2 *>(part + (size_t)a.rpt * D + 2 * row) = make_float2(m_run, l_run);
-                } else if constexpr (SHARED) {
+                } else if (SHARED && a.what == kPrefixes) {
                     const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
                     const size_t at = (size_t)ri.row * a.k.heads_q + ri.head;
                     float *d = a.half + at * D;
@@ -746,7 +746,26 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                             make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
                     a.half_lse[at] = l_run == 0.f ? -INFINITY : m_run + log2f(l_run);
                 } else {
-                    const float inv = l_run == 0.f ? 0.f : 1.f / l_run;  // (sum 0: it saw nothing; NaN stays)
+                    float inv = l_run == 0.f ? 0.f : 1.f / l_run;  // (sum 0: it saw nothing; NaN stays)
+                    float lse = 0.f;
+                    if constexpr (SHARED) {
+                        const size_t at = (size_t)ri.row * a.k.heads_q + ri.head;
+                        const Halves h(a, at, l_run == 0.f ? -INFINITY : m_run + log2f(l_run));
+                        lse = h.lse;
+                        inv *= h.own;
+                        if (a.what == kOwn) {
+                            const float4 *p = reinterpret_cast<const float4 *>(a.half + at * D);
+#pragma unroll
+                            for (int i = 0; i < D; i += 4) {
+                                const float4 x = __ldg(p + i / 4);
+                                o[i] = fmaf(o[i], inv, x.x * h.prefix);
+                                o[i + 1] = fmaf(o[i + 1], inv, x.y * h.prefix);
+                                o[i + 2] = fmaf(o[i + 2], inv, x.z * h.prefix);
+                                o[i + 3] = fmaf(o[i + 3], inv, x.w * h.prefix);
+                            }
+                            inv = 1.f;
+                        }
+                    }
                     uint16_t *d = a.k.out + (size_t)ri.row * a.k.ldo + (size_t)ri.head * D;
 #pragma unroll
                     for (int i = 0; i < D; i += 8) {
@@ -758,7 +777,9 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                         }
                         *reinterpret_cast<uint4 *>(d + i) = make_uint4(b[0], b[1], b[2], b[3]);
                     }
-                    if (a.k.lse != nullptr)
+                    if (SHARED && a.k.lse != nullptr)
+                        a.k.lse[(size_t)ri.row * a.k.heads_q + ri.head] = lse;
+                    else if (a.k.lse != nullptr)
                         a.k.lse[(size_t)ri.row * a.k.heads_q + ri.head] =
                             l_run == 0.f ? -INFINITY : kLn2 * (m_run + log2f(l_run));
                 }

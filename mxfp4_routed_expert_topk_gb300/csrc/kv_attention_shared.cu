@@ -7,8 +7,11 @@
 //
 // with o1, o2 its attention over the prefix and over the sequence's own tokens and e1, e2 the base-2
 // logarithms of their sums.  The first is one problem per group, with all of the group's rows in
-// row tiles that read the prefix once for up to 128 of them; the second is one per sequence.  Both are
-// the cache attention's kernels with other lengths and tables.
+// row tiles that read the prefix once for up to 128 of them, and its results go to the workspace in
+// fp32; the second is one per sequence and adds the first when it writes its own.  Both are the cache
+// attention's kernels with other lengths and tables.
+//
+// Small batches run once, each sequence over its prefix and its own tokens, as a second launch costs 15 us.
 #include <algorithm>
 
 #include "kv_attention_few.cuh"
@@ -17,37 +20,7 @@
 namespace moe {
 namespace {
 
-constexpr int kMergeWarps = 8;
-
-// A warp per (row, query head).
-template <int D>
-__global__ void __launch_bounds__(32 * kMergeWarps) kv_attention_merge_kernel(const KvAttentionArgs k, const float *half,
-                                                                               const float *half_lse) {
-    const int lane = threadIdx.x & 31;
-    const int64_t pairs = (int64_t)k.rows * k.heads_q;
-    const int64_t at = (int64_t)blockIdx.x * kMergeWarps + threadIdx.x / 32;
-    if (at >= pairs) return;
-    const int row = (int)(at / k.heads_q), head = (int)(at - (int64_t)row * k.heads_q);
-    if (row < k.cu_rows[0] || row >= k.cu_rows[k.seqs]) return;  // no sequence takes it
-    constexpr int V = D / 32;
-    float x[2][V], e[2];
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-        const float *o = half + (size_t)(i * pairs + at) * D + lane * V;
-        e[i] = half_lse[i * pairs + at];
-#pragma unroll
-        for (int j = 0; j < V; j++) x[i][j] = o[j];
-    }
-    // (a half that saw nothing has 0 and -infinity; NaN stays)
-    const float m = fmaxf(e[0], e[1]);
-    const float w0 = e[0] == -INFINITY ? 0.f : ex2(e[0] - m), w1 = e[1] == -INFINITY ? 0.f : ex2(e[1] - m);
-    const float l = w0 + w1, inv = l == 0.f ? 0.f : 1.f / l;
-    uint16_t *out = k.out + (size_t)row * k.ldo + (size_t)head * D + lane * V;
-#pragma unroll
-    for (int j = 0; j < V; j++)
-        out[j] = __bfloat16_as_ushort(__float2bfloat16((fmaf(x[0][j], w0, x[1][j] * w1)) * inv));
-    if (k.lse != nullptr && lane == 0) k.lse[at] = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
-}
+constexpr int kSmall = 8;  // tiles per SM
 
 cudaError_t run(const AttnSetup &s, cudaStream_t st) {
     if (s.a.rpt > kFewRows) return launch_rows<true>(s.tm, s.a, s.sms, s.smem_max, st);
@@ -63,7 +36,7 @@ cudaError_t kv_attention_shared_workspace_bytes(const KvView &kv, int rows, int 
     size_t own = 0, prefix = 0;
     cudaError_t e = part_bytes(kv, max_rows, heads_q, &own);
     if (e == cudaSuccess) e = part_bytes(kv, max_group_rows, heads_q, &prefix);
-    *bytes = sizeof(StatusWord) + std::max(own, prefix) + (size_t)2 * rows * heads_q * (kv.dim + 1) * sizeof(float);
+    *bytes = sizeof(StatusWord) + std::max(own, prefix) + (size_t)rows * heads_q * (kv.dim + 1) * sizeof(float);
     return e;
 }
 
@@ -75,28 +48,25 @@ cudaError_t launch_kv_attention_shared(const KvAttentionArgs &k, const int32_t *
     size_t own = 0, prefix = 0;
     if ((e = part_bytes(k.kv, k.max_rows, k.heads_q, &own)) != cudaSuccess) return e;
     if ((e = part_bytes(k.kv, max_group_rows, k.heads_q, &prefix)) != cudaSuccess) return e;
-    const size_t pairs = (size_t)k.rows * k.heads_q;
-    float *half = reinterpret_cast<float *>((char *)ws + sizeof(StatusWord) + std::max(own, prefix));
-    float *half_lse = half + 2 * pairs * k.kv.dim;
+    s.a.half = reinterpret_cast<float *>((char *)ws + sizeof(StatusWord) + std::max(own, prefix));
+    s.a.half_lse = s.a.half + (size_t)k.rows * k.heads_q * k.kv.dim;
     s.a.cu_groups = cu_groups;
     s.a.prefix_len = prefix_len;
     s.a.groups = groups;
+    s.a.group_rows = max_group_rows;
     TraceScope trace_scope("kv_attention_shared", st);
-    for (int i = 0; i < 2; i++) {
-        AttnSetup t = s;
-        t.a.prefix = i == 0;
-        t.a.k.max_rows = i == 0 ? max_group_rows : k.max_rows;
-        t.a.half = half + i * pairs * k.kv.dim;
-        t.a.half_lse = half_lse + i * pairs;
-        if ((e = set_tiles(t.a, i == 0 ? groups : k.seqs)) != cudaSuccess) return e;
-        if ((e = run(t, st)) != cudaSuccess) return e;
+    // (lengths are known on the device alone: by the most tiles that the tables have room for)
+    const int64_t tiles = (((int64_t)k.table_width * k.kv.page + kTokens - 1) / kTokens) * k.seqs * s.a.nrt * k.kv.heads;
+    if (tiles <= (int64_t)kSmall * s.sms) {
+        s.a.what = kWhole;
+        return run(s, st);
     }
-    const dim3 grid((unsigned)((pairs + kMergeWarps - 1) / kMergeWarps)), block(32 * kMergeWarps);
-    if (k.kv.dim == 128)
-        kv_attention_merge_kernel<128><<<grid, block, 0, st>>>(k, half, half_lse);
-    else
-        kv_attention_merge_kernel<64><<<grid, block, 0, st>>>(k, half, half_lse);
-    return cudaGetLastError();
+    AttnSetup t = s;
+    t.a.what = kPrefixes;
+    t.a.k.max_rows = max_group_rows;
+    if ((e = set_tiles(t.a, groups)) != cudaSuccess || (e = run(t, st)) != cudaSuccess) return e;
+    s.a.what = kOwn;
+    return run(s, st);
 }
 
 }  // namespace moe

@@ -6,9 +6,14 @@
 //
 // Reserving is one cluster of CTAs.  Every CTA sums the sequences' needs by itself (a scan over the
 // block) and counts the free pages of its part of the pool; the counts are exchanged through
-// distributed shared memory, and the CTA that finds free page number k writes it into the place
-// that is k-th in the line of (sequence, column).  Nothing is written before the call is known to
-// succeed, so a call that cannot be served changes nothing.
+// distributed shared memory, so that every warp knows the numbers of its free pages among all.  The
+// lowest ones lie in few CTAs' parts: those hand them to all CTAs' shared memory, and every thread
+// then looks up one or two places in the line of (sequence, column) for its pages.  Nothing is written
+// before the call is known to succeed, so a call that cannot be served changes nothing.
+//
+// What bounds it is the chain: 64 sequences of which few need a page take 6 us (three loads one after
+// the other, sums, the cluster's barriers).  512 sequences that take TTT pages of 400000 and map 77000
+// rows take MMM us; with the places looked up by the warps that find the pages 34.
 #include <algorithm>
 
 #include "kv_internal.cuh"
@@ -20,6 +25,8 @@ namespace {
 constexpr int kThreads = 1024;
 constexpr int kWarps = kThreads / 32;
 constexpr int kCluster = 8;
+constexpr int kSteps = 16;   // pieces of a warp's pages
+constexpr int kHand = 4096;  // pages that a CTA is handed at a time
 
 struct Sums {
     int64_t pages, rows;
@@ -64,7 +71,8 @@ __global__ void __launch_bounds__(kThreads, 1) kv_reserve_kernel(const KvReserve
     extern __shared__ int s_dyn[];
     int *s_page = s_dyn, *s_row = s_page + a.seqs + 1, *s_start = s_row + a.seqs + 1;  // pages, rows before a sequence
     __shared__ Sums s_warp[kWarps];
-    __shared__ int s_free[kWarps], s_cta[kCluster];
+    __shared__ int s_free[kSteps * kWarps], s_sum[kWarps], s_cta[kCluster], s_hand[kHand];
+    const int shift = 31 - __clz(a.page);
     const int rank = (int)cluster_ctarank(), tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     cluster_arrive();  // waited for before the first remote store: by then every CTA has started
 
@@ -116,41 +124,69 @@ __global__ void __launch_bounds__(kThreads, 1) kv_reserve_kernel(const KvReserve
     const int need = (int)total.pages;
     const bool search = code == MOE_OK && need > 0;  // (the same in every CTA)
 
-    // this warp's pages: consecutive ones, 4 to a lane
-    const int part = ((a.n_pages + kCluster - 1) / kCluster + 127) / 128 * 128;
-    const int lo = min((int64_t)rank * part, (int64_t)a.n_pages), hi = min((int64_t)lo + part, (int64_t)a.n_pages);
-    const int chunk = (part / 128 + kWarps - 1) / kWarps * 128;
-    const int w0 = min(lo + warp * chunk, hi), w1 = min(w0 + chunk, hi);
+    // The CTA's pages: kSteps times kWarps pieces in a row, a warp's pages 4 to a lane.
+    const int piece = ((a.n_pages + kCluster * kSteps * kWarps - 1) / (kCluster * kSteps * kWarps) + 127) / 128 * 128;
     const bool vec = ((uintptr_t)a.refs & 15u) == 0;
-    auto free_of = [&](int p) -> uint32_t {  // of pages p .. p + 3, a bit each
+    auto begin = [&](int step) {  // of this warp's piece
+        return (int)min((int64_t)((rank * kSteps + step) * kWarps + warp) * piece, (int64_t)a.n_pages);
+    };
+    auto free_of = [&](int p, int end) -> uint32_t {  // of pages p .. p + 3, a bit each
         uint32_t m = 0;
-        if (vec && p + 4 <= w1) {
+        if (vec && p + 4 <= end) {
             const int4 r = __ldcg(reinterpret_cast<const int4 *>(a.refs + p));
             m = (r.x == 0 ? 1u : 0u) | (r.y == 0 ? 2u : 0u) | (r.z == 0 ? 4u : 0u) | (r.w == 0 ? 8u : 0u);
         } else {
             for (int k = 0; k < 4; k++)
-                if (p + k < w1 && __ldcg(a.refs + p + k) == 0) m |= 1u << k;
+                if (p + k < end && __ldcg(a.refs + p + k) == 0) m |= 1u << k;
         }
         return m;
     };
-    int found = 0;
-    if (search)
-#pragma unroll 4
-        for (int p = w0 + 4 * lane; p < w1; p += 128) found += __popc(free_of(p));
-    found = __reduce_add_sync(0xffffffffu, found);
-    if (lane == 0) s_free[warp] = found;
+    if (search) {
+        constexpr int kSide = 8;  // pieces whose loads are in flight together
+        for (int s0 = 0; s0 < kSteps; s0 += kSide) {
+            int found[kSide];
+#pragma unroll
+            for (int j = 0; j < kSide; j++) found[j] = 0;
+            for (int i = 4 * lane; i - 4 * lane < piece; i += 128) {
+#pragma unroll
+                for (int j = 0; j < kSide; j++) {
+                    const int p = begin(s0 + j) + i, end = min(begin(s0 + j) + piece, a.n_pages);
+                    found[j] += p < end ? __popc(free_of(p, end)) : 0;
+                }
+            }
+#pragma unroll
+            for (int j = 0; j < kSide; j++) {
+                const int sum = __reduce_add_sync(0xffffffffu, found[j]);
+                if (lane == 0) s_free[(s0 + j) * kWarps + warp] = sum;
+            }
+        }
+    }
     __syncthreads();
-    int cta = 0, at = 0;
-    for (int w = 0; w < kWarps; w++) {
-        if (w < warp) at += s_free[w];
-        cta += s_free[w];
+    int cta = 0;
+    if (search) {  // running sums of the pieces' free pages
+        static_assert(kSteps * kWarps <= kThreads, "a thread per piece");
+        const int mine = tid < kSteps * kWarps ? s_free[tid] : 0;
+        int upto = mine;
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int o = __shfl_up_sync(0xffffffffu, upto, d);
+            if (lane >= d) upto += o;
+        }
+        if (lane == 31) s_sum[warp] = upto;
+        __syncthreads();
+        upto -= mine;
+        for (int w = 0; w < kSteps; w++) {
+            if (w < warp) upto += s_sum[w];
+            cta += s_sum[w];
+        }
+        if (tid < kSteps * kWarps) s_free[tid] = upto;
     }
     cluster_wait();
     if (tid < kCluster) store_cluster_i32(s_cta + rank, (uint32_t)tid, cta);
     cluster_sync();  // the counts are there; every check has been made
-    int all = 0;
+    int all = 0, first = 0;  // free pages; those of the CTAs before this one
     for (int k = 0; k < kCluster; k++) {
-        if (k < rank) at += s_cta[k];
+        if (k < rank) first += s_cta[k];
         all += s_cta[k];
     }
     if (search && all < need) code = MOE_ERR_NO_PAGE;
@@ -162,39 +198,81 @@ __global__ void __launch_bounds__(kThreads, 1) kv_reserve_kernel(const KvReserve
     }
     if (code != MOE_OK) return;
     if (search) {
-        for (int p0 = w0; p0 < w1 && at < need; p0 += 128) {
-            const int p = p0 + 4 * lane;
-            const uint32_t m = p < w1 ? free_of(p) : 0u;
-            int upto = __popc(m);
-            const int own = upto;
+        for (int from = 0; from < need; from += kCluster * kHand) {
+            const int to = min(from + kCluster * kHand, need);
+            if (from > 0) cluster_sync();  // (those of the round before are taken)
+            for (int step = 0; step < kSteps; step++) {
+                // this piece's first free page among all (those before `from` are taken, and not free now)
+                int at = max(first + s_free[step * kWarps + warp], from);
+                if (at >= to) break;
+                const int end = min(begin(step) + piece, a.n_pages);
+                for (int p = begin(step) + 4 * lane; p - 4 * lane < end && at < to; p += 128) {
+                    const uint32_t m = p < end ? free_of(p, end) : 0u;
+                    int upto = __popc(m);
+                    const int own = upto;
 #pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, upto, d);
-                if (lane >= d) upto += o;
-            }
-            int k = at + upto - own;
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const int o = __shfl_up_sync(0xffffffffu, upto, d);
+                        if (lane >= d) upto += o;
+                    }
+                    int k = at + upto - own;
+                    at += __shfl_sync(0xffffffffu, upto, 31);
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                if ((m >> i & 1u) == 0u) continue;
-                if (k < need) {
-                    const int b = place_of(s_page, a.seqs, k);
-                    const int col = (s_start[b] + a.page - 1) / a.page + k - s_page[b];
-                    a.refs[p + i] = 1;
-                    a.page_table[(size_t)b * a.table_width + col] = p + i;
+                    for (int i = 0; i < 4; i++) {
+                        if ((m >> i & 1u) == 0u) continue;
+                        const int h = k - from;
+                        if (k < to) store_cluster_i32(s_hand + h % kHand, (uint32_t)(h / kHand), p + i);
+                        k++;
+                    }
                 }
-                k++;
             }
-            at += __shfl_sync(0xffffffffu, upto, 31);
+            cluster_sync();
+            for (int i = tid; i < kHand; i += kThreads) {
+                const int k = from + rank * kHand + i;
+                if (k >= to) break;
+                const int b = place_of(s_page, a.seqs, k), page = s_hand[i];
+                const int col = ((s_start[b] + a.page - 1) >> shift) + k - s_page[b];
+                a.refs[page] = 1;
+                a.page_table[(size_t)b * a.table_width + col] = page;
+            }
         }
         cluster_sync();  // the table is complete
     }
     if (a.row_seq == nullptr && a.row_pos == nullptr && a.row_slot == nullptr) return;
-    for (int r = rank * kThreads + tid; r < (int)total.rows; r += kCluster * kThreads) {
-        const int b = place_of(s_row, a.seqs, r), pos = s_start[b] + r - s_row[b];
-        if (a.row_seq != nullptr) a.row_seq[r] = b;
-        if (a.row_pos != nullptr) a.row_pos[r] = pos;
-        if (a.row_slot != nullptr)
-            a.row_slot[r] = (int64_t)__ldcg(a.page_table + (size_t)b * a.table_width + pos / a.page) * a.page + pos % a.page;
+    // four rows of a thread at a time: their searches and loads go side by side
+    constexpr int kSide = 4, kStep = kCluster * kThreads;
+    for (int r0 = rank * kThreads + tid; r0 < (int)total.rows; r0 += kSide * kStep) {
+        int lo[kSide], hi[kSide];
+#pragma unroll
+        for (int j = 0; j < kSide; j++) lo[j] = 0, hi[j] = a.seqs;
+        for (int n = a.seqs; n > 1; n = (n + 1) >> 1) {
+#pragma unroll
+            for (int j = 0; j < kSide; j++) {
+                const int mid = (lo[j] + hi[j]) >> 1;
+                if (hi[j] - lo[j] <= 1) continue;
+                if (s_row[mid] <= r0 + j * kStep)
+                    lo[j] = mid;
+                else
+                    hi[j] = mid;
+            }
+        }
+        int pos[kSide], page[kSide];
+#pragma unroll
+        for (int j = 0; j < kSide; j++) {
+            const int r = r0 + j * kStep;
+            pos[j] = s_start[lo[j]] + r - s_row[lo[j]];
+            page[j] = 0;
+            if (r < (int)total.rows && a.row_slot != nullptr)
+                page[j] = __ldcg(a.page_table + (size_t)lo[j] * a.table_width + (pos[j] >> shift));
+        }
+#pragma unroll
+        for (int j = 0; j < kSide; j++) {
+            const int r = r0 + j * kStep;
+            if (r >= (int)total.rows) break;
+            if (a.row_seq != nullptr) a.row_seq[r] = lo[j];
+            if (a.row_pos != nullptr) a.row_pos[r] = pos[j];
+            if (a.row_slot != nullptr) a.row_slot[r] = ((int64_t)page[j] << shift) + (pos[j] & (a.page - 1));
+        }
     }
 }
 

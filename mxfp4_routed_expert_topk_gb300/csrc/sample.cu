@@ -768,6 +768,7 @@ struct Sampler {
             }
             return;
         }
+        const float low_ = low;  // (before infinities are put in place)
         W.m = key_value(key);
         W.c = fminf(__fdiv_rn(0x1.715476p+0f, T), 3.4028235e38f);
         infinite = W.m == INFINITY;
@@ -785,7 +786,9 @@ struct Sampler {
             if (a.vocab <= kList || low > kNone) {
                 // the tokens from `low` on, among which the first k are (a small vocabulary: all)
                 clear_counts();
+#pragma unroll 4
                 for (int v = v0 + lane; v < v1; v += 32) {
+                    if (!(X.largest(v) >= low_)) continue;
                     float x[kVec];
                     load(v, x);
 #pragma unroll
