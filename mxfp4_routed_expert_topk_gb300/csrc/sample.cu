@@ -206,7 +206,7 @@ struct Sampler {
     const SampleArgs &a;
     Smem &s;
     const uint32_t rank, ranks;
-    const int tid, lane, warp, r;
+    const int tid, lane, warp, row;
     const Row<BF16> X;
     int v0, v1;     // this warp's vectors
     bool infinite;  // the row's largest is +infinity: those are 0, everything else -infinity
@@ -214,7 +214,7 @@ struct Sampler {
 
     __device__ __forceinline__ Sampler(const SampleArgs &a_, Smem &s_)
         : a(a_), s(s_), rank(cluster_ctarank()), ranks(cluster_nctarank()), tid((int)threadIdx.x), lane(tid & 31),
-          warp(tid >> 5), r((int)(blockIdx.x / ranks)), X(a_.x, (size_t)r * a_.ld, a_.vocab), infinite(false) {
+          warp(tid >> 5), row((int)(blockIdx.x / ranks)), X(a_.x, (size_t)row * a_.ld, a_.vocab), infinite(false) {
         const int vectors = X.vectors(), per = (vectors + (int)ranks * kWarps - 1) / ((int)ranks * kWarps);
         v0 = min(((int)rank * kWarps + warp) * per, vectors);
         v1 = min(v0 + per, vectors);
@@ -403,16 +403,16 @@ struct Sampler {
     // ------------------------------------------------------------ output
     __device__ __forceinline__ void put(int i, float p) const {
         if (BF16)
-            (static_cast<uint16_t *>(a.probs) + (size_t)r * a.ldp)[i] = __bfloat16_as_ushort(__float2bfloat16(p));
+            (static_cast<uint16_t *>(a.probs) + (size_t)row * a.ldp)[i] = __bfloat16_as_ushort(__float2bfloat16(p));
         else
-            (static_cast<float *>(a.probs) + (size_t)r * a.ldp)[i] = p;
+            (static_cast<float *>(a.probs) + (size_t)row * a.ldp)[i] = p;
     }
     // Zeros in this CTA's part of the row.
     __device__ __forceinline__ void clear_row() const {
         const int per = (a.vocab + (int)ranks - 1) / (int)ranks;
         const int i0 = min((int)rank * per, a.vocab), i1 = min(i0 + per, a.vocab);
         constexpr int kSize = BF16 ? 2 : 4;
-        uint8_t *p = static_cast<uint8_t *>(a.probs) + ((size_t)r * a.ldp + i0) * kSize;
+        uint8_t *p = static_cast<uint8_t *>(a.probs) + ((size_t)row * a.ldp + i0) * kSize;
         uint8_t *end = p + (size_t)(i1 - i0) * kSize;
         uint8_t *q = (uint8_t *)(((uintptr_t)p + 15) & ~(uintptr_t)15), *qe = (uint8_t *)((uintptr_t)end & ~(uintptr_t)15);
         if (q > qe) q = qe = end;
@@ -476,9 +476,9 @@ struct Sampler {
         sort_by(n, [&](uint64_t key) { return (0xfffff - (int)(key >> 39)) >> shift; });
         constexpr uint64_t kWeight = (1ull << 39) - 1;
         scan(upto, n, [&](int i) { return s.list[i] & kWeight; });
-        const uint64_t aim = share_of(upto[n - 1], whole_uniform(a.u[r]), false);
+        const uint64_t aim = share_of(upto[n - 1], whole_uniform(a.u[row]), false);
         for (int i = tid; i < n; i += kThreads)
-            if (upto[i] > aim && (i == 0 || upto[i - 1] <= aim)) a.next[r] = 0xfffff - (int)(s.list[i] >> 39);
+            if (upto[i] > aim && (i == 0 || upto[i - 1] <= aim)) a.next[row] = 0xfffff - (int)(s.list[i] >> 39);
     }
     // The same for at most kFew tokens: each is compared with all, by two threads.
     __device__ __forceinline__ void finish_few(int n, int k, uint64_t part, uint64_t lim, uint64_t least) const {
@@ -524,8 +524,8 @@ struct Sampler {
             }
         }
         before += __shfl_xor_sync(0xffffffffu, before, 1);
-        const uint64_t aim = share_of(total, whole_uniform(a.u[r]), false);
-        if (w != 0 && (tid & 1) == 0 && before <= aim && aim < before + w) a.next[r] = index;
+        const uint64_t aim = share_of(total, whole_uniform(a.u[row]), false);
+        if (w != 0 && (tid & 1) == 0 && before <= aim && aim < before + w) a.next[row] = index;
     }
     __device__ __forceinline__ uint64_t cta_sum(uint64_t v) const {
 #pragma unroll
@@ -713,7 +713,7 @@ struct Sampler {
         cluster_arrive();  // waited for before the first remote store: by then every CTA has started
         // the first token of the order: the largest value of each vector, and the first vector that has it
         // (vectors rise in each thread); NaN is passed over
-        const int k = a.top_k != nullptr ? a.top_k[r] : 0;
+        const int k = a.top_k != nullptr ? a.top_k[row] : 0;
         const bool by_count = k > 0 && k < a.vocab, lead = by_count && k <= kSmallK && a.vocab > kList;
         float top = kNone, tops[kSubs];
         int top_v = -1;
@@ -757,14 +757,14 @@ struct Sampler {
             low = fminf(low, __uint_as_float(s.low[q]));
         }
 
-        const float T = a.temperature[r];
+        const float T = a.temperature[row];
         if (key == 0 || !(T > 0.f)) {  // nothing to draw from, or nothing to draw
             if (PROBS) {
                 clear_row();
                 cluster_sync();
                 if (first() && tid == 0 && key != 0) put(key_index(key), 1.f);
             } else if (first() && tid == 0) {
-                a.next[r] = key == 0 ? -1 : key_index(key);
+                a.next[row] = key == 0 ? -1 : key_index(key);
             }
             return;
         }
@@ -776,8 +776,8 @@ struct Sampler {
             W.m = 0.f;
             low = low == INFINITY ? 0.f : kNone;
         }
-        const uint64_t part = a.top_p != nullptr ? max(first_bits(a.top_p[r], 1ull << kUniform), (uint64_t)1) : 1ull << kUniform;
-        const uint64_t least = a.min_p != nullptr ? first_bits(a.min_p[r], 0) << (kGrid - kUniform) : 0;
+        const uint64_t part = a.top_p != nullptr ? max(first_bits(a.top_p[row], 1ull << kUniform), (uint64_t)1) : 1ull << kUniform;
+        const uint64_t least = a.min_p != nullptr ? first_bits(a.min_p[row], 0) << (kGrid - kUniform) : 0;
         const bool by_share = part < 1ull << kUniform;
 
         uint64_t cut = 0, before, cta;  // tokens below this key are not kept
@@ -892,25 +892,70 @@ struct Sampler {
         l -= kVec * 0x4b000000u;
         return ((uint64_t)h << 23) + l;
     }
-    // The weights of vector v that stand before or at the cut and weigh at least `least`.
-    __device__ __forceinline__ void kept(int v, uint64_t cut, uint64_t least, uint64_t (&w)[kVec]) const {
-        float x[kVec], y[kVec];
+    // The octaves of vector v's values that stand before or at the cut (of others: -60).
+    __device__ __forceinline__ void before_cut(int v, uint64_t cut, float (&y)[kVec]) const {
+        float x[kVec];
         load(v, x);
         const float cx = cut != 0 ? key_value(cut) : kNone;
-        const int ci = cut != 0 ? key_index(cut) : 0;
+        const int last = cut != 0 ? key_index(cut) - X.first(v) : kVec;  // (of values that equal the cut's)
 #pragma unroll
-        for (int j = 0; j < kVec; j++)
-            if (!(x[j] > cx || (x[j] == cx && X.first(v) + j <= ci))) x[j] = kNone;
+        for (int j = 0; j < kVec; j++) x[j] = x[j] > cx || (x[j] == cx && j <= last) ? x[j] : kNone;
+#pragma unroll
+        for (int j = 0; j < kVec; j += 2) W.octaves(x[j], x[j + 1], y[j], y[j + 1]);
+    }
+    // The weights of vector v that stand before or at the cut and weigh at least `least`.
+    __device__ __forceinline__ void kept(int v, uint64_t cut, uint64_t least, uint64_t (&w)[kVec]) const {
+        float y[kVec];
+        before_cut(v, cut, y);
 #pragma unroll
         for (int j = 0; j < kVec; j += 2) {
             uint32_t hi[2], lo[2];
-            W.octaves(x[j], x[j + 1], y[j], y[j + 1]);
             Weigh::parts(y[j], y[j + 1], hi, lo);
 #pragma unroll
             for (int i = 0; i < 2; i++) {
                 w[j + i] = Weigh::join(hi[i], lo[i]);
                 if (w[j + i] < least) w[j + i] = 0;
             }
+        }
+    }
+    // The probabilities of vector v: its kept weights by their sum, the reciprocal of which is r.
+    __device__ __forceinline__ void put_vector(int v, uint64_t cut, float least, float all, float r) const {
+        float y[kVec], p[kVec];
+        before_cut(v, cut, y);
+#pragma unroll
+        for (int j = 0; j < kVec; j += 2) {
+            uint32_t hi[2], lo[2];
+            Weigh::parts(y[j], y[j + 1], hi, lo);
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                // (24 significant bits at most: exact)
+                float w = fmaf(__uint_as_float(hi[i]) - 8388608.f, 8388608.f, __uint_as_float(lo[i]) - 8388608.f);
+                w = w < least ? 0.f : w;
+                // Markstein's division: with the rounded reciprocal, one step from the rounded product gives
+                // the rounded quotient
+                const float q = __fmul_rn(w, r);
+                p[j + i] = fmaf(fmaf(-q, all, w), r, q);
+            }
+        }
+        const int i0 = X.first(v);
+        constexpr int kSize = BF16 ? 2 : 4;
+        uint8_t *to = static_cast<uint8_t *>(a.probs) + ((ptrdiff_t)((size_t)row * a.ldp) + i0) * kSize;
+        if (X.whole_vector(v) && ((uintptr_t)to & 15u) == 0) {
+            uint32_t u[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++) {
+                if constexpr (BF16) {
+                    const __nv_bfloat162 z = __floats2bfloat162_rn(p[2 * k], p[2 * k + 1]);
+                    u[k] = *reinterpret_cast<const uint32_t *>(&z);
+                } else {
+                    u[k] = __float_as_uint(p[k]);
+                }
+            }
+            *reinterpret_cast<uint4 *>(to) = make_uint4(u[0], u[1], u[2], u[3]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < kVec; j++)
+                if (i0 + j >= 0 && i0 + j < a.vocab) put(i0 + j, p[j]);
         }
     }
     __device__ __forceinline__ uint64_t kept_sum(int v, int end, uint64_t cut, uint64_t least) const {
@@ -930,19 +975,12 @@ struct Sampler {
         const uint64_t mine = known ? (lane == 0 ? s.warp[warp] : 0) : kept_sum(v0 + lane, v1, cut, least);
         const uint64_t total = add_up(mine, 2, before, cta);
         if (PROBS) {
-            const float all = __ull2float_rn(total);
-            for (int v = v0 + lane; v < v1; v += 32) {
-                uint64_t w[kVec];
-                kept(v, cut, least, w);
-#pragma unroll
-                for (int j = 0; j < kVec; j++) {
-                    const int i = X.first(v) + j;
-                    if (i >= 0 && i < a.vocab) put(i, w[j] == 0 ? 0.f : __fdiv_rn(__ull2float_rn(w[j]), all));
-                }
-            }
+            const float all = __ull2float_rn(total), inv = __fdiv_rn(1.f, all), at_least = (float)least;
+#pragma unroll 2
+            for (int v = v0 + lane; v < v1; v += 32) put_vector(v, cut, at_least, all, inv);
             return;
         }
-        const uint64_t aim = share_of(total, whole_uniform(a.u[r]), false);
+        const uint64_t aim = share_of(total, whole_uniform(a.u[row]), false);
         if (aim < before || aim >= before + cta) return;  // in another CTA's part
         // the warp whose part holds the point; the CTA's warps divide that part
         int w = 0;
@@ -979,7 +1017,7 @@ struct Sampler {
                     c += x[j];
                     if (found < 0 && c > aim) found = X.first(v + lane) + j;
                 }
-                a.next[r] = found;
+                a.next[row] = found;
             }
             before += __shfl_sync(0xffffffffu, upto, 31);
             if (before > aim) break;
@@ -995,10 +1033,14 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
 
 PerDevice g_sms(0);
 
-// CTAs per row: one for 16384 values, or more where there are few rows, 8 at most (the portable size).
-int cluster_size(int rows, int vocab, int sms) {
+// CTAs per row: as many as fit the device at once (4 CTAs of an SM), or more, so that the rows under way
+// stay in L2 (256 rows of 131072: 125 us with 4, 170 with 2); 8 at most (the portable size).
+int cluster_size(int rows, size_t row_bytes, int sms) {
+    const int64_t slots = 4 * (int64_t)sms;
     int c = 1;
-    while (c < kMaxCluster && (int64_t)rows * c * 2 <= 4 * (int64_t)sms) c *= 2;
+    while (c < kMaxCluster &&
+           (rows * c * 2 <= slots || std::min<int64_t>(rows, slots / c) * (int64_t)row_bytes > (80 << 20)))
+        c *= 2;
     return c;
 }
 
@@ -1010,7 +1052,7 @@ cudaError_t launch(const SampleArgs &a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     if ((e = ensure_dynamic_smem(sample_kernel<BF16, PROBS>, sizeof(Smem), smem_set)) != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = cluster_config(attr, a.rows, cluster_size(a.rows, a.vocab, sms), kThreads, st);
+    cudaLaunchConfig_t cfg = cluster_config(attr, a.rows, cluster_size(a.rows, (size_t)a.vocab * (BF16 ? 2 : 4), sms), kThreads, st);
     cfg.dynamicSmemBytes = sizeof(Smem);
     return cudaLaunchKernelEx(&cfg, sample_kernel<BF16, PROBS>, a);
 }
