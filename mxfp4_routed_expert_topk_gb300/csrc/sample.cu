@@ -212,9 +212,9 @@ struct Sampler {
     bool infinite;  // the row's largest is +infinity: those are 0, everything else -infinity
     Weigh W;
 
-    __device__ __forceinline__ Sampler(const SampleArgs &a_, Smem &s_)
+    __device__ __forceinline__ Sampler(const SampleArgs &a_, Smem &s_, int row_)
         : a(a_), s(s_), rank(cluster_ctarank()), ranks(cluster_nctarank()), tid((int)threadIdx.x), lane(tid & 31),
-          warp(tid >> 5), row((int)(blockIdx.x / ranks)), X(a_.x, (size_t)row * a_.ld, a_.vocab), infinite(false) {
+          warp(tid >> 5), row(row_), X(a_.x, (size_t)row * a_.ld, a_.vocab), infinite(false) {
         const int vectors = X.vectors(), per = (vectors + (int)ranks * kWarps - 1) / ((int)ranks * kWarps);
         v0 = min(((int)rank * kWarps + warp) * per, vectors);
         v1 = min(v0 + per, vectors);
@@ -587,11 +587,11 @@ struct Sampler {
     // The cluster's bins -> rank 0, each CTA a part of them.
     __device__ __forceinline__ void merge_bins() const {
         cluster_sync();
-        const int per = kBins / (int)ranks;
-        for (int i = tid; i < per; i += kThreads) {
+        const int per = (kBins + (int)ranks - 1) / (int)ranks, end = min((int)(rank + 1) * per, kBins);
+        for (int i = (int)rank * per + tid; i < end; i += kThreads) {
             uint32_t c = 0;
-            for (uint32_t q = 0; q < ranks; q++) c += ld_cluster(s.fast.bin + (int)rank * per + i, q);
-            store_cluster_u32(s.merged + (int)rank * per + i, 0, c);
+            for (uint32_t q = 0; q < ranks; q++) c += ld_cluster(s.fast.bin + i, q);
+            store_cluster_u32(s.merged + i, 0, c);
         }
         cluster_sync();
     }
@@ -1025,10 +1025,47 @@ struct Sampler {
     }
 };
 
+// The row that cluster `unit` takes where not all are under way at once: first those whose share of the
+// weights is asked for without a top-k, which take three times as long.  (256 rows of 131072, an eighth of
+// them such: HHH us, in their order 127.)
+__device__ __forceinline__ int row_of(const SampleArgs &a, Smem &s, int unit) {
+    const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int slow = 0, mine = -1;  // slow rows so far
+    for (int round = 0; round < 2; round++) {
+        const int all = slow;  // (in the second round)
+        slow = 0;
+        for (int r0 = 0; r0 < a.rows; r0 += kThreads) {
+            const int r = r0 + tid;
+            bool f = false;
+            if (r < a.rows && a.temperature[r] > 0.f && a.top_p[r] < 1.f) {
+                const int k = a.top_k != nullptr ? a.top_k[r] : 0;
+                f = !(k > 0 && k <= kSmallK);
+            }
+            const uint32_t m = __ballot_sync(0xffffffffu, f);
+            __syncthreads();
+            if (lane == 0) s.wcnt[warp] = (uint32_t)__popc(m);
+            __syncthreads();
+            int before = slow + __popc(m & ((1u << lane) - 1u));
+            for (int w = 0; w < kWarps; w++) {
+                if (w < warp) before += (int)s.wcnt[w];
+                slow += (int)s.wcnt[w];
+            }
+            if (round == 1 && r < a.rows && unit == (f ? before : all + r - before)) mine = r;
+        }
+    }
+    if (mine >= 0) s.n = mine;
+    __syncthreads();
+    mine = s.n;
+    __syncthreads();
+    return mine;
+}
+
 template <bool BF16, bool PROBS>
 __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a) {
     extern __shared__ __align__(16) unsigned char raw[];
-    Sampler<BF16, PROBS>(a, *reinterpret_cast<Smem *>(raw)).run();
+    Smem &s = *reinterpret_cast<Smem *>(raw);
+    const int unit = (int)(blockIdx.x / cluster_nctarank());
+    Sampler<BF16, PROBS>(a, s, a.in_order ? unit : row_of(a, s, unit)).run();
 }
 
 PerDevice g_sms(0);
@@ -1037,22 +1074,22 @@ PerDevice g_sms(0);
 // stay in L2 (256 rows of 131072: 125 us with 4, 170 with 2); 8 at most (the portable size).
 int cluster_size(int rows, size_t row_bytes, int sms) {
     const int64_t slots = 4 * (int64_t)sms;
-    int c = 1;
-    while (c < kMaxCluster &&
-           (rows * c * 2 <= slots || std::min<int64_t>(rows, slots / c) * (int64_t)row_bytes > (80 << 20)))
-        c *= 2;
+    int c = (int)std::min<int64_t>(kMaxCluster, std::max<int64_t>(1, slots / rows));
+    while (c < kMaxCluster && std::min<int64_t>(rows, slots / c) * (int64_t)row_bytes > (80 << 20)) c++;
     return c;
 }
 
 template <bool BF16, bool PROBS>
-cudaError_t launch(const SampleArgs &a, cudaStream_t st) {
+cudaError_t launch(SampleArgs a, cudaStream_t st) {
     static PerDevice smem_set(0);
     int sms = 0;
     cudaError_t e = device_attr(cudaDevAttrMultiProcessorCount, g_sms, &sms);
     if (e != cudaSuccess) return e;
     if ((e = ensure_dynamic_smem(sample_kernel<BF16, PROBS>, sizeof(Smem), smem_set)) != cudaSuccess) return e;
     cudaLaunchAttribute attr[1];
-    cudaLaunchConfig_t cfg = cluster_config(attr, a.rows, cluster_size(a.rows, (size_t)a.vocab * (BF16 ? 2 : 4), sms), kThreads, st);
+    const int c = cluster_size(a.rows, (size_t)a.vocab * (BF16 ? 2 : 4), sms);
+    a.in_order = a.top_p == nullptr || a.vocab <= kList || (int64_t)a.rows * c <= 4 * (int64_t)sms || a.rows > 16 * kThreads;
+    cudaLaunchConfig_t cfg = cluster_config(attr, a.rows, c, kThreads, st);
     cfg.dynamicSmemBytes = sizeof(Smem);
     return cudaLaunchKernelEx(&cfg, sample_kernel<BF16, PROBS>, a);
 }
