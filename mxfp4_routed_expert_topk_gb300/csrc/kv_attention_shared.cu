@@ -11,7 +11,8 @@
 // fp32; the second is one per sequence and adds the first when it writes its own.  Both are the cache
 // attention's kernels with other lengths and tables.
 //
-// Small batches run once, each sequence over its prefix and its own tokens, as a second launch costs 15 us.
+// Small batches run once, each sequence over its prefix and its own tokens: two runs take 50 us or more,
+// however little there is to do.
 #include <algorithm>
 
 #include "kv_attention_few.cuh"
@@ -20,7 +21,11 @@
 namespace moe {
 namespace {
 
-constexpr int kSmall = 8;  // tiles per SM
+// Tiles per SM (as many as the tables have room for) up to which a batch is small.  Once / twice, one row of
+// 56 heads of 128: 16 sequences of 2000 + 200 tokens (14 tiles per SM) 33 / 49 us, 64 of 1000 + 100 (30)
+// 53 / 58, 2 of 30000 (25) 47 / 56, 8 of 16000 (53) 60 / 53, 64 of 4000 + 300 (115) 113 / 78; five rows, 32 of
+// 2000 + 300 (30) 73 / 80.
+constexpr int kSmall = 32;
 
 cudaError_t run(const AttnSetup &s, cudaStream_t st) {
     if (s.a.rpt > kFewRows) return launch_rows<true>(s.tm, s.a, s.sms, s.smem_max, st);

@@ -27,7 +27,10 @@ def _built():
 
 class Shared(Case):
     """Sequences in groups: members[g] of them share the first prefix[g] tokens.  The other members' own
-    entries for the shared pages name no page."""
+    entries for the shared pages name no page.  Tables with room for many tokens make the call run twice
+    (prefixes, then own tokens), others once."""
+
+    twice = False
 
     def __init__(self, members, prefix, n, own, heads, group, dim, page, **kw):
         old, at = [], 0
@@ -47,6 +50,11 @@ class Shared(Case):
                     self.kv[b] = tuple(np.concatenate([self.kv[b0][i][:w * page], self.kv[b][i][w * page:]]) for i in (0, 1))
             self.groups.append(b0 + m)
             self.whole += [w * page] * m
+        if self.twice:
+            tiles = 33 * torch.cuda.get_device_properties(0).multi_processor_count // (len(n) * heads) + 1
+            room = np.full((len(n), -(-128 * tiles // page)), -1, dtype=np.int32)
+            room[:, :self.table.shape[1]] = self.table[:, :room.shape[1]]
+            self.table = room if room.shape[1] > self.table.shape[1] else self.table
         self.max_rows = max(n)
         self.max_group_rows = max(1, max(sum(n[a:b]) for a, b in zip(self.groups, self.groups[1:])))
 
@@ -94,6 +102,13 @@ class Shared(Case):
                 want = m[..., 0] + np.log(l)
                 assert (np.abs(gl[r].reshape(want.shape) - want) <= ds + 2.0 ** -20 * (1 + np.abs(want) + np.abs(s).max(-1))).all()
         return out, lse
+
+
+@pytest.fixture(autouse=True, params=[False, True], ids=["once", "twice"])
+def _ways(request):
+    Shared.twice = request.param
+    yield
+    Shared.twice = False
 
 
 SHAPES = [
