@@ -397,8 +397,9 @@ moe_status moe_kv_attention(const moe_kv *kv, int layer, const uint16_t *q, size
  * (cu_groups [groups+1], ascending from 0 to seqs: every sequence is in one, alone if need be),
  * whose first prefix_len[g] tokens are the same (0: nothing is shared).  What is taken as shared
  * are the prefix's whole pages, as named by the first columns of the table row of the group's first
- * sequence (the other sequences' entries there are not read); tokens of a page that the prefix does
- * not fill are read for each sequence, from its own table.  New rows stand behind the prefix: a
+ * sequence with rows (the other sequences' entries there are not read: one that has ended may have
+ * given its pages back); tokens of a page that the prefix does not fill are read for each sequence,
+ * from its own table.  New rows stand behind the prefix: a
  * sequence with rows has kv_len[b] - (its rows) >= prefix_len[g], counted in whole pages, or is
  * reported as MOE_ERR_BAD_PAGE, as are groups that do not take the sequences in order, and the
  * errors of moe_kv_attention; rows are then not valid.  A group has at most max_group_rows rows in
@@ -468,7 +469,7 @@ moe_status moe_kv_release(const int32_t *keep, const int32_t *kv_len, int seqs, 
  * the lowest index i at which the kept weights of tokens 0 .. i sum to more than floor(S t / 2^24).
  * moe_sample_probs: probs [rows][vocab] in `dtype`, row r at probs + r * ldp, the kept weights divided
  * by S (both rounded to fp32, then to `dtype`), 0 elsewhere: what moe_verify_sampled takes as p or q.
- * probs may be x itself.  temperature <= 0 or NaN: the first token of the order (probability 1), whatever
+ * probs may be x itself (with ldp = ld).  temperature <= 0 or NaN: the first token of the order (probability 1), whatever
  * the cuts.  A row of nothing but NaN and -infinity: next = -1, probabilities 0.
  * ws: moe_sample_workspace_size() bytes. */
 moe_status moe_sample_workspace_size(int rows, int vocab, size_t *bytes);

@@ -511,6 +511,7 @@ moe_status moe_sample_probs(const void *x, size_t ld, int dtype, int rows, int v
     const moe_status s = sample_check(a, dtype, ws, ws_bytes);
     if (s != MOE_OK) return s;
     if (ldp < (size_t)vocab || (rows > 0 && (probs == nullptr || !aligned(probs, a.bf16 ? 2 : 4)))) return MOE_ERR_INVALID_ARG;
+    if (probs == x && ldp != ld && rows > 1) return MOE_ERR_INVALID_ARG;  // (a row would be written over another's logits)
     if (rows == 0) return MOE_OK;
     return cuda_status(launch_sample(a, (cudaStream_t)stream));
 }

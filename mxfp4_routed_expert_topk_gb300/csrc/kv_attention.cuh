@@ -113,6 +113,21 @@ __device__ __forceinline__ int whole_pages(const AttnArgs &a, int g) {
     return max(a.prefix_len[g], 0) & -a.k.kv.page;
 }
 
+// The sequence whose row of the table names a prefix's pages: the first of g0 .. g1 - 1 that has rows
+// (one that has ended may have given its pages back).
+__device__ __forceinline__ int lead_of(const AttnArgs &a, int g0, int g1) {
+    const int row = a.k.cu_rows[g0];
+    if (a.k.cu_rows[g0 + 1] > row) return g0;
+    while (g1 - g0 > 1) {  // the last that begins at or before the first row
+        const int mid = (g0 + g1) >> 1;
+        if (a.k.cu_rows[mid] <= row)
+            g0 = mid;
+        else
+            g1 = mid;
+    }
+    return g0;
+}
+
 // What load_item finds, where a group's prefix or a sequence's own tokens are the item.
 __device__ __forceinline__ void load_shared(const AttnArgs &a, SharedItem &x) {
     const int64_t room = min((int64_t)a.k.table_width * a.k.kv.page, (int64_t)kMaxLen);
@@ -121,7 +136,7 @@ __device__ __forceinline__ void load_shared(const AttnArgs &a, SharedItem &x) {
         const int g = x.b, g0 = a.cu_groups[g], g1 = a.cu_groups[g + 1];
         // the groups take all sequences, in order
         x.ok = g0 >= 0 && g0 <= g1 && g1 <= a.k.seqs && (g > 0 || g0 == 0) && (g + 1 < a.groups || g1 == a.k.seqs);
-        x.b = x.ok ? g0 : 0;
+        x.b = x.ok && g0 < g1 ? lead_of(a, g0, g1) : 0;
         x.row0 = hi = 0;
         if (x.ok) {
             x.row0 = a.k.cu_rows[g0];
@@ -154,7 +169,7 @@ __device__ __forceinline__ void load_shared(const AttnArgs &a, SharedItem &x) {
         const int prefix = whole_pages(a, g), before = (int)min((int64_t)prefix, room);
         if (prefix > before) x.ok = false;
         x.col0 = before / a.k.kv.page;
-        x.lead = min(max(g0, 0), x.b);
+        x.lead = a.what == kWhole && x.ok && x.n > 0 && before > 0 ? lead_of(a, g0, g1) : 0;
         const int all = max(a.k.kv_len[x.b], 0);
         if ((int64_t)all > room) x.ok = false;
         len = (int)min((int64_t)all, room) - before;
@@ -257,6 +272,10 @@ __device__ __forceinline__ Line cut_line(const AttnArgs &a, int64_t *sums, Start
     const int items = (SHARED && a.what == kPrefixes ? a.groups : a.k.seqs) * a.nrt;
     const int per = (items + NT - 1) / NT;
     const int i0 = min(tid * per, items), i1 = min(i0 + per, items);
+    if (SHARED && a.what == kWhole && blockIdx.x == 0) {  // (else the groups themselves are the items)
+        for (int g = tid; g < a.groups; g += NT)
+            if (a.cu_groups[g] > a.cu_groups[g + 1]) set_status(a.k.st, MOE_ERR_BAD_PAGE, 1);
+    }
     // two rounds over the thread's items: their sum, then those that hold the workers' starts
     Line l;
     int64_t mine = 0, pre = 0, lo[NW];

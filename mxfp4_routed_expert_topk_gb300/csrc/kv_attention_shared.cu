@@ -61,8 +61,8 @@ cudaError_t launch_kv_attention_shared(const KvAttentionArgs &k, const int32_t *
     s.a.group_rows = max_group_rows;
     TraceScope trace_scope("kv_attention_shared", st);
     // (lengths are known on the device alone: by the most tiles that the tables have room for)
-    const int64_t tiles = (((int64_t)k.table_width * k.kv.page + kTokens - 1) / kTokens) * k.seqs * s.a.nrt * k.kv.heads;
-    if (tiles <= (int64_t)kSmall * s.sms) {
+    const double tiles = (double)(((int64_t)k.table_width * k.kv.page + kTokens - 1) / kTokens) * k.seqs * s.a.nrt * k.kv.heads;
+    if (tiles <= (double)kSmall * s.sms) {
         s.a.what = kWhole;
         return run(s, st);
     }

@@ -44,10 +44,13 @@ class Shared(Case):
         for m, p in zip(members, prefix):
             b0 = self.groups[-1]
             w = p // page
-            for b in range(b0 + 1, b0 + m):
+            lead = next((b for b in range(b0, b0 + m) if n[b]), b0)  # whose row of the table names the pages
+            for b in range(b0, b0 + m):
+                if b == lead:
+                    continue
                 self.table[b, :w] = -1
                 if self.kv[b][0].shape[0]:
-                    self.kv[b] = tuple(np.concatenate([self.kv[b0][i][:w * page], self.kv[b][i][w * page:]]) for i in (0, 1))
+                    self.kv[b] = tuple(np.concatenate([self.kv[lead][i][:w * page], self.kv[b][i][w * page:]]) for i in (0, 1))
             self.groups.append(b0 + m)
             self.whole += [w * page] * m
         if self.twice:
@@ -124,6 +127,7 @@ SHAPES = [
     ([1, 4, 1, 3], [100, 300, 0, 64], [1, 1, 2, 1, 1, 3, 1, 1, 1], [5, 0, 9, 44, 3, 70, 0, 1, 2], 2, 5, 64, 16),
     ([1, 1, 1], [0, 0, 0], [1, 3, 1], [200, 0, 5], 2, 3, 64, 32),    # nothing is shared
     ([4, 3], [256, 128], [1, 0, 2, 0, 0, 1, 0], [3, 0, 4, 9, 1, 0, 2], 2, 7, 128, 16),   # sequences without rows
+    ([6, 2], [64, 32], [0, 0, 0, 1, 0, 2, 0, 1], [3, 0, 4, 9, 1, 0, 2, 5], 2, 3, 64, 16),  # the first ones have ended
     ([0, 3, 0, 0, 2, 0], [64, 128, 0, 9, 40, 5], [1, 1, 1, 1, 1], [5, 6, 7, 8, 9], 1, 7, 128, 16),  # empty groups
     ([70], [256], [1] * 70, [2] * 70, 1, 2, 128, 64),
     ([2], [6000], [1, 1], [10, 200], 2, 7, 128, 64),                 # a long prefix over many CTAs
@@ -272,7 +276,7 @@ def test_reports_what_it_cannot_do():
 
     big = 2 ** 31 - 1
     bad = [dict(groups=[0, 2, 3]), dict(groups=[1, 2, 4]), dict(groups=[0, 5, 4]), dict(groups=[0, -1, 4]), dict(groups=[0, 2, big]),
-           dict(groups=[3, 2, 4]), dict(cu=[0, 1, 3, 4, 6]), dict(cu=[0, 3, 1, 4, 5]), dict(cu=[-1, 1, 3, 4, 5]),
+           dict(groups=[3, 2, 4]), dict(groups=[0, 3, 2, 4], prefix=[128, 0, 64]), dict(cu=[0, 1, 3, 4, 6]), dict(cu=[0, 3, 1, 4, 5]), dict(cu=[-1, 1, 3, 4, 5]),
            dict(prefix=[160, 64]), dict(prefix=[big, 64]), dict(lens=[100, 130, 70, 66]), dict(lens=[138, 130, big, 66]),
            dict(max_rows=1), dict(max_group_rows=2)]
     for page in (-1, c.cache.n_pages, big, -2 ** 31):

@@ -92,6 +92,7 @@ def test_sampling_refusals(L):
         assert f(n=255) == moe.MOE_ERR_WORKSPACE
         assert f(rows=0, x=None, t=None) == moe.MOE_OK
     assert sample(u=None) == BAD and sample(nxt=None) == BAD
+    assert probs(out=FAKE, x=FAKE, ldp=101) == BAD      # over the logits with other rows
     assert probs(out=None) == BAD and probs(ldp=99) == BAD and probs(out=vp((1 << 20) + 2)) == BAD
 
 
