@@ -56,6 +56,10 @@ struct Smem {
     union {
         uint64_t stage[kList];  // a CTA's own tokens for the list; rank 0: the list's weights
         uint32_t merged[kBins]; // rank 0's: the cluster's bins
+        struct {
+            uint64_t sum[kExact];
+            uint32_t cnt[kExact];
+        } both;
     };
     uint64_t list[kList];       // rank 0's: keys
     uint64_t cta[3][kMaxCluster];
@@ -220,6 +224,8 @@ struct Sampler {
         v1 = min(v0 + per, vectors);
     }
     __device__ __forceinline__ bool first() const { return rank == 0; }
+    // This thread's first vector where the CTAs' warps take 32 each in turn.
+    __device__ __forceinline__ int turn() const { return (warp * (int)ranks + (int)rank) * 32 + lane; }
 
     __device__ __forceinline__ void load(int v, float (&x)[kVec]) const {
         X.load(v, kNone, x);
@@ -549,15 +555,25 @@ struct Sampler {
         cluster_sync();  // (other CTAs add to s.total)
     }
     // A bound that k values of this CTA do not fall below, from the largest of each part of the
-    // threads' values; -infinity if those do not tell.  `top`: the largest of all.
-    __device__ __forceinline__ float bound_of(const float (&tops)[kSubs], float top, int k) const {
+    // threads' values, or from all of them; -infinity if those do not tell.  `top`: the largest.
+    __device__ __forceinline__ float bound_of(const float (&tops)[kSubs], float top, int k, bool all) const {
         constexpr float kPerUnit = 16.f * 1.442695f;
         if (tid == 0) s.bound = kNone;
-#pragma unroll
-        for (int i = 0; i < kSubs; i++) {
-            if (tops[i] == kNone) continue;
-            const float d = (top - tops[i]) * kPerUnit;
+        auto count = [&](float x) {
+            if (!(x > kNone)) return;
+            const float d = (top - x) * kPerUnit;
             if (!(d >= (float)kBins)) atomicAdd(s.fast.bin + (int)d, 1u);  // (NaN, of infinities: 0)
+        };
+        if (all) {
+            for (int v = turn(); v < X.vectors(); v += (int)ranks * kThreads) {
+                float x[kVec];
+                X.load(v, kNone, x);
+#pragma unroll
+                for (int j = 0; j < kVec; j++) count(x[j]);
+            }
+        } else {
+#pragma unroll
+            for (int i = 0; i < kSubs; i++) count(tops[i]);
         }
         __syncthreads();
         constexpr int kPer = kBins / kThreads;
@@ -645,6 +661,20 @@ struct Sampler {
     }
 
     // ------------------------------------------- exact search, digit by digit
+    // Rank 0: the listed token at which tokens, or weights, reach `target`, c0 and w0 of them being before
+    // the list: told with the weights up to and with it (0: none).
+    __device__ __forceinline__ void resolve(int n, bool weights, uint64_t c0, uint64_t w0, uint64_t target) const {
+        uint64_t *upto = s.stage;
+        scan(upto, n, [&](int i) { return listed(i); });
+        if (tid == 0) tell(Word{0, 0, 0, 0});
+        __syncthreads();
+        for (int i = tid; i < n; i += kThreads) {
+            const uint64_t w = w0 + (i > 0 ? upto[i - 1] : 0), here = w0 + upto[i];
+            const bool is = weights ? w < target && target <= here : c0 + i + 1 == target;
+            if (is) tell(Word{s.list[i], here, 0, 0});
+        }
+    }
+
     // The token at which tokens, or weights, reach `target` in the order: its key, and the weights up to
     // and with it.
     __device__ __noinline__ uint64_t search(bool weights, uint64_t target, uint64_t &upto) const {
@@ -654,6 +684,7 @@ struct Sampler {
             const int shift = digit_shift(level), mask = (1 << digit_bits(level)) - 1;
             // the digits so far (between the logit's and the index's stand constant bits)
             const int above = level == 0 ? 64 : digit_shift(level - 1);
+            auto in = [&](uint64_t key) { return level == 0 || key >> above == prefix; };
             cluster_sync();  // the word is read, and the bins
             for (int i = tid; i < kExact; i += kThreads) s.exact.cnt[i] = 0, s.exact.sum[i] = 0;
             __syncthreads();
@@ -662,23 +693,28 @@ struct Sampler {
                 for (int j = 0; j < kVec; j++) {
                     if (!(y[j] > -kReach)) continue;
                     const uint64_t key = key_of(x[j], X.first(v) + j);
-                    if (level > 0 && key >> above != prefix) continue;
+                    if (!in(key)) continue;
                     const int d = mask - (int)(key >> shift & mask);
                     atomicAdd(s.exact.cnt + d, 1u);
                     atomicAdd((unsigned long long *)(s.exact.sum + d), (unsigned long long)Weigh::weight(y[j]));
                 }
             });
             cluster_sync();
+            // each CTA adds up a part of the bins, for rank 0
+            const int per = (kExact + (int)ranks - 1) / (int)ranks, end = min((int)(rank + 1) * per, kExact);
+            for (int i = (int)rank * per + tid; i < end; i += kThreads) {
+                uint32_t c = 0;
+                uint64_t w = 0;
+                for (uint32_t q = 0; q < ranks; q++) c += ld_cluster(s.exact.cnt + i, q), w += ld_cluster(s.exact.sum + i, q);
+                store_cluster_u64(&s.both.sum[i], 0, w);
+                store_cluster_u32(&s.both.cnt[i], 0, c);
+            }
+            cluster_sync();
             if (first()) {
                 constexpr int kPer = kExact / kThreads;
-                uint32_t cnt[kPer], c = 0;
-                uint64_t sum[kPer], w = 0;
-                for (int i = 0; i < kPer; i++) {
-                    cnt[i] = 0, sum[i] = 0;
-                    for (uint32_t q = 0; q < ranks; q++)
-                        cnt[i] += ld_cluster(s.exact.cnt + tid * kPer + i, q), sum[i] += ld_cluster(s.exact.sum + tid * kPer + i, q);
-                    c += cnt[i], w += sum[i];
-                }
+                uint32_t c = 0;
+                uint64_t w = 0;
+                for (int i = 0; i < kPer; i++) c += s.both.cnt[tid * kPer + i], w += s.both.sum[tid * kPer + i];
                 uint32_t uc = c;
                 uint64_t uw = w;
 #pragma unroll
@@ -687,15 +723,17 @@ struct Sampler {
                     const uint64_t ow = __shfl_up_sync(0xffffffffu, uw, d);
                     if (lane >= d) uc += oc, uw += ow;
                 }
-                if (lane == 31) s.wcnt[warp] = uc, s.warp[warp] = uw;
+                if (lane == 31) s.wcnt[warp] = uc, s.wscan[warp] = uw;
                 __syncthreads();
-                for (int q = 0; q < warp; q++) uc += s.wcnt[q], uw += s.warp[q];
+                for (int q = 0; q < warp; q++) uc += s.wcnt[q], uw += s.wscan[q];
                 uint64_t bc = c0 + uc - c, bw = w0 + uw - w;
                 for (int i = 0; i < kPer; i++) {
-                    const uint64_t before = weights ? bw : bc, here = weights ? sum[i] : cnt[i];
-                    if (before < target && target <= before + here) tell(Word{(uint64_t)(tid * kPer + i), bc, bw, bw + sum[i]});
-                    bc += cnt[i];
-                    bw += sum[i];
+                    const uint32_t cnt = s.both.cnt[tid * kPer + i];
+                    const uint64_t sum = s.both.sum[tid * kPer + i];
+                    const uint64_t before = weights ? bw : bc, here = weights ? sum : cnt;
+                    if (before < target && target <= before + here) tell(Word{(uint64_t)(tid * kPer + i), bc, bw, cnt});
+                    bc += cnt;
+                    bw += sum;
                 }
             }
             cluster_sync();
@@ -703,9 +741,27 @@ struct Sampler {
             prefix = level == 4 ? (prefix << 22) | (0xfffull << 10) | d : (prefix << digit_bits(level)) | d;
             c0 = s.word.b;
             w0 = s.word.c;
-            upto = s.word.d;
+            if (s.word.d <= kList) {  // the rest on the list
+                clear_counts();
+                each([&](int v, const float (&x)[kVec], const float (&y)[kVec]) {
+#pragma unroll
+                    for (int j = 0; j < kVec; j++)
+                        if (y[j] > -kReach) {
+                            const uint64_t key = key_of(x[j], X.first(v) + j);
+                            if (key >> shift == prefix) stage(x[j], X.first(v) + j);
+                        }
+                });
+                const int n = collect();
+                if (first()) {
+                    sort_list(n, 0.f, kReach);
+                    resolve(n, weights, c0, w0, target);
+                }
+                cluster_sync();
+                break;
+            }
         }
-        return prefix;
+        upto = s.word.b;
+        return s.word.a;
     }
 
     // -------------------------------------------------------------- the row
@@ -717,17 +773,22 @@ struct Sampler {
         const bool by_count = k > 0 && k < a.vocab, lead = by_count && k <= kSmallK && a.vocab > kList;
         float top = kNone, tops[kSubs];
         int top_v = -1;
-        const int len = (v1 - v0 + 32 * kSubs - 1) / (32 * kSubs) * 32;  // vectors of a part
+        // (here the CTAs and the parts of a thread take turns, so that each has its share of the large values
+        // wherever in the vocabulary they lie)
+        const int step = (int)ranks * kThreads, from = turn();
 #pragma unroll
-        for (int i = 0; i < kSubs; i++) {
-            tops[i] = kNone;
-#pragma unroll 8
-            for (int v = v0 + i * len + lane; v < min(v0 + (i + 1) * len, v1); v += 32) {
-                const float m = X.largest(v);
-                tops[i] = fmaxf(tops[i], m);
-                if (m > top) {
-                    top = m;
-                    top_v = v;
+        for (int i = 0; i < kSubs; i++) tops[i] = kNone;
+#pragma unroll 2
+        for (int v = from; v < X.vectors(); v += kSubs * step) {
+            float m[kSubs];
+#pragma unroll
+            for (int i = 0; i < kSubs; i++) m[i] = v + i * step < X.vectors() ? X.largest(v + i * step) : kNone;
+#pragma unroll
+            for (int i = 0; i < kSubs; i++) {
+                tops[i] = fmaxf(tops[i], m[i]);
+                if (m[i] > top) {
+                    top = m[i];
+                    top_v = v + i * step;
                 }
             }
         }
@@ -744,7 +805,10 @@ struct Sampler {
         if (lane == 0) s.warp[warp] = key;
         clear_bins();
         for (int w = 0; w < kWarps; w++) key = max(key, s.warp[w]);
-        const float bound = lead ? bound_of(tops, key != 0 ? key_value(key) : 0.f, (k + (int)ranks - 1) / (int)ranks) : kNone;
+        const float bound = lead ? bound_of(tops, key != 0 ? key_value(key) : 0.f, (k + (int)ranks - 1) / (int)ranks,
+                                          // (too few vectors for their largest to tell a small list)
+                                          a.vocab < 4 * kVec * k)
+                               : kNone;
         cluster_wait();
         if (tid < (int)ranks) {
             store_cluster_u64(&s.cta[0][rank], (uint32_t)tid, key);
@@ -787,7 +851,7 @@ struct Sampler {
                 // the tokens from `low` on, among which the first k are (a small vocabulary: all)
                 clear_counts();
 #pragma unroll 4
-                for (int v = v0 + lane; v < v1; v += 32) {
+                for (int v = from; v < X.vectors(); v += step) {
                     if (!(X.largest(v) >= low_)) continue;
                     float x[kVec];
                     load(v, x);
@@ -832,14 +896,7 @@ struct Sampler {
                     if (whole_list) return finish(n, false, 0, 0, target, least, (float)(b1 + 1) / scale);
                     if (first()) {
                         sort_list(n, (float)b0 / scale, (float)(b1 + 1) / scale);
-                        uint64_t *upto = s.stage;
-                        scan(upto, n, [&](int i) { return listed(i); });
-                        if (tid == 0) tell(Word{0, 0, 0, 0});
-                        __syncthreads();
-                        for (int i = tid; i < n; i += kThreads) {
-                            const uint64_t b = sum_above + (i > 0 ? upto[i - 1] : 0);
-                            if (b < target && target <= sum_above + upto[i]) tell(Word{s.list[i], sum_above + upto[i], 0, 0});
-                        }
+                        resolve(n, true, 0, sum_above, target);
                     }
                     cluster_sync();
                     cut = s.word.a;
