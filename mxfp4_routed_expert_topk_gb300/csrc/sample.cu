@@ -486,20 +486,20 @@ struct Sampler {
         for (int i = tid; i < n; i += kThreads)
             if (upto[i] > aim && (i == 0 || upto[i - 1] <= aim)) a.next[row] = 0xfffff - (int)(s.list[i] >> 39);
     }
-    // The same for at most kFew tokens: each is compared with all, by two threads.
-    __device__ __forceinline__ void finish_few(int n, int k, uint64_t part, uint64_t lim, uint64_t least) const {
+    // Of at most kFew listed tokens, thread 2 i and 2 i + 1's: its key and weight (0 behind the last), and how
+    // many stand before it and what they weigh.  Leaves the keys and weights in pairs in s.stage.
+    __device__ __forceinline__ void compare(int n, uint64_t &key, uint64_t &w, int &rank_, uint64_t &before) const {
         static_assert(2 * kFew <= kThreads && 2 * kFew <= kList, "two threads a token");
         ulonglong2 *pair = reinterpret_cast<ulonglong2 *>(s.stage);
         const int i = tid >> 1;
-        uint64_t key = 0, w = 0;
+        key = w = before = 0;
+        rank_ = 0;
         if (i < n) {
             key = s.list[i];
             w = W(key_value(key));
             if ((tid & 1) == 0) pair[i] = make_ulonglong2(key, w);
         }
         __syncthreads();
-        uint64_t before = 0;
-        int rank_ = 0;
         if (i - (lane >> 1) < n) {  // (whole warps)
             for (int j = tid & 1; j < n; j += 2) {
                 const ulonglong2 o = pair[j];
@@ -511,6 +511,14 @@ struct Sampler {
         }
         before += __shfl_xor_sync(0xffffffffu, before, 1);
         rank_ += __shfl_xor_sync(0xffffffffu, rank_, 1);
+    }
+    // The same for at most kFew tokens: each is compared with all, by two threads.
+    __device__ __forceinline__ void finish_few(int n, int k, uint64_t part, uint64_t lim, uint64_t least) const {
+        ulonglong2 *pair = reinterpret_cast<ulonglong2 *>(s.stage);
+        const int i = tid >> 1;
+        uint64_t key, w, before;
+        int rank_;
+        compare(n, key, w, rank_, before);
         const bool mine = i < n && rank_ < k;
         if (lim == 0) lim = share_of(cta_sum(mine && (tid & 1) == 0 ? w : 0), part, true);
         if (!mine || before >= lim || w < least) w = 0;
@@ -661,17 +669,28 @@ struct Sampler {
     }
 
     // ------------------------------------------- exact search, digit by digit
-    // Rank 0: the listed token at which tokens, or weights, reach `target`, c0 and w0 of them being before
-    // the list: told with the weights up to and with it (0: none).
-    __device__ __forceinline__ void resolve(int n, bool weights, uint64_t c0, uint64_t w0, uint64_t target) const {
+    // Rank 0: the token of a list whose octaves lie between -from and -to at which tokens, or weights, reach
+    // `target`, c0 and w0 of them being before the list: told with the weights up to and with it (0: none).
+    __device__ __forceinline__ void resolve(int n, float from, float to, bool weights, uint64_t c0, uint64_t w0,
+                                            uint64_t target) const {
+        if (tid == 0) tell(Word{0, 0, 0, 0});
+        auto look = [&](uint64_t key, uint64_t rank_, uint64_t before, uint64_t w) {
+            const bool is = weights ? w0 + before < target && target <= w0 + before + w : c0 + rank_ + 1 == target;
+            if (is) tell(Word{key, w0 + before + w, 0, 0});
+        };
+        if (n <= kFew) {
+            uint64_t key, w, before;
+            int rank_;
+            compare(n, key, w, rank_, before);  // (a barrier in it stands between the tellings)
+            if ((tid & 1) == 0 && (tid >> 1) < n) look(key, (uint64_t)rank_, before, w);
+            return;
+        }
+        sort_list(n, from, to);
         uint64_t *upto = s.stage;
         scan(upto, n, [&](int i) { return listed(i); });
-        if (tid == 0) tell(Word{0, 0, 0, 0});
-        __syncthreads();
         for (int i = tid; i < n; i += kThreads) {
-            const uint64_t w = w0 + (i > 0 ? upto[i - 1] : 0), here = w0 + upto[i];
-            const bool is = weights ? w < target && target <= here : c0 + i + 1 == target;
-            if (is) tell(Word{s.list[i], here, 0, 0});
+            const uint64_t before = i > 0 ? upto[i - 1] : 0;
+            look(s.list[i], (uint64_t)i, before, upto[i] - before);
         }
     }
 
@@ -753,8 +772,7 @@ struct Sampler {
                 });
                 const int n = collect();
                 if (first()) {
-                    sort_list(n, 0.f, kReach);
-                    resolve(n, weights, c0, w0, target);
+                    resolve(n, 0.f, kReach, weights, c0, w0, target);
                 }
                 cluster_sync();
                 break;
@@ -895,8 +913,7 @@ struct Sampler {
                 if (n <= kList && n > 0) {
                     if (whole_list) return finish(n, false, 0, 0, target, least, (float)(b1 + 1) / scale);
                     if (first()) {
-                        sort_list(n, (float)b0 / scale, (float)(b1 + 1) / scale);
-                        resolve(n, true, 0, sum_above, target);
+                        resolve(n, (float)b0 / scale, (float)(b1 + 1) / scale, true, 0, sum_above, target);
                     }
                     cluster_sync();
                     cut = s.word.a;
