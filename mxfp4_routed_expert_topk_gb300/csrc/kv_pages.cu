@@ -12,8 +12,9 @@
 // before the call is known to succeed, so a call that cannot be served changes nothing.
 //
 // What bounds it is the chain: 64 sequences of which few need a page take 6 us (three loads one after
-// the other, sums, the cluster's barriers).  512 sequences that take TTT pages of 400000 and map 77000
-// rows take MMM us; with the places looked up by the warps that find the pages 34.
+// the other, sums, the cluster's barriers).  512 sequences that take 7200 pages of 400000 and map 115000
+// rows take 28 us (counting 4, handing out 7, rows 10); with the places looked up by the warps that find the
+// pages, and one row of a thread at a time, 48.  Called from Python either takes 35 to 45.
 #include <algorithm>
 
 #include "kv_internal.cuh"
