@@ -11,10 +11,11 @@
 // then looks up one or two places in the line of (sequence, column) for its pages.  Nothing is written
 // before the call is known to succeed, so a call that cannot be served changes nothing.
 //
-// What bounds it is the chain: 64 sequences of which few need a page take 6 us (three loads one after
-// the other, sums, the cluster's barriers).  512 sequences that take 7200 pages of 400000 and map 115000
-// rows take 28 us (counting 4, handing out 7, rows 10); with the places looked up by the warps that find the
-// pages, and one row of a thread at a time, 48.  Called from Python either takes 35 to 45.
+// What bounds it is the chain: 64 sequences of which none needs a page take 6 us (3 of them loads one
+// after the other and sums).  512 sequences that take 7200 pages of 400000 and map 115000 rows take 31 us
+// (by stamps: needs 4, counting 6, exchange 2, handing out 8, rows 10; the rest is start and end); where
+// the warps that find the pages also looked up their places it was 57.  Called from Python either takes 35
+// to 45.
 #include <algorithm>
 
 #include "kv_internal.cuh"

@@ -19,12 +19,14 @@
 //   - where the list does not hold them (thousands of equal logits) or a larger top-k is asked for, the cut
 //     is found digit by digit in exact histograms.
 //
-// Measured on the device: one row of 32001 values 10 (top-k of 1) to 26 us (top-p alone); 256 rows of
-// 131072, settings mixed, 128 us, where rows with a top-k take 25 to 50 each with 152 under way and rows of
-// top-p alone 110; distributions of 96 rows of 131071, top-p alone, 110 us (29 % of the FMA and ALU pipes, 38 %
-// of the issue slots; half of the stalls wait for L2).  Not better: copying a row's vectors ahead into shared
-// memory (96 rows 123 us), four vectors' loads in flight per thread (113; with their arithmetic unrolled 187),
-// listing the largest 1024 first for top-p alone (150), functions called in place of inlined (137).
+// Measured on the device: one row of 32001 values 5 (its largest), 10 (top-k of 1), 12 (50), 20 (1000), 24 to 29 us
+// (top-p alone); 256 rows of 131072, settings mixed, 128 us, where rows of top-p alone (a twelfth) take 110 each
+// and those with a top-k 38 to 54, many under way together; distributions of 96 rows of 131071, top-p alone, 109 us
+// (29 and 27 % of the ALU and FMA pipes, 39 % of the issue slots; waits for loads are the commonest stall).  Not better
+// (each against the kernel as it then was): copying a row's vectors ahead into shared memory, 96 rows 123 us
+// against 110; four vectors' loads in flight per thread 113 against 110, with their arithmetic unrolled 187
+// against 134; listing the largest 1024 first for top-p alone 150 against 130; functions called in place of
+// inlined 137 against 114.
 #include <algorithm>
 
 #include "vocab_row.cuh"
