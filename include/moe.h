@@ -432,7 +432,7 @@ moe_status moe_kv_attention_shared(const moe_kv *kv, int layer, const uint16_t *
  * count or length, more tokens than the table has room for or 2^30, more than `rows` rows in all, or
  * new rows that would join tokens in a page that is not held once (MOE_ERR_BAD_PAGE), the table and
  * the counts stay as they were, cu_rows becomes all 0 and kv_len = start.  A sequence without new
- * rows may have any length.  seqs <= 16384, n_pages <= 2^24.
+ * rows may have any length.  seqs <= 16384, n_pages <= 2^24, rows <= 2^30.
  *
  * moe_kv_release gives back what tokens keep[b] .. kv_len[b]-1 occupied (rejected drafts; keep 0:
  * a finished sequence): columns ceil(keep / page_tokens) .. ceil(kv_len / page_tokens) - 1 become -1

@@ -452,6 +452,7 @@ moe_status moe_kv_reserve(const int32_t *new_rows, const int32_t *start, int seq
     if (s != MOE_OK) return s;
     if (rows < 0 || cu_rows == nullptr || (seqs > 0 && (new_rows == nullptr || start == nullptr || kv_len == nullptr)))
         return MOE_ERR_INVALID_ARG;
+    if (rows > (1 << 30)) return MOE_ERR_UNSUPPORTED_SHAPE;  // (rows are counted in 32 bits, some past the last)
     KvReserveArgs a = {new_rows, start,   seqs,   page_table, table_width, refs,    n_pages,         page_tokens,
                        rows,     cu_rows, kv_len, row_seq,    row_pos,     row_slot, (StatusWord *)ws};
     return cuda_status(launch_kv_reserve(a, (cudaStream_t)stream));

@@ -72,6 +72,7 @@ def test_pages_refusals(L):
         assert f(n=255) == moe.MOE_ERR_WORKSPACE
     for bad in (dict(new=None), dict(start=None), dict(cu=None), dict(rows=-1)):
         assert reserve(**bad) == BAD, bad
+    assert reserve(rows=(1 << 30) + 1) == moe.MOE_ERR_UNSUPPORTED_SHAPE
     assert release(keep=None) == BAD
     assert release(seqs=0, keep=None, lens=None, table=None) == moe.MOE_OK
 
