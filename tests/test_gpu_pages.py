@@ -301,3 +301,39 @@ def test_refusals():
         moe.moe_kv_reserve(n, n, t, r, 16, 2, row_slot=dev([0, 0]))
     with pytest.raises(ValueError):
         moe.moe_kv_release(n, dev([1]), t, r, 16)
+
+
+def test_as_many_sequences_as_there_may_be():
+    r = np.random.default_rng(5)
+    c = Pool(16384, 12, 16384 * 6 + 11, 16, held=[0, 7, 9])
+    c.reserve(r.integers(0, 40, 16384))
+    c.reserve(r.integers(0, 3, 16384))
+    c.release(np.maximum(c.len - 9, 0))
+    c.reserve(r.integers(0, 60, 16384))
+
+
+def test_as_many_pages_as_there_may_be():
+    """2^24 pages, of which few are free: the last ones and some in between."""
+    n_pages = 1 << 24
+    free = torch.tensor([5, 4095, 4096, 9000001] + list(range(n_pages - 300, n_pages)), device="cuda")
+    refs = torch.ones(n_pages, dtype=torch.int32, device="cuda")
+    refs[free] = 0
+    table = torch.full((4, 100), -1, dtype=torch.int32, device="cuda")
+    ws = moe.workspace(moe.moe_kv_pages_workspace_size(4, n_pages))
+    n = [128 * 100, 1, 128 * 99 + 1, 128 * 100]
+    cu, total, seq, pos, slot = moe.moe_kv_reserve(dev(n), dev([0] * 4), table, refs, 128, sum(n), ws=ws)
+    assert moe.moe_check_status(ws) == moe.MOE_OK
+    want = free[:301].tolist()
+    got = table.tolist()
+    assert got[0] + got[1][:1] + got[2] + got[3] == want and got[1][1:] == [-1] * 99
+    assert refs.sum().item() == n_pages - len(free) + 301 and (refs[free[:301]] == 1).all()
+    at = 0
+    for b, m in enumerate(n):
+        pages = torch.tensor(got[b], device="cuda").long()
+        t = torch.arange(m, device="cuda")
+        assert torch.equal(slot[at:at + m], pages[t // 128] * 128 + t % 128)
+        assert (seq[at:at + m] == b).all() and torch.equal(pos[at:at + m].long(), t)
+        at += m
+    moe.moe_kv_release(dev([0] * 4), total, table, refs, 128, ws=ws)
+    assert moe.moe_check_status(ws) == moe.MOE_OK
+    assert refs.sum().item() == n_pages - len(free) and (table == -1).all()
