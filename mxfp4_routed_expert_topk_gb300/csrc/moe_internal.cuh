@@ -203,23 +203,28 @@ inline cudaError_t device_attr(cudaDeviceAttr attr, PerDevice &cache, int *out) 
     return cudaSuccess;
 }
 
-// Raise a kernel's dynamic shared memory limit on the current device to `bytes` if
-// needed (per kernel and device, remembered in `cur`, init 0).  Returns the error of
-// the attribute call.
+// Raise a kernel's dynamic shared memory limit on the current device, if `bytes` asks for it, to all
+// that its static shared memory leaves of a block's largest (so threads that make their first calls
+// together set the same).  `cur`, init 0, keeps the limit per device; CUDA's 48 KB without this
+// are static and dynamic together.  Returns the error of the attribute call.
 template <typename K>
 inline cudaError_t ensure_dynamic_smem(K kernel, size_t bytes, PerDevice &cur) {
-    if (bytes <= 48 * 1024) return cudaSuccess;
     int dev = 0;
     cudaError_t e = current_device(&dev);
     if (e != cudaSuccess) return e;
-    if ((int)bytes <= cur.v[dev].load(std::memory_order_relaxed)) return cudaSuccess;
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
-    if (e == cudaSuccess) {
-        int old = cur.v[dev].load(std::memory_order_relaxed);
-        while (old < (int)bytes && !cur.v[dev].compare_exchange_weak(old, (int)bytes, std::memory_order_relaxed)) {
-        }
+    if (bytes <= (size_t)cur.v[dev].load(std::memory_order_relaxed)) return cudaSuccess;
+    cudaFuncAttributes f;
+    if ((e = cudaFuncGetAttributes(&f, kernel)) != cudaSuccess) return e;
+    int limit = 48 * 1024 - (int)f.sharedSizeBytes;
+    if ((int64_t)bytes > limit) {
+        int most = 0;
+        if ((e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev)) != cudaSuccess) return e;
+        limit = most - (int)f.sharedSizeBytes;
+        if ((int64_t)bytes > limit) return cudaErrorInvalidValue;
+        if ((e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, limit)) != cudaSuccess) return e;
     }
-    return e;
+    cur.v[dev].store(limit, std::memory_order_relaxed);
+    return cudaSuccess;
 }
 
 // Launch helpers implemented per translation unit.
