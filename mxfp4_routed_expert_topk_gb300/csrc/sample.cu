@@ -71,6 +71,7 @@ struct Smem {
     };
     uint64_t list[kList];       // rank 0's: keys
     uint64_t cta[3][kMaxCluster];
+    uint64_t key[kMaxCluster];  // every CTA's first token of the order
     uint64_t warp[kWarps];
     uint64_t wscan[kWarps];
     uint32_t wcnt[kWarps];
@@ -264,8 +265,10 @@ struct Sampler {
     }
     __device__ __forceinline__ uint64_t key_of(float x, int i) const { return order_key(x, i); }
 
-    // Sum of the CTAs' values (each thread's own), in all of them; `upto`: of the CTAs before this one,
-    // `cta`: of this one.  Leaves the warps' sums in s.warp.
+    // Sum of the CTAs' values (each thread's own), in all of them; `before`: of the CTAs before this one,
+    // `cta`: of this one.  Leaves the warps' sums in s.warp.  A round's slot may be stored to again once a
+    // barrier of the cluster stands between: sums that follow one another take different rounds, as the later
+    // one's own barrier then frees the earlier one's slot.
     __device__ __forceinline__ uint64_t add_up(uint64_t v, int round, uint64_t &before, uint64_t &cta) const {
 #pragma unroll
         for (int d = 16; d > 0; d >>= 1) v += __shfl_xor_sync(0xffffffffu, v, d);
@@ -837,13 +840,13 @@ struct Sampler {
                                : kNone;
         cluster_wait();
         if (tid < (int)ranks) {
-            store_cluster_u64(&s.cta[0][rank], (uint32_t)tid, key);
+            store_cluster_u64(s.key + rank, (uint32_t)tid, key);  // (a place of its own: a sum may follow at once)
             store_cluster_u32(&s.low[rank], (uint32_t)tid, __float_as_uint(bound));
         }
         cluster_sync();
         float low = INFINITY;
         for (uint32_t q = 0; q < ranks; q++) {
-            key = max(key, s.cta[0][q]);
+            key = max(key, s.key[q]);
             low = fminf(low, __uint_as_float(s.low[q]));
         }
 

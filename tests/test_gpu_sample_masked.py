@@ -1,0 +1,107 @@
+"""GPU: sampling from vocabularies of which many tokens are masked, or hold infinities or NaN, at sizes that a
+small list does not hold, with every cut; compared exactly, as in the other tests of sampling."""
+import math
+
+import pytest
+import torch
+
+from tests.test_gpu_sample import check, dev
+
+pytestmark = pytest.mark.gpu
+
+moe = pytest.importorskip("mxfp4_routed_expert_topk_gb300")
+
+INF, NAN, LOW = math.inf, math.nan, -3.3895314e38  # (the lowest bf16)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    moe.build()
+
+
+def rows_of(V, dtype, seed=0):
+    """Rows that differ in what is left of them."""
+    g = torch.Generator(device="cuda").manual_seed(V + seed)
+    x = torch.randn((22, V), generator=g, device="cuda") * 3
+    order = torch.randperm(V, generator=g, device="cuda")
+    at = torch.arange(V, device="cuda")
+
+    def only(r, where):
+        y = torch.full((V,), -INF, device="cuda")
+        y[where] = x[r, where]
+        x[r] = y
+
+    x[0] = -INF
+    x[1] = NAN
+    only(2, order[:1])
+    only(3, at[-5:])
+    only(4, order[:300])
+    only(5, order[:1024])
+    only(6, order[:1025])
+    only(7, order[:V // 2])
+    only(8, at[:V // 2])                       # whole CTAs without a token
+    only(9, at[V // 2:])
+    only(10, at[-1:])
+    x[11, ::2] = NAN
+    x[12, order[0]] = INF
+    x[13, order[:3]] = INF
+    x[14, order[:2048 + V // 64]] = INF        # more than the list holds
+    x[15] = INF
+    x[16] = LOW
+    x[17, order[100:]] = LOW                   # a mask of the lowest value
+    x[18] = torch.where(at % 3 == 0, NAN, -INF)
+    x[19, order[:7]] = 3.0e38
+    x[20, order[:2]], x[20, order[2:V // 3]], x[20, order[V // 3:V // 2]] = INF, NAN, LOW
+    only(21, order[:40])
+    x[21, order[:40]] = 1.0                    # as many equal ones as are left
+    return x.to(dtype)
+
+
+def in_place(x, T, probs, k=None, p=None, m=None, **_):
+    moe.moe_sample_probs(x, dev(T), top_k=dev(k, torch.int32), top_p=dev(p), min_p=dev(m), probs=x)
+    assert torch.equal(x, probs)
+
+
+CUTS = [dict(), dict(k=5), dict(k=50, p=0.9), dict(k=1024), dict(k=1025), dict(k=1500, p=0.99, m=0.001), dict(k=-1, p=0.3),
+        dict(p=0.999), dict(p=0.5, m=0.01), dict(m=0.2), dict(k=3000, p=0.5)]
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V", [2049, 2056, 5003, 70000, 131071])
+def test_rows_with_little_left(V, dtype):
+    x = rows_of(V, dtype)
+    R = len(x)
+    for i, cut in enumerate(CUTS + [dict(k=V - 1)]):
+        s = {n: [v] * R for n, v in cut.items()}
+        T, u = [1.0] * R, [(0.07 + 0.31 * (i + r)) % 1.0 for r in range(R)]
+        _, probs = check(x, T, u=u, **s)
+        in_place(x.clone(), T, probs, **s)
+
+
+@pytest.mark.parametrize("T", [0.0, -1.0, NAN, 1e-45, 1e-3, 0.2, 1e3, 3e38, INF])
+@pytest.mark.parametrize("V", [2049, 20000])
+def test_temperatures(V, T):
+    x = rows_of(V, torch.float32, seed=1)
+    R = len(x)
+    for cut in (dict(), dict(k=40), dict(k=1100, p=0.9), dict(p=0.7), dict(p=0.95, m=0.001)):
+        check(x, [T] * R, u=[0.83] * R, **{n: [v] * R for n, v in cut.items()})
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V,times", [(2049, 30), (2305, 1), (4099, 12), (9001, 5)])
+def test_many_rows_without_a_bound(V, times, dtype):
+    """A top-k that no list holds, next to others, with clusters of every size: the first token of the order, the
+    counts and the sums of a row's CTAs are exchanged one right after the other."""
+    x = torch.cat([rows_of(V, dtype, seed=i) for i in range(times)])
+    R = len(x)
+    k = [(1025, 1500, V - 1, 2000, 60)[r % 5] for r in range(R)]
+    p = [(1.0, 0.9, 0.5, 0.99)[r % 4] for r in range(R)]
+    u = [((r * 37) % 101) / 101 for r in range(R)]
+    got, probs = check(x, [0.9] * R, k=k, p=p, u=u)
+    in_place(x.clone(), [0.9] * R, probs, k=k, p=p)
+    args = dict(top_k=dev(k, torch.int32), top_p=dev(p))
+    for _ in range(20):
+        assert moe.moe_sample(x, dev([0.9] * R), dev(u), **args).tolist() == got
+        assert torch.equal(moe.moe_sample_probs(x, dev([0.9] * R), **args), probs)
