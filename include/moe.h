@@ -469,8 +469,8 @@ moe_status moe_kv_release(const int32_t *keep, const int32_t *kv_len, int seqs, 
  * the lowest index i at which the kept weights of tokens 0 .. i sum to more than floor(S t / 2^24).
  * moe_sample_probs: probs [rows][vocab] in `dtype`, row r at probs + r * ldp, the kept weights divided
  * by S (both rounded to fp32, then to `dtype`), 0 elsewhere: what moe_verify_sampled takes as p or q.
- * probs may be x itself (with ldp = ld).  temperature <= 0 or NaN: the first token of the order (probability 1), whatever
- * the cuts.  A row of nothing but NaN and -infinity: next = -1, probabilities 0.
+ * probs may be x itself (with ldp = ld); rows of the two overlap in no other way.  temperature <= 0 or NaN: the first token
+ * of the order (probability 1), whatever the cuts.  A row of nothing but NaN and -infinity: next = -1, probabilities 0.
  * ws: moe_sample_workspace_size() bytes. */
 moe_status moe_sample_workspace_size(int rows, int vocab, size_t *bytes);
 moe_status moe_sample(const void *x, size_t ld, int dtype, int rows, int vocab, const float *temperature,

@@ -215,12 +215,12 @@ __device__ __forceinline__ int digit_bits(int level) { return level == 3 ? 2 : 1
 // ------------------------------------------------------- a row, by a cluster
 template <bool BF16, bool PROBS>
 struct Sampler {
-    static constexpr int kVec = Row<BF16>::kVec;
+    static constexpr int kVec = Row<BF16, PROBS>::kVec;
     const SampleArgs &a;
     Smem &s;
     const uint32_t rank, ranks;
     const int tid, lane, warp, row;
-    const Row<BF16> X;
+    const Row<BF16, PROBS> X;  // (the probabilities may be written over the logits)
     int v0, v1;     // this warp's vectors
     bool infinite;  // the row's largest is +infinity: those are 0, everything else -infinity
     Weigh W;

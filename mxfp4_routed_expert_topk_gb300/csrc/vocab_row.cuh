@@ -36,8 +36,9 @@ __device__ __forceinline__ uint32_t max2_bf16(uint32_t a, uint32_t b) {
 }
 
 // A row of n values, cut into vectors of 16 bytes on 16-byte boundaries: vector 0 is the
-// (possibly partial) one that holds the row's first value.
-template <bool BF16>
+// (possibly partial) one that holds the row's first value.  WRITTEN: the kernel writes to the row, too, so
+// that its loads may not go the way that is for constant memory.
+template <bool BF16, bool WRITTEN = false>
 struct Row {
     static constexpr int kVec = BF16 ? 8 : 4;
     static constexpr int kSize = BF16 ? 2 : 4;
@@ -54,12 +55,16 @@ struct Row {
     __device__ __forceinline__ float at(int i) const {
         return BF16 ? bf16_bits_to_float(reinterpret_cast<const uint16_t *>(p)[i]) : reinterpret_cast<const float *>(p)[i];
     }
+    __device__ __forceinline__ uint4 load16(int i) const {  // from value i on
+        const uint4 *q = reinterpret_cast<const uint4 *>(p + (ptrdiff_t)i * kSize);
+        return WRITTEN ? __ldcg(q) : __ldg(q);
+    }
     // largest value of vector v (NaN if it has none)
     __device__ __forceinline__ float largest(int v) const {
         if constexpr (BF16) {
             const int i0 = first(v);
             if (i0 >= 0 && i0 + kVec <= n) {
-                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p + (ptrdiff_t)i0 * kSize));
+                const uint4 u = load16(i0);
                 const uint32_t m = max2_bf16(max2_bf16(u.x, u.y), max2_bf16(u.z, u.w));
                 return fmaxf(__uint_as_float(m << 16), __uint_as_float(m & 0xffff0000u));
             }
@@ -75,7 +80,7 @@ struct Row {
     __device__ __forceinline__ void load(int v, float none, float (&x)[kVec]) const {
         const int i0 = first(v);
         if (i0 >= 0 && i0 + kVec <= n) {
-            const uint4 u = __ldg(reinterpret_cast<const uint4 *>(p + (ptrdiff_t)i0 * kSize));
+            const uint4 u = load16(i0);
             const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
             for (int k = 0; k < 4; k++) {

@@ -105,3 +105,21 @@ def test_many_rows_without_a_bound(V, times, dtype):
     for _ in range(20):
         assert moe.moe_sample(x, dev([0.9] * R), dev(u), **args).tolist() == got
         assert torch.equal(moe.moe_sample_probs(x, dev([0.9] * R), **args), probs)
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("V,lead", [(2051, 1), (5003, 3), (40007, 0), (40007, 7)])
+def test_over_the_logits_at_any_address(V, lead, dtype):
+    """Rows that begin and end inside a vector, written over while other CTAs of the row still read theirs, each
+    call into the values that the one before has left."""
+    rows = rows_of(V, dtype, seed=lead)
+    R = len(rows)
+    wide = torch.full((R, V + 9), 100.0, dtype=dtype, device="cuda")  # (what is not of a row would win)
+    x = wide[:, lead:lead + V]
+    for cut in (dict(), dict(k=30), dict(k=1100), dict(p=0.9), dict(k=1100, p=0.8, m=0.001)):
+        x.copy_(rows)
+        s = {n: [v] * R for n, v in cut.items()}
+        for T in (1.0, 0.0):
+            _, probs = check(x.clone(), [T] * R, **s)
+            in_place(x, [T] * R, probs, **s)
+        assert (wide[:, :lead] == 100).all() and (wide[:, lead + V:] == 100).all()
