@@ -436,9 +436,9 @@ moe_status moe_kv_attention_shared(const moe_kv *kv, int layer, const uint16_t *
  *
  * moe_kv_release gives back what tokens keep[b] .. kv_len[b]-1 occupied (rejected drafts; keep 0:
  * a finished sequence): columns ceil(keep / page_tokens) .. ceil(kv_len / page_tokens) - 1 become -1
- * and their pages' counts fall by one each.  keep >= kv_len gives nothing back.  A negative keep, a
- * length past the table (the sequence is left alone), or an entry that names no held page, is
- * reported as MOE_ERR_BAD_PAGE.
+ * and their pages' counts fall by one each.  keep >= kv_len, not negative, gives nothing back, whatever the
+ * length.  A negative keep, a length past the table with a keep below it (the sequence is left alone in
+ * either case), or an entry that names no held page, is reported as MOE_ERR_BAD_PAGE.
  *
  * page_tokens 16, 32, 64 or 128.  ws: moe_kv_pages_workspace_size() bytes (the status word). */
 moe_status moe_kv_pages_workspace_size(int seqs, int n_pages, size_t *bytes);

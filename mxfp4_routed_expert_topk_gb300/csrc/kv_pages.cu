@@ -281,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, 1) kv_reserve_kernel(const KvReserve
 // A block per sequence: its dropped columns.
 __global__ void __launch_bounds__(128) kv_release_kernel(const KvReleaseArgs a) {
     const int b = blockIdx.x, keep = a.keep[b], len = a.kv_len[b];
-    if (len <= keep) return;
+    if (keep >= 0 && len <= keep) return;
     if (keep < 0 || (int64_t)len > (int64_t)a.table_width * a.page) {
         if (threadIdx.x == 0) set_status(a.st, MOE_ERR_BAD_PAGE, 1);
         return;
