@@ -273,8 +273,10 @@ __device__ __forceinline__ Line cut_line(const AttnArgs &a, int64_t *sums, Start
     const int per = (items + NT - 1) / NT;
     const int i0 = min(tid * per, items), i1 = min(i0 + per, items);
     if (SHARED && a.what == kWhole && blockIdx.x == 0) {  // (else the groups themselves are the items)
-        for (int g = tid; g < a.groups; g += NT)
-            if (a.cu_groups[g] > a.cu_groups[g + 1]) set_status(a.k.st, MOE_ERR_BAD_PAGE, 1);
+        for (int g = tid; g < a.groups; g += NT) {
+            const int g0 = a.cu_groups[g], g1 = a.cu_groups[g + 1];
+            if (g0 > g1 || (g == 0 && g0 != 0) || (g + 1 == a.groups && g1 != a.k.seqs)) set_status(a.k.st, MOE_ERR_BAD_PAGE, 1);
+        }
     }
     // two rounds over the thread's items: their sum, then those that hold the workers' starts
     Line l;
