@@ -67,9 +67,10 @@ struct AttnArgs {
     const int32_t *cu_groups, *prefix_len;
     int groups, group_rows;  // groups, and the most rows of one
     SharedPart what;
-    // outputs over the prefixes in fp32 [rows][heads_q][dim], and the base-2 logarithms of their sums
-    // [rows][heads_q]: written over prefixes, and added to what is found over own tokens
-    float *half, *half_lse;
+    // sums over the prefixes in fp32 [rows][heads_q][dim], and the references and sums of weights that they go
+    // by [rows][heads_q]: written over prefixes, and added to what is found over own tokens
+    float *half;
+    float2 *half_ml;
 };
 
 namespace {
@@ -867,18 +868,21 @@ __device__ __forceinline__ const uint8_t *value_codes(const AttnArgs &a, const S
     return a.k.kv.codes(page, a.k.layer, 1, g.head) + (size_t)(t % P) * a.k.kv.dim;
 }
 
-// A row's result over its own tokens (e: the base-2 logarithm of its sum) with that over the prefix of
-// its group.
+// A row's sums over its own tokens (by reference `ref`; l: of its weights) with those over the prefix of its
+// group.  References hold value scales, as everywhere: a part whose weights are far below the other's may
+// still have the larger products.
 struct Halves {
     float own, prefix, lse;  // factors of the two; the logarithm of the whole sum
-    __device__ __forceinline__ Halves(const AttnArgs &a, size_t at, float e) {
-        // (a half that saw nothing has 0 and -infinity; NaN stays)
-        const float p = a.what == kOwn ? __ldg(a.half_lse + at) : -INFINITY, m = fmaxf(e, p);
-        const float we = e == -INFINITY ? 0.f : ex2(e - m), wp = p == -INFINITY ? 0.f : ex2(p - m);
-        const float l = we + wp, inv = l == 0.f ? 0.f : 1.f / l;
-        own = we * inv;
-        prefix = wp * inv;
-        lse = l == 0.f ? -INFINITY : kLn2 * (m + log2f(l));
+    __device__ __forceinline__ Halves(const AttnArgs &a, size_t at, float ref, float l) {
+        const float2 p = a.what == kOwn ? __ldg(a.half_ml + at) : make_float2(-INFINITY, 0.f);
+        const float m = fmaxf(ref, p.x);
+        // (as roots: a sum may be large where its reference is more than 126 below; sum 0: it saw nothing; NaN stays)
+        own = l == 0.f ? 0.f : ex2(0.5f * (ref - m));
+        prefix = p.y == 0.f ? 0.f : ex2(0.5f * (p.x - m));
+        const float all = fmaf(own * l, own, prefix * p.y * prefix), inv = all == 0.f ? 0.f : 1.f / all;
+        lse = all == 0.f ? -INFINITY : kLn2 * (m + log2f(all));
+        own *= own * inv;
+        prefix *= prefix * inv;
     }
     __device__ __forceinline__ float add(float o, float p) const { return fmaf(o, own, p * prefix); }
 };
@@ -983,24 +987,23 @@ __device__ __forceinline__ void join_role(const AttnArgs &a, const Line &line, i
             }
             const int R = g.rt * a.rpt + r, qi = R / a.group, row = g.row0 + qi;
             const int hq = g.head * a.group + R - qi * a.group;
-            const float inv = l == 0.f ? 0.f : 1.f / l;
             uint16_t *out = a.k.out + (size_t)row * a.k.ldo + (size_t)hq * D + lane * V;
             if constexpr (SHARED) {
                 const size_t at = (size_t)row * a.k.heads_q + hq;
                 float *half = a.half + at * D + lane * V;
-                const float e = l == 0.f ? -INFINITY : m + log2f(l);
                 if (a.what == kPrefixes) {
 #pragma unroll
-                    for (int j = 0; j < V; j++) half[j] = acc[j] * inv;
-                    if (lane == 0) a.half_lse[at] = e;
+                    for (int j = 0; j < V; j++) half[j] = acc[j];
+                    if (lane == 0) a.half_ml[at] = make_float2(m, l);
                     continue;
                 }
-                const Halves h(a, at, e);
+                const Halves h(a, at, m, l);
 #pragma unroll
                 for (int j = 0; j < V; j++)
-                    out[j] = __bfloat16_as_ushort(__float2bfloat16(h.add(acc[j] * inv, a.what == kOwn ? __ldg(half + j) : 0.f)));
+                    out[j] = __bfloat16_as_ushort(__float2bfloat16(h.add(acc[j], a.what == kOwn ? __ldg(half + j) : 0.f)));
                 if (a.k.lse != nullptr && lane == 0) a.k.lse[at] = h.lse;
             } else {
+                const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll
                 for (int j = 0; j < V; j++) out[j] = __bfloat16_as_ushort(__float2bfloat16(acc[j] * inv));
                 if (a.k.lse != nullptr && lane == 0)

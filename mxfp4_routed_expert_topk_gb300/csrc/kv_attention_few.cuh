@@ -478,13 +478,12 @@ __global__ void __launch_bounds__(kFewThreads, 1) kv_attention_few_kernel(const 
             float lse_shared = 0.f;
             float *part = part_of ? a.part + (size_t)(2 * worker + (tile0 == 0 ? 1 : 0)) * slot_floats : nullptr;
             // (a row that saw nothing is told by its sum; NaN stays)
-            ab[row].y = part_of ? 1.f : l == 0.f ? 0.f : 1.f / l;
+            ab[row].y = part_of || (SHARED && a.what == kPrefixes) ? 1.f : l == 0.f ? 0.f : 1.f / l;
             const bool live = *(volatile int *)abort_flag == 0;
             if constexpr (SHARED) {
                 if (!part_of && a.what != kPrefixes && rows[row].row >= 0) {
-                    const Halves h(a, (size_t)rows[row].row * a.k.heads_q + rows[row].head,
-                                   l == 0.f ? -INFINITY : m_run + log2f(l));
-                    ab[row] = make_float2(h.prefix, h.own * (l == 0.f ? 0.f : 1.f / l));
+                    const Halves h(a, (size_t)rows[row].row * a.k.heads_q + rows[row].head, m_run, l);
+                    ab[row] = make_float2(h.prefix, h.own);
                     lse_shared = h.lse;
                 }
             }
@@ -492,7 +491,7 @@ __global__ void __launch_bounds__(kFewThreads, 1) kv_attention_few_kernel(const 
                 if (part_of)
                     *reinterpret_cast<float2 *>(part + (size_t)R * D + 2 * row) = make_float2(m_run, l);
                 else if (SHARED && a.what == kPrefixes)
-                    a.half_lse[(size_t)rows[row].row * a.k.heads_q + rows[row].head] = l == 0.f ? -INFINITY : m_run + log2f(l);
+                    a.half_ml[(size_t)rows[row].row * a.k.heads_q + rows[row].head] = make_float2(m_run, l);
                 else if (SHARED && a.k.lse != nullptr)
                     a.k.lse[(size_t)rows[row].row * a.k.heads_q + rows[row].head] = lse_shared;
                 else if (a.k.lse != nullptr)

@@ -737,22 +737,20 @@ __global__ void __launch_bounds__(kThreads, 1) kv_attention_rows_kernel(const __
                         *reinterpret_cast<float4 *>(d + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
                     *reinterpret_cast<float2 *>(part + (size_t)a.rpt * D + 2 * row) = make_float2(m_run, l_run);
                 } else if (SHARED && a.what == kPrefixes) {
-                    const float inv = l_run == 0.f ? 0.f : 1.f / l_run;
                     const size_t at = (size_t)ri.row * a.k.heads_q + ri.head;
                     float *d = a.half + at * D;
 #pragma unroll
                     for (int i = 0; i < D; i += 4)
-                        *reinterpret_cast<float4 *>(d + i) =
-                            make_float4(o[i] * inv, o[i + 1] * inv, o[i + 2] * inv, o[i + 3] * inv);
-                    a.half_lse[at] = l_run == 0.f ? -INFINITY : m_run + log2f(l_run);
+                        *reinterpret_cast<float4 *>(d + i) = make_float4(o[i], o[i + 1], o[i + 2], o[i + 3]);
+                    a.half_ml[at] = make_float2(m_run, l_run);
                 } else {
                     float inv = l_run == 0.f ? 0.f : 1.f / l_run;  // (sum 0: it saw nothing; NaN stays)
                     float lse = 0.f;
                     if constexpr (SHARED) {
                         const size_t at = (size_t)ri.row * a.k.heads_q + ri.head;
-                        const Halves h(a, at, l_run == 0.f ? -INFINITY : m_run + log2f(l_run));
+                        const Halves h(a, at, m_run, l_run);
                         lse = h.lse;
-                        inv *= h.own;
+                        inv = h.own;
                         if (a.what == kOwn) {
                             const float4 *p = reinterpret_cast<const float4 *>(a.half + at * D);
 #pragma unroll

@@ -3,10 +3,10 @@
 //
 // Every row of a group sees all of its prefix, so a row's result is
 //
-//   o = (2^(e1 - m) o1 + 2^(e2 - m) o2) / (2^(e1 - m) + 2^(e2 - m)),  m = max(e1, e2)
+//   o = (2^(m1 - m) o1 + 2^(m2 - m) o2) / (2^(m1 - m) l1 + 2^(m2 - m) l2),  m = max(m1, m2)
 //
-// with o1, o2 its attention over the prefix and over the sequence's own tokens and e1, e2 the base-2
-// logarithms of their sums.  The first is one problem per group, with all of the group's rows in
+// with o1, o2 its sums of weighted values over the prefix and over the sequence's own tokens, l1, l2 those of
+// the weights, and m1, m2 the references that they go by.  The first is one problem per group, with all of the group's rows in
 // row tiles that read the prefix once for up to 128 of them, and its results go to the workspace in
 // fp32; the second is one per sequence and adds the first when it writes its own.  Both are the cache
 // attention's kernels with other lengths and tables.
@@ -41,7 +41,7 @@ cudaError_t kv_attention_shared_workspace_bytes(const KvView &kv, int rows, int 
     size_t own = 0, prefix = 0;
     cudaError_t e = part_bytes(kv, max_rows, heads_q, &own);
     if (e == cudaSuccess) e = part_bytes(kv, max_group_rows, heads_q, &prefix);
-    *bytes = sizeof(StatusWord) + std::max(own, prefix) + (size_t)rows * heads_q * (kv.dim + 1) * sizeof(float);
+    *bytes = sizeof(StatusWord) + std::max(own, prefix) + (size_t)rows * heads_q * (kv.dim + 2) * sizeof(float);
     return e;
 }
 
@@ -54,7 +54,7 @@ cudaError_t launch_kv_attention_shared(const KvAttentionArgs &k, const int32_t *
     if ((e = part_bytes(k.kv, k.max_rows, k.heads_q, &own)) != cudaSuccess) return e;
     if ((e = part_bytes(k.kv, max_group_rows, k.heads_q, &prefix)) != cudaSuccess) return e;
     s.a.half = reinterpret_cast<float *>((char *)ws + sizeof(StatusWord) + std::max(own, prefix));
-    s.a.half_lse = s.a.half + (size_t)k.rows * k.heads_q * k.kv.dim;
+    s.a.half_ml = reinterpret_cast<float2 *>(s.a.half + (size_t)k.rows * k.heads_q * k.kv.dim);
     s.a.cu_groups = cu_groups;
     s.a.prefix_len = prefix_len;
     s.a.groups = groups;

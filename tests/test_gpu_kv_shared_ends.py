@@ -1,8 +1,10 @@
 """GPU: attention with shared prefixes where a call is at an end of what it takes: groups that do not take
 the sequences, parts of a row's sum that are far apart."""
+import numpy as np
 import pytest
 import torch
 
+from tests.test_gpu_kv import e4m3_values
 from tests.test_gpu_kv_shared import Shared
 
 pytestmark = pytest.mark.gpu
@@ -42,3 +44,46 @@ def test_groups_past_the_last_sequence_are_reported():
     for groups, prefix in (([0, 2, 4], [128, 64]), ([0, 0, 2, 2, 4, 4], [7, 128, 99, 64, 64])):
         out, status = call(groups, prefix)
         assert status == moe.MOE_OK and torch.equal(out, good), groups
+
+
+def far_apart(c, octaves, low, prefix_scale, own_scale):
+    """All keys equal but for their sign, so that the scores of the prefixes (low = 0) or of the own tokens (1)
+    lie `octaves` below the others; values as they were, on pages of the given scales.  Returns the scale."""
+    c.q.fill_(1.0)
+    val = e4m3_values()
+    for g, p in enumerate(c.prefix):
+        w = p // c.P
+        lead = c.table[c.groups[g]].copy()
+        for b in range(c.groups[g], c.groups[g + 1]):
+            ids = np.concatenate([lead[:w], c.table[b, w:-(-c.lens[b] // c.P)]])
+            for part, ours in ((0, ids[:w]), (1, ids[w:])):
+                keys = c.codes_np[ours, 0]
+                c.codes_np[ours, 0] = np.where(keys & 0x7F == 0x7F, keys, 0xB8 if part == low else 0x38)  # -1, 1
+                c.scales_np[ours, 0] = 1.0
+                c.scales_np[ours, 1] = own_scale if part else prefix_scale
+            full = val[c.codes_np[ids]] * c.scales_np[ids].astype(np.float64)[..., None, None]
+            c.kv[b] = tuple(full.transpose(1, 0, 3, 2, 4).reshape(2, -1, c.H, c.D)[:, :c.lens[b]])
+    c.upload()
+    return octaves * np.log(2.0) / (2 * c.D)
+
+
+FAR = [
+    ([3], [256], [1, 1, 1], [30, 1, 200], 2, 4, 128, 64),             # the few-rows form
+    ([2, 1], [64, 32], [1, 2, 1], [0, 7, 5], 2, 3, 64, 16),
+    ([3], [384], [5, 2, 5], [40, 3, 300], 2, 7, 128, 64),             # the rows form, with copies and without
+    ([2], [256], [20, 17], [9, 150], 1, 8, 64, 32),
+    ([2], [6016], [1, 1], [3000, 5000], 1, 7, 128, 64),               # units that several workers join
+    ([2], [6016], [9, 9], [3000, 5000], 1, 4, 128, 64),
+]
+
+
+@pytest.mark.parametrize("octaves,big,small", [(1, 70, -70), (60, 20, -30), (125, 60, -60), (130, 60, -60), (144, 60, -80), (200, 100, -90),
+                                               (222, 110, -90)])
+@pytest.mark.parametrize("low", [0, 1])
+@pytest.mark.parametrize("shape", FAR, ids=[str(i) for i in range(len(FAR))])
+def test_a_part_far_below_may_have_the_larger_values(shape, low, octaves, big, small):
+    """A part whose sum is 2^-octaves of the other's counts where its values are 2^(big - small) times as large."""
+    c = Shared(*shape, seed=octaves)
+    scales = (2.0 ** big, 2.0 ** small) if low == 0 else (2.0 ** small, 2.0 ** big)
+    scale = far_apart(c, octaves, low, *scales)
+    c.check(scale=scale)
