@@ -1,10 +1,14 @@
 """GPU: attention with shared prefixes where a call is at an end of what it takes: groups that do not take
 the sequences, parts of a row's sum that are far apart."""
+import copy
+import math
+
 import numpy as np
 import pytest
 import torch
 
 from tests.test_gpu_kv import e4m3_values
+from tests.test_gpu_kv_ranges import GROUPS, reference
 from tests.test_gpu_kv_shared import Shared
 
 pytestmark = pytest.mark.gpu
@@ -87,3 +91,67 @@ def test_a_part_far_below_may_have_the_larger_values(shape, low, octaves, big, s
     scales = (2.0 ** big, 2.0 ** small) if low == 0 else (2.0 ** small, 2.0 ** big)
     scale = far_apart(c, octaves, low, *scales)
     c.check(scale=scale)
+
+
+def check_ranges(c, scale=None):
+    """Against 64 bits with the tolerance for scales that lie far apart; prefixes end with a tile."""
+    scale = c.D ** -0.5 if scale is None else scale
+    assert all(p % 128 == 0 for p in c.prefix)
+    out, lse = c.run(scale=scale)
+    ref = copy.copy(c)
+    ref.table = c.table.copy()
+    for g, p in enumerate(c.prefix):
+        lead = next(b for b in range(c.groups[g], c.groups[g + 1]) if c.n[b])
+        ref.table[c.groups[g]:c.groups[g + 1], :p // c.P] = c.table[lead, :p // c.P]
+    want, rl, tol, ltol = reference(ref, scale)
+    over = np.abs(out.double().cpu().numpy() - want) - tol
+    assert over.max() <= 0, f"output off by {over.max():.3e} beyond its tolerance"
+    assert (np.abs(lse.double().cpu().numpy() - rl) <= ltol).all()
+
+
+@pytest.mark.parametrize("group", GROUPS)
+@pytest.mark.parametrize("dim,page", [(128, 16), (64, 32)])
+@pytest.mark.parametrize("exponents", [(0, -16), (4, -20), (60, 0, -60), (-80, 2), (-126,), (90,)])
+def test_value_scales_far_apart(group, dim, page, exponents):
+    """Peaked weights over pages whose value scales differ, in the prefixes and behind them."""
+    c = Shared([2, 1], [256, 128], [5, 2, 3], [54, 7, 140], 2, group, dim, page, seed=group, qscale=9.0)
+    r = np.random.default_rng(group)
+    pages = np.unique(c.table[c.table >= 0])
+    c.scales_np[pages, 1] = 2.0 ** r.choice(exponents, (len(pages), c.H))
+    c.upload()
+    check_ranges(c)
+
+
+@pytest.mark.parametrize("group", GROUPS)
+@pytest.mark.parametrize("part", ["prefix", "own", "all"])
+def test_pages_of_zero_values(group, part):
+    """Values of nothing but zeros (their scale is 2^-126) in one part of a row's tokens, or in both."""
+    c = Shared([3], [256], [1, 4, 5], [60, 3, 140], 1, group, 128, 16, seed=group, qscale=4.0)
+    lead = c.table[0, :16].copy()
+    own = np.unique(c.table[:, 16:][c.table[:, 16:] >= 0])
+    zero = {"prefix": lead, "own": own, "all": np.concatenate([lead, own])}[part]
+    c.codes_np[zero, 1] = np.where(c.codes_np[zero, 1] & 0x7F == 0x7F, c.codes_np[zero, 1], 0)
+    c.scales_np[zero, 1] = 2.0 ** -126
+    c.upload()
+    check_ranges(c)
+
+
+@pytest.mark.parametrize("group", GROUPS)
+@pytest.mark.parametrize("scale", [math.inf, math.nan, -math.inf])
+def test_scales_that_are_no_numbers_reach_those_that_see_them(group, scale):
+    """A page of the prefix: all rows of its group, in that head.  A page of one sequence: its rows from there on."""
+    c = Shared([2, 1], [128, 64], [5, 2, 3], [30, 7, 9], 2, group, 128, 16, seed=5)
+    clean, lse = c.run()
+    keep = c.scales_np.copy()
+    c.scales_np[c.table[0, 2], 1, 0] = scale
+    c.upload()
+    out, lse2 = c.run()
+    assert torch.isnan(out[:7, :group]).all()
+    assert torch.equal(out[7:], clean[7:]) and torch.equal(out[:, group:], clean[:, group:]) and torch.equal(lse2[7:], lse[7:])
+    c.scales_np = keep
+    assert (128 + 30 + 2) % 16 == 0                          # the third row of sequence 0 begins a page
+    c.scales_np[c.table[0, 160 // 16], 1, 1] = scale
+    c.upload()
+    out, lse2 = c.run()
+    assert torch.isnan(out[2:5, group:]).all()
+    assert torch.equal(out[:2], clean[:2]) and torch.equal(out[5:], clean[5:]) and torch.equal(out[:, :group], clean[:, :group])

@@ -123,3 +123,20 @@ def test_over_the_logits_at_any_address(V, lead, dtype):
             _, probs = check(x.clone(), [T] * R, **s)
             in_place(x, [T] * R, probs, **s)
         assert (wide[:, :lead] == 100).all() and (wide[:, lead + V:] == 100).all()
+
+
+def test_more_rows_than_are_put_in_order():
+    """Above 4096 rows the clusters take them one after the other; above 100000, of a few tokens."""
+    R, V = 4500, 2100
+    x = rows_of(V, torch.bfloat16)[torch.arange(R, device="cuda") % 22]
+    k, p = [(0, 3, 1100, 0)[r % 4] for r in range(R)], [(0.9, 1.0, 0.5)[r % 3] for r in range(R)]
+    u = [r / R for r in range(R)]
+    args = dict(top_k=dev(k, torch.int32), top_p=dev(p))
+    got, probs = moe.moe_sample(x, dev([1.0] * R), dev(u), **args), moe.moe_sample_probs(x, dev([1.0] * R), **args)
+    for part in (range(0, 60), range(4090, 4130), range(4460, 4500)):
+        a, b = part[0], part[-1] + 1
+        few, q = check(x[a:b], [1.0] * len(part), k=k[a:b], p=p[a:b], u=u[a:b])
+        assert got[a:b].tolist() == few and torch.equal(probs[a:b], q)
+    x = torch.randn((120000, 3), device="cuda")
+    got = moe.moe_sample(x, dev([0.0] * 120000), dev([0.5] * 120000))
+    assert torch.equal(got.long(), x.argmax(-1))
