@@ -392,10 +392,14 @@ moe_status moe_kv_attention(const moe_kv *kv, int layer, const uint16_t *q, size
                             float *lse, void *ws, size_t ws_bytes, moe_stream_t stream);
 
 /* Attention of sequences that share prefixes (several continuations sampled from one prompt,
- * requests about one document): the same result as moe_kv_attention, with the shared tokens read
- * once for all rows of a group.  Group g has the sequences cu_groups[g] .. cu_groups[g+1]-1
+ * requests about one document): the same result as moe_kv_attention, with the shared tokens read once
+ * for up to 128 of a group's rows times query heads of a key/value head (16 rows of 7: once, 96 of 7:
+ * six times).  That is so where the tables have room for more than 32 tiles of 128 tokens per SM, key/value
+ * heads and row tiles counted; smaller batches read the tokens for each sequence, in one launch.
+ *
+ * Group g has the sequences cu_groups[g] .. cu_groups[g+1]-1
  * (cu_groups [groups+1], ascending from 0 to seqs: every sequence is in one, alone if need be),
- * whose first prefix_len[g] tokens are the same (0: nothing is shared).  What is taken as shared
+ * whose first prefix_len[g] tokens are the same (0 or less: nothing is shared).  What is taken as shared
  * are the prefix's whole pages, as named by the first columns of the table row of the group's first
  * sequence with rows (the other sequences' entries there are not read: one that has ended may have
  * given its pages back); tokens of a page that the prefix does not fill are read for each sequence,
@@ -405,8 +409,11 @@ moe_status moe_kv_attention(const moe_kv *kv, int layer, const uint16_t *q, size
  * errors of moe_kv_attention; rows are then not valid.  A group has at most max_group_rows rows in
  * all (max_group_rows * heads_q / heads <= 2^24), a sequence at most max_rows.  q, out, lse, scale and
  * the rest as for moe_kv_attention; the two parts of a row's result are held and added in fp32.
+ *
  * ws: moe_kv_attention_shared_workspace_size() bytes for `rows` rows and the current device (what
- * serves more rows serves fewer). */
+ * serves more rows serves fewer): those of moe_kv_attention for the larger of max_rows and
+ * max_group_rows, and 4 * rows * heads_q * (head_dim + 2) for the rows' first parts (239 MB for 8192
+ * rows of 56 heads of 128). */
 moe_status moe_kv_attention_shared_workspace_size(const moe_kv *kv, int rows, int max_rows, int max_group_rows,
                                                   int heads_q, size_t *bytes);
 moe_status moe_kv_attention_shared(const moe_kv *kv, int layer, const uint16_t *q, size_t ldq, int rows, int heads_q,
@@ -471,7 +478,8 @@ moe_status moe_kv_release(const int32_t *keep, const int32_t *kv_len, int seqs, 
  * by S (both rounded to fp32, then to `dtype`), 0 elsewhere: what moe_verify_sampled takes as p or q.
  * probs may be x itself (with ldp = ld); rows of the two overlap in no other way.  temperature <= 0 or NaN: the first token
  * of the order (probability 1), whatever the cuts.  A row of nothing but NaN and -infinity: next = -1, probabilities 0.
- * ws: moe_sample_workspace_size() bytes. */
+ * ws: moe_sample_workspace_size() bytes: a status word, as every call has one.  Sampling finds no errors on the
+ * device and leaves it as it is. */
 moe_status moe_sample_workspace_size(int rows, int vocab, size_t *bytes);
 moe_status moe_sample(const void *x, size_t ld, int dtype, int rows, int vocab, const float *temperature,
                       const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *next,

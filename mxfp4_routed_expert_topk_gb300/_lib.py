@@ -679,7 +679,7 @@ def moe_kv_attention_shared(cache: KvCache, layer: int, q: torch.Tensor, cu_rows
                             max_group_rows: int, scale: float | None = None, out: torch.Tensor | None = None,
                             lse: torch.Tensor | None = None, ws: torch.Tensor | None = None, stream=None):
     """moe_kv_attention of sequences in groups cu_groups [groups + 1] that share their first prefix_len [groups]
-    tokens, which are read once for each group; returns out (bf16, like q)."""
+    tokens, which are read once for up to 128 rows and query heads of a group; returns out (bf16, like q)."""
     rows, heads_q, _ = q.shape
     dim = cache.head_dim
     ldq = _need_heads(q, heads_q, dim, "q")

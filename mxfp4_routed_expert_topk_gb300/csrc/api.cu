@@ -496,8 +496,7 @@ moe_status sample_check(const SampleArgs &a, int dtype, const void *ws, size_t w
 moe_status moe_sample(const void *x, size_t ld, int dtype, int rows, int vocab, const float *temperature,
                       const int32_t *top_k, const float *top_p, const float *min_p, const float *u, int32_t *next,
                       void *ws, size_t ws_bytes, moe_stream_t stream) {
-    SampleArgs a = {x,     ld,    dtype == MOE_PROB_BF16, rows, vocab, temperature, top_k, top_p, min_p, u, next,
-                    nullptr, 0, (StatusWord *)ws};
+    SampleArgs a = {x, ld, dtype == MOE_PROB_BF16, rows, vocab, temperature, top_k, top_p, min_p, u, next, nullptr, 0};
     const moe_status s = sample_check(a, dtype, ws, ws_bytes);
     if (s != MOE_OK) return s;
     if (rows > 0 && (u == nullptr || next == nullptr)) return MOE_ERR_INVALID_ARG;
@@ -507,8 +506,7 @@ moe_status moe_sample(const void *x, size_t ld, int dtype, int rows, int vocab, 
 moe_status moe_sample_probs(const void *x, size_t ld, int dtype, int rows, int vocab, const float *temperature,
                             const int32_t *top_k, const float *top_p, const float *min_p, void *probs, size_t ldp,
                             void *ws, size_t ws_bytes, moe_stream_t stream) {
-    SampleArgs a = {x,     ld,    dtype == MOE_PROB_BF16, rows, vocab, temperature, top_k, top_p, min_p, nullptr, nullptr,
-                    probs, ldp, (StatusWord *)ws};
+    SampleArgs a = {x, ld, dtype == MOE_PROB_BF16, rows, vocab, temperature, top_k, top_p, min_p, nullptr, nullptr, probs, ldp};
     const moe_status s = sample_check(a, dtype, ws, ws_bytes);
     if (s != MOE_OK) return s;
     if (ldp < (size_t)vocab || (rows > 0 && (probs == nullptr || !aligned(probs, a.bf16 ? 2 : 4)))) return MOE_ERR_INVALID_ARG;

@@ -6,12 +6,12 @@
 //   o = (2^(m1 - m) o1 + 2^(m2 - m) o2) / (2^(m1 - m) l1 + 2^(m2 - m) l2),  m = max(m1, m2)
 //
 // with o1, o2 its sums of weighted values over the prefix and over the sequence's own tokens, l1, l2 those of
-// the weights, and m1, m2 the references that they go by.  The first is one problem per group, with all of the group's rows in
-// row tiles that read the prefix once for up to 128 of them, and its results go to the workspace in
-// fp32; the second is one per sequence and adds the first when it writes its own.  Both are the cache
-// attention's kernels with other lengths and tables.
+// the weights, and m1, m2 the references that they go by.  The first is one problem per group, with all of
+// the group's rows in row tiles that read the prefix once for up to 128 of them, and its results go to the
+// workspace in fp32; the second is one per sequence and adds the first when it writes its own.  Both are the
+// cache attention's kernels with other lengths and tables.
 //
-// Small batches run once, each sequence over its prefix and its own tokens: two runs take 50 us or more,
+// Small batches run once, each sequence over its prefix and its own tokens: two runs take 38 us or more,
 // however little there is to do.
 #include <algorithm>
 
@@ -21,10 +21,11 @@
 namespace moe {
 namespace {
 
-// Tiles per SM (as many as the tables have room for) up to which a batch is small.  Once / twice, one row of
-// 56 heads of 128: 16 sequences of 2000 + 200 tokens (14 tiles per SM) 33 / 49 us, 64 of 1000 + 100 (30)
-// 53 / 58, 2 of 30000 (25) 47 / 56, 8 of 16000 (53) 60 / 53, 64 of 4000 + 300 (115) 113 / 78; five rows, 32 of
-// 2000 + 300 (30) 73 / 80.
+// Tiles per SM (as many as the tables have room for: the lengths are known on the device alone, so short
+// sequences with wide tables run twice) up to which a batch is small.  Once / twice, one row of
+// 56 heads of 128, tables as wide as the sequences are long: 16 sequences of 2000 + 200 tokens (14 tiles per SM)
+// 33 / 49 us, 64 of 1000 + 100 (30) 51 / 57, 2 of 30000 (25) 47 / 58, 8 of 16000 (53) 61 / 53, 64 of 4000 +
+// 300 (115) 112 / 78; five rows, 32 of 2000 + 300 (30) 72 / 79.
 constexpr int kSmall = 32;
 
 cudaError_t run(const AttnSetup &s, cudaStream_t st) {

@@ -130,7 +130,6 @@ struct SampleArgs {
     int32_t *next;
     void *probs;  // not null: the distribution in place of the draw
     size_t ldp;
-    StatusWord *st;
     bool in_order;  // whether the clusters take the rows in their order (set by the launch)
 };
 cudaError_t launch_sample(const SampleArgs &a, cudaStream_t st);

@@ -19,10 +19,10 @@
 //   - where the list does not hold them (thousands of equal logits) or a larger top-k is asked for, the cut
 //     is found digit by digit in exact histograms.
 //
-// Measured on the device: one row of 32001 values 5 (its largest), 10 (top-k of 1), 12 (50), 20 (1000), 24 to 29 us
-// (top-p alone); 256 rows of 131072, settings mixed, 128 us, where rows of top-p alone (a twelfth) take 110 each
-// and those with a top-k 38 to 54, many under way together; distributions of 96 rows of 131071, top-p alone, 109 us
-// (29 and 27 % of the ALU and FMA pipes, 39 % of the issue slots; waits for loads are the commonest stall).  Not better
+// Measured on the device: one row of 32001 values 5 (its largest), 10 (top-k of 1), 11 (50), 19 (1000), 24 to 29 us
+// (top-p alone); 256 rows of 131072, settings mixed, 127 us, where rows of top-p alone (a twelfth) take 110 each
+// and those with a top-k 38 to 54, many under way together; distributions of 96 rows of 131071, top-p alone, 108 us
+// (31 and 29 % of the ALU and FMA pipes, 39 % of the issue slots; waits for loads are the commonest stall).  Not better
 // (each against the kernel as it then was): copying a row's vectors ahead into shared memory, 96 rows 123 us
 // against 110; four vectors' loads in flight per thread 113 against 110, with their arithmetic unrolled 187
 // against 134; listing the largest 1024 first for top-p alone 150 against 130; functions called in place of
@@ -1111,8 +1111,8 @@ struct Sampler {
 };
 
 // The row that cluster `unit` takes where not all are under way at once: first those whose share of the
-// weights is asked for without a top-k, which take three times as long.  (256 rows of 131072, an eighth of
-// them such: 115 us, in their order 127.)
+// weights is asked for without a top-k, which take two to three times as long.  (256 rows of 131072, a twelfth
+// of them such: 127 us, in their order 148.)
 __device__ __forceinline__ int row_of(const SampleArgs &a, Smem &s, int unit) {
     const int tid = (int)threadIdx.x, lane = tid & 31, warp = tid >> 5;
     int slow = 0, mine = -1;  // slow rows so far
@@ -1156,7 +1156,7 @@ __global__ void __launch_bounds__(kThreads, 4) sample_kernel(const SampleArgs a)
 PerDevice g_sms(0);
 
 // CTAs per row: as many as fit the device at once (4 CTAs of an SM), or more, so that the rows under way
-// stay in L2 (256 rows of 131072: 125 us with 4, 170 with 2); 8 at most (the portable size).
+// stay in L2 (256 rows of 131072: 127 us with 4, 199 with 2); 8 at most (the portable size).
 int cluster_size(int rows, size_t row_bytes, int sms) {
     const int64_t slots = 4 * (int64_t)sms;
     int c = (int)std::min<int64_t>(kMaxCluster, std::max<int64_t>(1, slots / rows));
