@@ -59,3 +59,58 @@ idx, _ = moe.moe_route_topk(x, w, 4)
 want = (x.double() @ w.double().T).topk(4, sorted=True).indices
 assert torch.equal(idx.long(), want), (idx, want)
 """)
+
+
+CAPTURED = {
+    "reserve": """
+n = 3000
+table, refs, one = torch.full((n, 2), -1, **i32), torch.zeros(n + 5, **i32), torch.ones(n, **i32)
+zero, ws = 0 * one, moe.workspace(256)
+cu, lens = torch.zeros(n + 1, **i32), torch.zeros(n, **i32)
+maps = dict(row_seq=torch.zeros(n, **i32), row_pos=torch.zeros(n, **i32), row_slot=torch.zeros(n, dtype=torch.int64, device="cuda"))
+call = lambda: moe.moe_kv_reserve(one, zero, table, refs, 16, n, cu_rows=cu, kv_len=lens, ws=ws, **maps)
+done = lambda: torch.equal(cu, torch.arange(n + 1, **i32)) and int(refs.sum()) == n
+""",
+    "sample": """
+x = torch.randn((3, 70000), device="cuda")
+x[:, 777] = 60.0
+t, u, out, ws = torch.ones(3, device="cuda"), torch.full((3,), 0.5, device="cuda"), torch.zeros(3, **i32), moe.workspace(256)
+call = lambda: moe.moe_sample(x, t, u, next_token=out, ws=ws)
+done = lambda: out.tolist() == [777] * 3
+""",
+    "route": """
+x, w = torch.ones((6, 4096), device="cuda").bfloat16(), torch.zeros((64, 4096), device="cuda").bfloat16()
+w[[5, 9]] = torch.tensor([[2.0], [1.0]], device="cuda").bfloat16()
+idx, wt = torch.zeros((6, 2), **i32), torch.zeros((6, 2), device="cuda")
+ws = moe.workspace(moe.moe_workspace_size(moe.MOE_OP_ROUTE, 64, 4096, 32, 6, 2))
+call = lambda: moe.moe_route_topk(x, w, 2, idx=idx, w=wt, ws=ws)
+done = lambda: idx.tolist() == [[5, 9]] * 6
+""",
+    "attention": """
+c = moe.KvCache(4, 1, 1, 128, 16)
+c.buffer.zero_()
+c.codes(0).view(torch.uint8).fill_(0x38)
+c.scales(0).fill_(1.0)
+at, lens, table = torch.tensor([0, 1], **i32), torch.tensor([40], **i32), torch.tensor([[2, 0, 3]], **i32)
+q, out = torch.ones((1, 2, 128), device="cuda").bfloat16(), torch.zeros((1, 2, 128), device="cuda").bfloat16()
+pre = torch.tensor([32], **i32)
+ws = moe.workspace(moe.moe_kv_attention_shared_workspace_size(c, 1, 1, 1, 2))
+call = lambda: moe.moe_kv_attention_shared(c, 0, q, at, lens, table, at, pre, 1, 1, out=out, ws=ws)
+done = lambda: bool((out == 1).all())
+""",
+}
+
+
+@pytest.mark.parametrize("what", CAPTURED)
+def test_first_call_inside_a_capture(what):
+    """What a kernel needs before its first launch is set up while a stream is captured, too."""
+    in_a_process(CAPTURED[what] + """
+torch.cuda.synchronize()
+g = torch.cuda.CUDAGraph()
+with torch.cuda.graph(g):
+    call()
+assert not done()
+g.replay()
+torch.cuda.synchronize()
+assert done() and moe.moe_check_status(ws) == moe.MOE_OK
+""")
